@@ -273,6 +273,48 @@ int disco_fused_bwd(const disco_psi* psi, const void* x, int x_dtype, const void
                     const void* gy, int gy_dtype, void* gx, int gx_dtype, float* gw, float* gbias,
                     int32_t B, int32_t Ci, int32_t Co, int32_t groups, void* stream);
 
+/* ---- Layer norm ----------------------------------------------------------
+ * Normalisation over the channels, the step that stands before the
+ * convolution in a pre-norm residual block.  Tensors are dense and seen as
+ * [outer, C, inner]: a field [B, C, nlat, nlon] is outer = B, inner =
+ * nlat*nlon; channel-last rows [n, C] are outer = n, inner = 1.  Pointers
+ * need the alignment of their element only.  Statistics are float32, the
+ * mean first and then the centred squares.  Outputs may not overlap inputs. */
+
+/* Forward:
+ *   s = x, or x + residual rounded to x_dtype and stored in `sum`
+ *   mean = 1/C sum_c s,  rstd = 1/sqrt(1/C sum_c (s - mean)^2 + eps)
+ *   y = (s - mean) * rstd * gamma[c] + beta[c]
+ * x, residual, sum: [outer, C, inner] of x_dtype (residual and sum both given
+ * or both NULL); gamma, beta: [C] float32, either NULL for ones / zeros; y:
+ * [outer, C, inner] of y_dtype; mean, rstd: [outer, inner] float32, both given
+ * (the gradient needs them) or both NULL.  outer == 0 or inner == 0 does
+ * nothing.  Points are independent: a NaN or an infinity stays in its own. */
+int disco_layer_norm_fwd(const void* x, int x_dtype, const void* residual, const float* gamma,
+                         const float* beta, void* y, int y_dtype, void* sum, float* mean,
+                         float* rstd, int64_t outer, int32_t C, int64_t inner, float eps,
+                         void* stream);
+
+/* Bytes of device workspace that disco_layer_norm_bwd needs for ggamma or
+ * gbeta (partial sums per workgroup), or a negative status. */
+int64_t disco_layer_norm_bwd_workspace(int64_t outer, int32_t C, int64_t inner);
+
+/* Gradients, with h = (x - mean) * rstd and t = gy * gamma[c]:
+ *   gx = rstd * (t - 1/C sum_c t - h * 1/C sum_c t*h) + gsum
+ *   ggamma[c] = sum_{outer, inner} gy * h,   gbeta[c] = sum_{outer, inner} gy
+ * x: what was normalised (the forward's `sum` where it had a residual);
+ * gy, gsum: [outer, C, inner] of gy_dtype; gsum is the gradient that reaches
+ * that sum past the norm, NULL for none; gx: [outer, C, inner] of gx_dtype or
+ * NULL; ggamma, gbeta: [C] float32, either NULL (not all three).  The
+ * parameter sums run in a fixed order in float32, so results are
+ * reproducible; they need `workspace` (may be NULL when neither is asked
+ * for).  An empty tensor gives zero parameter gradients. */
+int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtype,
+                         const float* mean, const float* rstd, const float* gamma,
+                         const void* gsum, void* gx, int gx_dtype, float* ggamma, float* gbeta,
+                         void* workspace, int64_t workspace_bytes, int64_t outer, int32_t C,
+                         int64_t inner, void* stream);
+
 /* Per-kernel timing, for benchmarks and profiling (not part of the pages'
  * method).  With enable != 0, every kernel the library launches from then on
  * is bracketed by a pair of HIP events recorded on its launch stream; with 0,

@@ -16,6 +16,9 @@ Entry points (same names as the C ABI, without the ``disco_`` prefix):
     einsum_grad_xk(gy, w, ...)   -> gxk         adjoint of einsum in xk
     einsum_grad_w(xk, gy, ...)   -> gw          adjoint of einsum in w
     fused_bwd(psi, x, w, gy, ...) -> (gx, gw, gbias)   X_K recomputed, never whole
+  around the layer in a training step:
+    layer_norm_fwd(x, gamma, beta, residual=...) -> (y, sum, mean, rstd)
+    layer_norm_bwd(x, gy, mean, rstd, gamma, gsum=...) -> (gx, ggamma, gbeta)
 """
 from __future__ import annotations
 
@@ -90,6 +93,11 @@ def _load():
                                                I32, I32, I32, I32, P]),
         "disco_fused_bwd": (ctypes.c_int, [P, P, ctypes.c_int, P, ctypes.c_int, P, ctypes.c_int, P,
                                            ctypes.c_int, P, P, I32, I32, I32, I32, P]),
+        "disco_layer_norm_fwd": (ctypes.c_int, [P, ctypes.c_int, P, P, P, P, ctypes.c_int, P, P, P,
+                                                I64, I32, I64, ctypes.c_float, P]),
+        "disco_layer_norm_bwd_workspace": (I64, [I64, I32, I64]),
+        "disco_layer_norm_bwd": (ctypes.c_int, [P, ctypes.c_int, P, ctypes.c_int, P, P, P, P, P,
+                                                ctypes.c_int, P, P, P, I64, I64, I32, I64, P]),
         "disco_kernel_timing": (ctypes.c_int, [ctypes.c_int]),
         "disco_kernel_timing_read": (ctypes.c_int, [ctypes.c_char_p, I32, ctypes.POINTER(D),
                                                     ctypes.POINTER(I64), I32]),
@@ -108,7 +116,8 @@ EXPORTED = ("disco_psi_build", "disco_psi_query", "disco_psi_export", "disco_psi
             "disco_psi_free", "disco_contract", "disco_einsum", "disco_fused_fwd",
             "disco_fused_fwd_noalloc",
             "disco_fused_is_spectral", "disco_contract_transpose", "disco_einsum_grad_xk",
-            "disco_einsum_grad_w", "disco_fused_bwd", "disco_kernel_timing", "disco_kernel_timing_read",
+            "disco_einsum_grad_w", "disco_fused_bwd", "disco_layer_norm_fwd",
+            "disco_layer_norm_bwd_workspace", "disco_layer_norm_bwd", "disco_kernel_timing", "disco_kernel_timing_read",
             "disco_last_error", "disco_version")
 
 
@@ -475,3 +484,115 @@ def fused_bwd(psi: Psi, x, w, gy, groups: int = 1, need_gx: bool = True, need_gw
                                 gb.data_ptr() if gb is not None else None,
                                 B, Ci, Co, groups, _stream(stream)), "fused_bwd")
     return gx, gw, gb
+
+
+# ----------------------------------------------------------------------------
+# layer norm
+# ----------------------------------------------------------------------------
+def _norm_view(x, axis):
+    """(outer, C, inner, shape without the channel axis) of x's channel axis."""
+    if x.dim() < 2:
+        raise ValueError("x must have at least two dimensions")
+    if not -x.dim() <= axis < x.dim():
+        raise ValueError(f"axis {axis} is out of range for {x.dim()} dimensions")
+    axis %= x.dim()
+    shape = x.shape
+    outer = inner = 1
+    for n in shape[:axis]:
+        outer *= n
+    for n in shape[axis + 1:]:
+        inner *= n
+    return outer, shape[axis], inner, shape[:axis] + shape[axis + 1:]
+
+
+def _f32_ptr(t, name, shape):
+    """Pointer of an optional float32 tensor."""
+    if t is None:
+        return None
+    _need(t, name, shape)
+    if t.dtype != _torch().float32:
+        raise ValueError(f"{name} must be float32")
+    return t.data_ptr()
+
+
+def _workspace(nbytes, device, stream):
+    """Scratch for one call: the allocator keeps it until the call's stream is
+    done with it."""
+    torch = _torch()
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None and nbytes:
+        ws.record_stream(stream)
+    return ws
+
+
+def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, axis: int = 1,
+                   y=None, out_dtype=None, need_stats: bool = True, stream=None):
+    """Layer norm over `axis` (1: the channels of a field [B, C, nlat, nlon];
+    -1: channel-last rows): y = (s - mean) * rstd * gamma + beta with s = x, or
+    s = x + residual rounded to x's dtype.
+
+    Returns (y, s, mean, rstd): s is None without a residual, the statistics
+    (float32, x's shape without the axis) None with need_stats=False.  y has
+    out_dtype, or x's dtype."""
+    torch = _torch()
+    outer, C, inner, points = _norm_view(x, axis)
+    _need(x, "x", x.shape)
+    gptr, bptr = _f32_ptr(gamma, "gamma", (C,)), _f32_ptr(beta, "beta", (C,))
+    s = mean = rstd = None
+    if residual is not None:
+        _need(residual, "residual", x.shape)
+        if residual.dtype != x.dtype:
+            raise ValueError(f"residual must have x's dtype ({x.dtype})")
+        s = torch.empty_like(x)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    _need(y, "y", x.shape)
+    if need_stats:
+        mean = torch.empty(points, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(points, dtype=torch.float32, device=x.device)
+    _check(_lib.disco_layer_norm_fwd(
+        x.data_ptr(), _dtype_code(x), residual.data_ptr() if s is not None else None, gptr, bptr,
+        y.data_ptr(), _dtype_code(y), s.data_ptr() if s is not None else None,
+        mean.data_ptr() if need_stats else None, rstd.data_ptr() if need_stats else None,
+        outer, C, inner, eps, _stream(stream)), "layer_norm_fwd")
+    return y, s, mean, rstd
+
+
+def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need_gx: bool = True,
+                   need_gparams: bool = True, gx_dtype=None, stream=None):
+    """Gradients (gx, ggamma, gbeta) of sum(gy * layer_norm_fwd(x)); entries not
+    asked for are None.  x is what was normalised (the forward's s where it had
+    a residual).  gsum (gy's dtype): the gradient that reaches x past the norm,
+    added to gx.  gx has gx_dtype, or float32."""
+    torch = _torch()
+    outer, C, inner, points = _norm_view(x, axis)
+    _need(x, "x", x.shape)
+    _need(gy, "gy", x.shape)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are needed")
+    mptr, rptr = _f32_ptr(mean, "mean", points), _f32_ptr(rstd, "rstd", points)
+    gptr = _f32_ptr(gamma, "gamma", (C,))
+    if gsum is not None:
+        _need(gsum, "gsum", x.shape)
+        if gsum.dtype != gy.dtype:
+            raise ValueError(f"gsum must have gy's dtype ({gy.dtype})")
+    gx = gg = gb = None
+    if need_gx:
+        gx = torch.empty(x.shape, dtype=torch.float32 if gx_dtype is None else gx_dtype,
+                         device=x.device)
+    ws, nws = None, 0
+    if need_gparams:
+        gg = torch.empty((C,), dtype=torch.float32, device=x.device)
+        gb = torch.empty((C,), dtype=torch.float32, device=x.device)
+        nws = _lib.disco_layer_norm_bwd_workspace(outer, C, inner)
+        if nws < 0:
+            _check(nws, "layer_norm_bwd")
+        ws = _workspace(nws, x.device, stream)
+    _check(_lib.disco_layer_norm_bwd(
+        x.data_ptr(), _dtype_code(x), gy.data_ptr(), _dtype_code(gy), mptr, rptr, gptr,
+        gsum.data_ptr() if gsum is not None else None,
+        gx.data_ptr() if need_gx else None, _dtype_code(gx) if need_gx else F32,
+        gg.data_ptr() if need_gparams else None, gb.data_ptr() if need_gparams else None,
+        ws.data_ptr() if need_gparams else None, nws, outer, C, inner, _stream(stream)),
+        "layer_norm_bwd")
+    return gx, gg, gb

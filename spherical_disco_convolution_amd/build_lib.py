@@ -26,6 +26,8 @@ SOURCES = [
     "kernels_fused_mfma.hip",
     "kernels_spectral.hip",
     "kernels_backward.hip",
+    "training_api.cpp",
+    "kernels_layer_norm.hip",
     "spectral_host.cpp",
     "kernel_timing.cpp",
 ]

@@ -31,8 +31,6 @@ int set_error(int code, const char* fmt, ...) {
 
 void clear_error() { g_last_error.clear(); }
 
-namespace {
-
 int dtype_size(int dt) { return dt == DISCO_F32 ? 4 : (dt == DISCO_BF16 ? 2 : 0); }
 
 bool valid_dtype(int dt) { return dt == DISCO_F32 || dt == DISCO_BF16; }
@@ -71,6 +69,8 @@ int current_device(int* dev) {
     }
     return DISCO_OK;
 }
+
+namespace {
 
 int check_psi_on_device(const disco_psi* psi, int dev) {
     if (psi == nullptr) return set_error(DISCO_EINVAL, "psi handle is NULL");

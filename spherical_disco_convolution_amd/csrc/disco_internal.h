@@ -21,6 +21,16 @@ int set_error(int code, const char* fmt, ...);   // records message, returns cod
 void clear_error();
 
 // ---------------------------------------------------------------------------
+// Argument checks shared by the C-ABI entry points (disco_api.cpp)
+// ---------------------------------------------------------------------------
+int dtype_size(int dt);      // bytes of an element, 0 for an unknown code
+bool valid_dtype(int dt);
+// EINVAL unless ptr is device (or managed) memory of `device`
+int check_device_ptr(const void* ptr, const char* name, int device);
+bool overlap(const void* a, size_t na, const void* b, size_t nb);
+int current_device(int* dev);
+
+// ---------------------------------------------------------------------------
 // Host form of Psi (float64)
 // ---------------------------------------------------------------------------
 // One support window: the input row `lat` contributes longitudes
@@ -185,6 +195,17 @@ int launch_einsum_grad_w(const void* xk, int xk_dtype, const void* gy, int gy_dt
 int launch_fused_bwd(const disco_psi* psi, const void* x, int x_dtype, const void* w, int w_dtype,
                      const void* gy, int gy_dtype, void* gx, int gx_dtype, float* gw, float* gbias,
                      int B, int Ci, int Co, int groups, void* stream);
+
+// Layer norm (kernels_layer_norm.hip): tensors seen as [outer, C, inner]
+size_t layer_norm_bwd_workspace(int64_t outer, int C, int64_t inner);
+int launch_layer_norm_fwd(const void* x, int x_dtype, const void* residual, const float* gamma,
+                          const float* beta, void* y, int y_dtype, void* sum, float* mean,
+                          float* rstd, int64_t outer, int C, int64_t inner, float eps,
+                          void* stream);
+int launch_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtype,
+                          const float* mean, const float* rstd, const float* gamma,
+                          const void* gsum, void* gx, int gx_dtype, float* ggamma, float* gbeta,
+                          float* partial, int64_t outer, int C, int64_t inner, void* stream);
 
 // Scope around one kernel launch: while disco_kernel_timing(1) is in effect,
 // records a HIP event on the launch stream at construction and at
