@@ -315,6 +315,48 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
                          void* workspace, int64_t workspace_bytes, int64_t outer, int32_t C,
                          int64_t inner, void* stream);
 
+/* ---- Orthogonalised weight updates --------------------------------------
+ * The optimiser step for the layer's weights [Co, Ci/groups, K], seen as
+ * `batch` = groups matrices of rows = Co/groups by cols = (Ci/groups)*K, one
+ * after another.  A matrix M is replaced by the nearby matrix whose singular
+ * values are all near one:
+ *   X = M / (|M|_F + eps)
+ *   steps times: A = X X^T, X <- a X + (b A + c A^2) X      (coeffs = a, b, c)
+ * (X^T in X's place where rows > cols: the same map).  Accuracy goes by the
+ * result's type: a float32 result has float32 accuracy (operands as pairs of
+ * float16, three matrix-core products for one); a bfloat16 result is within a
+ * bfloat16 rounding of it (single float16 products in all but the last two
+ * steps).  steps lies in 1..64.  coeffs: three floats in HOST memory, or NULL
+ * for 3.4445, -4.7750, 2.0315; EUNSUPPORTED where they would carry the
+ * singular values out of the operands' range (above about 3.5).  A NaN or an
+ * infinity anywhere in a matrix makes its whole result NaN; a zero matrix
+ * stays zero (eps > 0).  Results do not depend on the other matrices of the
+ * batch and are reproducible. */
+
+/* Bytes of device workspace that the two calls below need, or a negative
+ * status (EUNSUPPORTED for more than 65535 matrices). */
+int64_t disco_orthogonalize_workspace(int32_t batch, int32_t rows, int32_t cols);
+
+/* o = the orthogonalised m; m [batch, rows, cols] of m_dtype, o of o_dtype. */
+int disco_orthogonalize(const void* m, int m_dtype, void* o, int o_dtype, int32_t batch,
+                        int32_t rows, int32_t cols, int32_t steps, const float* coeffs, float eps,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* One optimiser step (momentum, orthogonalisation and the weight update of the
+ * Muon optimiser):
+ *   momentum_out = beta * momentum + grad
+ *   u     = grad + beta * momentum_out   (nesterov != 0), or momentum_out
+ *   w_out = w * (1 - lr * weight_decay) - lr * scale * orthogonalised(u)
+ * grad of grad_dtype, momentum float32, w and w_out of w_dtype (float32, or
+ * bfloat16 weights with no float32 master); w16: bfloat16 copy of a float32
+ * w_out for a bfloat16 layer, or NULL.  momentum_out may be momentum and
+ * w_out may be w; otherwise no output overlaps another tensor. */
+int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, float* momentum_out,
+                    const void* w, int w_dtype, void* w_out, void* w16, float lr, float beta,
+                    int nesterov, float weight_decay, float scale, int32_t batch, int32_t rows,
+                    int32_t cols, int32_t steps, const float* coeffs, float eps, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
 /* Per-kernel timing, for benchmarks and profiling (not part of the pages'
  * method).  With enable != 0, every kernel the library launches from then on
  * is bracketed by a pair of HIP events recorded on its launch stream; with 0,

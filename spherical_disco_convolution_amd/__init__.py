@@ -19,6 +19,8 @@ Entry points (same names as the C ABI, without the ``disco_`` prefix):
   around the layer in a training step:
     layer_norm_fwd(x, gamma, beta, residual=...) -> (y, sum, mean, rstd)
     layer_norm_bwd(x, gy, mean, rstd, gamma, gsum=...) -> (gx, ggamma, gbeta)
+    orthogonalize(m, ...) -> o                  Newton-Schulz products
+    muon_step(w, grad, momentum, lr, ...) -> (w, momentum, w16)   one optimiser step
 """
 from __future__ import annotations
 
@@ -98,6 +100,13 @@ def _load():
         "disco_layer_norm_bwd_workspace": (I64, [I64, I32, I64]),
         "disco_layer_norm_bwd": (ctypes.c_int, [P, ctypes.c_int, P, ctypes.c_int, P, P, P, P, P,
                                                 ctypes.c_int, P, P, P, I64, I64, I32, I64, P]),
+        "disco_orthogonalize_workspace": (I64, [I32, I32, I32]),
+        "disco_orthogonalize": (ctypes.c_int, [P, ctypes.c_int, P, ctypes.c_int, I32, I32, I32, I32, P,
+                                               ctypes.c_float, P, I64, P]),
+        "disco_muon_step": (ctypes.c_int, [P, ctypes.c_int, P, P, P, ctypes.c_int, P, P, ctypes.c_float,
+                                           ctypes.c_float, ctypes.c_int, ctypes.c_float,
+                                           ctypes.c_float, I32, I32, I32, I32, P, ctypes.c_float, P,
+                                           I64, P]),
         "disco_kernel_timing": (ctypes.c_int, [ctypes.c_int]),
         "disco_kernel_timing_read": (ctypes.c_int, [ctypes.c_char_p, I32, ctypes.POINTER(D),
                                                     ctypes.POINTER(I64), I32]),
@@ -117,7 +126,8 @@ EXPORTED = ("disco_psi_build", "disco_psi_query", "disco_psi_export", "disco_psi
             "disco_fused_fwd_noalloc",
             "disco_fused_is_spectral", "disco_contract_transpose", "disco_einsum_grad_xk",
             "disco_einsum_grad_w", "disco_fused_bwd", "disco_layer_norm_fwd",
-            "disco_layer_norm_bwd_workspace", "disco_layer_norm_bwd", "disco_kernel_timing", "disco_kernel_timing_read",
+            "disco_layer_norm_bwd_workspace", "disco_layer_norm_bwd", "disco_orthogonalize_workspace",
+            "disco_orthogonalize", "disco_muon_step", "disco_kernel_timing", "disco_kernel_timing_read",
             "disco_last_error", "disco_version")
 
 
@@ -596,3 +606,95 @@ def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need
         ws.data_ptr() if need_gparams else None, nws, outer, C, inner, _stream(stream)),
         "layer_norm_bwd")
     return gx, gg, gb
+
+
+# ----------------------------------------------------------------------------
+# orthogonalised weight updates
+# ----------------------------------------------------------------------------
+def _coeffs(coeffs):
+    if coeffs is None:
+        return None
+    coeffs = tuple(float(c) for c in coeffs)
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be three numbers (a, b, c)")
+    return (ctypes.c_float * 3)(*coeffs)
+
+
+def _ortho_workspace(batch, rows, cols, device, stream, what):
+    n = _lib.disco_orthogonalize_workspace(batch, rows, cols)
+    if n < 0:
+        _check(n, what)
+    return _workspace(n, device, stream), n
+
+
+def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps: float = 1e-7,
+                  stream=None):
+    """Newton-Schulz orthogonalisation of a matrix [rows, cols] or of each
+    matrix of a batch [batch, rows, cols]: singular values near one, singular
+    vectors kept.  The result has out_dtype, or m's dtype, and that type's
+    accuracy.  coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
+    torch = _torch()
+    if m.dim() not in (2, 3):
+        raise ValueError("m must be [rows, cols] or [batch, rows, cols]")
+    _need(m, "m", m.shape)
+    batch = m.shape[0] if m.dim() == 3 else 1
+    rows, cols = m.shape[-2:]
+    if out is None:
+        out = torch.empty(m.shape, dtype=m.dtype if out_dtype is None else out_dtype, device=m.device)
+    _need(out, "out", m.shape)
+    ws, nws = _ortho_workspace(batch, rows, cols, m.device, stream, "orthogonalize")
+    _check(_lib.disco_orthogonalize(m.data_ptr(), _dtype_code(m), out.data_ptr(), _dtype_code(out),
+                                    batch, rows, cols, steps, _coeffs(coeffs), eps, ws.data_ptr(),
+                                    nws, _stream(stream)), "orthogonalize")
+    return out
+
+
+def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool = True,
+              weight_decay: float = 0.0, scale: float | None = None, steps: int = 5, coeffs=None,
+              eps: float = 1e-7, groups: int = 1, w_out=None, momentum_out=None,
+              need_bf16_copy: bool = False, w16=None, stream=None):
+    """One step of the optimiser that orthogonalises the momentum:
+
+        momentum <- beta momentum + grad
+        u = grad + beta momentum (nesterov), or momentum
+        w <- w (1 - lr weight_decay) - lr scale orthogonalize(u)
+
+    w [Co, ...] is seen as `groups` matrices of Co/groups rows (the layer's
+    weight [Co, Ci/groups, K] with its groups); grad and momentum (float32)
+    have its shape.  scale None: sqrt(max(1, rows/cols)).  w and momentum are
+    updated in place unless w_out / momentum_out are given.  need_bf16_copy:
+    also return (in w16, if given) the bfloat16 copy of a float32 w.
+    Returns (w, momentum, w16)."""
+    torch = _torch()
+    if w.dim() < 2:
+        raise ValueError("w must have at least two dimensions")
+    if groups < 1 or w.shape[0] % groups:
+        raise ValueError(f"groups ({groups}) must divide w's {w.shape[0]} rows")
+    _need(w, "w", w.shape)
+    _need(grad, "grad", w.shape)
+    mptr = _f32_ptr(momentum, "momentum", w.shape)
+    if mptr is None:
+        raise ValueError("momentum is needed (zeros at first)")
+    w_out = w if w_out is None else w_out
+    momentum_out = momentum if momentum_out is None else momentum_out
+    _need(w_out, "w_out", w.shape)
+    if w_out.dtype != w.dtype:
+        raise ValueError(f"w_out must have w's dtype ({w.dtype})")
+    rows, cols = w.shape[0] // groups, 1
+    for n in w.shape[1:]:
+        cols *= n
+    if scale is None:
+        scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
+    if w16 is None and need_bf16_copy:
+        w16 = torch.empty(w.shape, dtype=torch.bfloat16, device=w.device)
+    if w16 is not None:
+        _need(w16, "w16", w.shape)
+        if w16.dtype != torch.bfloat16:
+            raise ValueError("w16 must be bfloat16")
+    ws, nws = _ortho_workspace(groups, rows, cols, w.device, stream, "muon_step")
+    _check(_lib.disco_muon_step(
+        grad.data_ptr(), _dtype_code(grad), mptr, _f32_ptr(momentum_out, "momentum_out", w.shape),
+        w.data_ptr(), _dtype_code(w), w_out.data_ptr(), w16.data_ptr() if w16 is not None else None,
+        lr, beta, int(nesterov), weight_decay, scale, groups, rows, cols, steps, _coeffs(coeffs), eps,
+        ws.data_ptr(), nws, _stream(stream)), "muon_step")
+    return w_out, momentum_out, w16

@@ -28,6 +28,7 @@ SOURCES = [
     "kernels_backward.hip",
     "training_api.cpp",
     "kernels_layer_norm.hip",
+    "kernels_orthogonalize.hip",
     "spectral_host.cpp",
     "kernel_timing.cpp",
 ]

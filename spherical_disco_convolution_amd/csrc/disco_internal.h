@@ -207,6 +207,30 @@ int launch_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dty
                           const void* gsum, void* gx, int gx_dtype, float* ggamma, float* gbeta,
                           float* partial, int64_t outer, int C, int64_t inner, void* stream);
 
+// Orthogonalised updates (kernels_orthogonalize.hip).  `batch` matrices of
+// rows x cols, one after another.  The matrix is m (momentum_out NULL), or the
+// momentum update of the gradient m; the result goes to o, or into the weights.
+struct OrthoCall {
+    const void* m;
+    int m_dtype;
+    const float* momentum;
+    float* momentum_out;
+    float beta;
+    int nesterov;
+    void* o;              // exclusive with w
+    int out_dtype;        // of o, or of w and w_out
+    const void* w;
+    void* w_out;
+    void* w16;            // bf16 copy of w_out, or NULL
+    float keep, rate;     // w_out = keep * w - rate * orthogonalised
+    int batch, rows, cols, steps;
+    float coeffs[3];
+    float eps;
+    void* workspace;
+};
+size_t orthogonalize_workspace(int batch, int rows, int cols);
+int launch_orthogonalize(const OrthoCall& c, void* stream);
+
 // Scope around one kernel launch: while disco_kernel_timing(1) is in effect,
 // records a HIP event on the launch stream at construction and at
 // destruction, for disco_kernel_timing_read.  The name must be a string
