@@ -25,6 +25,7 @@ Entry points (same names as the C ABI, without the ``disco_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -257,11 +258,18 @@ def _torch_dtype(code: int):
     return torch.float32 if code == F32 else torch.bfloat16
 
 
-def _stream(stream):
+def _raw_current_stream():
+    """Handle of the current device's current stream.  torch.cuda.current_stream()
+    builds a Stream object each time (2.7 us, against 0.1 us for the handle)."""
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
+def _stream(stream):
+    return ctypes.c_void_p(_raw_current_stream() if stream is None else stream.cuda_stream)
 
 
 def _need(t, name, shape):
@@ -507,12 +515,8 @@ def _norm_view(x, axis):
         raise ValueError(f"axis {axis} is out of range for {x.dim()} dimensions")
     axis %= x.dim()
     shape = x.shape
-    outer = inner = 1
-    for n in shape[:axis]:
-        outer *= n
-    for n in shape[axis + 1:]:
-        inner *= n
-    return outer, shape[axis], inner, shape[:axis] + shape[axis + 1:]
+    before, after = shape[:axis], shape[axis + 1:]
+    return math.prod(before), shape[axis], math.prod(after), before + after
 
 
 def _f32_ptr(t, name, shape):
@@ -555,11 +559,12 @@ def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, a
             raise ValueError(f"residual must have x's dtype ({x.dtype})")
         s = torch.empty_like(x)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    _need(y, "y", x.shape)
+        y = torch.empty_like(x, dtype=x.dtype if out_dtype is None else out_dtype)
+    else:
+        _need(y, "y", x.shape)
     if need_stats:
-        mean = torch.empty(points, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(points, dtype=torch.float32, device=x.device)
+        mean = x.new_empty(points, dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     _check(_lib.disco_layer_norm_fwd(
         x.data_ptr(), _dtype_code(x), residual.data_ptr() if s is not None else None, gptr, bptr,
         y.data_ptr(), _dtype_code(y), s.data_ptr() if s is not None else None,
@@ -588,12 +593,11 @@ def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need
             raise ValueError(f"gsum must have gy's dtype ({gy.dtype})")
     gx = gg = gb = None
     if need_gx:
-        gx = torch.empty(x.shape, dtype=torch.float32 if gx_dtype is None else gx_dtype,
-                         device=x.device)
+        gx = torch.empty_like(x, dtype=torch.float32 if gx_dtype is None else gx_dtype)
     ws, nws = None, 0
     if need_gparams:
-        gg = torch.empty((C,), dtype=torch.float32, device=x.device)
-        gb = torch.empty((C,), dtype=torch.float32, device=x.device)
+        gg = x.new_empty((C,), dtype=torch.float32)
+        gb = torch.empty_like(gg)
         nws = _lib.disco_layer_norm_bwd_workspace(outer, C, inner)
         if nws < 0:
             _check(nws, "layer_norm_bwd")
@@ -680,9 +684,7 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
     _need(w_out, "w_out", w.shape)
     if w_out.dtype != w.dtype:
         raise ValueError(f"w_out must have w's dtype ({w.dtype})")
-    rows, cols = w.shape[0] // groups, 1
-    for n in w.shape[1:]:
-        cols *= n
+    rows, cols = w.shape[0] // groups, math.prod(w.shape[1:])
     if scale is None:
         scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
     if w16 is None and need_bf16_copy:

@@ -326,8 +326,14 @@ __global__ __launch_bounds__(1024) void ln_fwd_field_walk(
 // Backward of a field.  Persistent workgroups walk tiles of 64 V points; each
 // lane keeps its channels' ggamma and gbeta in registers over all its tiles,
 // and a workgroup's sums go to partial[block * WP + wp][2][C] at the end.
-template <typename TX, typename TG, typename TO, int V, int CPW>
-__global__ __launch_bounds__(1024) void ln_bwd_field(
+//
+// At C = 128 bf16 with gsum (721 x 1440, 1.07 GB) the tile is two points a lane:
+// 110 registers, so that two workgroups of 8 waves share a compute unit and one
+// loads while the other waits for its sums: 242 us, 4.4 TB/s.  Four points a
+// lane spill (367 us), and loading the next tile ahead with 244 registers and
+// one workgroup a unit comes to 281 us.
+template <typename TX, typename TG, typename TO, int V, int CPW, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void ln_bwd_field(
     const TX* __restrict__ x, const TG* __restrict__ gy, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const float* __restrict__ gamma,
     const TG* __restrict__ gsum, TO* __restrict__ gx, float* __restrict__ partial, int C,
@@ -341,9 +347,10 @@ __global__ __launch_bounds__(1024) void ln_bwd_field(
     for (int i = 0; i < CPW; ++i) dg[i] = db[i] = 0.0f;
     const float rc = 1.0f / (float)C;
     int parity = 0;
+
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        // whole accesses only, as in the forward kernel; the first `skip` points
-        // of a lane are another lane's and stay out of the parameter sums
+        // whole accesses only, as in the forward kernel; a lane's first `skip`
+        // points are another lane's and stay out of the parameter sums
         const int64_t g0 = (tile * WP + wp) * 64 + lane;
         const int64_t g = min(g0, total - 1);
         const int64_t b = split_index(g, groups, total);
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(1024) void ln_bwd_field(
         const int skip = g0 < total ? (int)(at0 - n0) : V;
         const int64_t o = (b * C + c0) * inner + n0;
         Pack<TX, V> vx[CPW];
-        Pack<TG, V> vg[CPW];
+        Pack<TG, V> vg[CPW], vs[CPW];
         Pack<float, V> mu, r;
         mu.load(mean_in + b * inner + n0);
         r.load(rstd_in + b * inner + n0);
@@ -361,6 +368,10 @@ __global__ __launch_bounds__(1024) void ln_bwd_field(
             vx[i].load(x + at);
             vg[i].load(gy + at);
         }
+        if (gsum != nullptr)
+#pragma unroll
+            for (int i = 0; i < CPW; ++i)
+                vs[i].load(gsum + o + (int64_t)min(i, nc - 1) * inner);
         float s1[V], s2[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) s1[e] = s2[e] = 0.0f;
@@ -416,23 +427,17 @@ __global__ __launch_bounds__(1024) void ln_bwd_field(
 #pragma unroll
             for (int i = 0; i < CPW; ++i)
                 if (i < nc) {
-                    const int64_t at = o + (int64_t)i * inner;
                     const float ga = gamma ? gamma[c0 + i] : 1.0f;
                     float f[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float h = (vx[i].get(e) - mu.get(e)) * r.get(e);
                         f[e] = r.get(e) * (vg[i].get(e) * ga - s1[e] - h * s2[e]);
-                    }
-                    if (gsum != nullptr) {
-                        Pack<TG, V> k;
-                        k.load(gsum + at);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) f[e] += k.get(e);
+                        if (gsum != nullptr) f[e] += vs[i].get(e);
                     }
                     Pack<TO, V> k;
                     k.set(f);
-                    k.store(gx + at);
+                    k.store(gx + o + (int64_t)i * inner);
                 }
         }
     }
@@ -535,9 +540,9 @@ __global__ __launch_bounds__(256) void ln_bwd_params_walk(
 // ---------------------------------------------------------------------------
 // rows: inner == 1
 // ---------------------------------------------------------------------------
-// Sum over the `tpr` threads of a row; tpr <= 64: lanes of one wave, else the
-// whole workgroup through LDS (red: 16 floats; ends with every thread holding
-// the sum and red free again).
+// Sum over the `tpr` threads of a row; tpr <= 64: lanes of one wave, else
+// tpr / 64 waves through LDS (red: 16 floats; the whole workgroup takes part and
+// red is free again at the end).
 __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
     if (tpr <= 64) {
         for (int m = tpr >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m);
@@ -545,10 +550,12 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
     }
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    const int wave = threadIdx.x >> 6, n = tpr >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
+    const float* mine = red + wave / n * n;
     float t = 0.0f;
-    for (int k = 0; k < tpr >> 6; ++k) t += red[k];
+    for (int k = 0; k < n; ++k) t += mine[k];
     __syncthreads();
     return t;
 }
@@ -663,28 +670,31 @@ __global__ __launch_bounds__(1024) void ln_fwd_row_walk(
 
 // Backward of rows.  Persistent workgroups of blockDim / tpr row slots; each
 // thread keeps the parameter sums of its channels in registers over all its
-// rows, and the slots are added in LDS, in slot order, at the end.
+// rows, and the slots are added in LDS, in slot order, at the end, so that a
+// workgroup leaves one row of partial sums.  gamma waits in LDS.
 template <typename TX, typename TG, typename TO, int V, int NV>
-__global__ __launch_bounds__(1024) void ln_bwd_row(
+__global__ __launch_bounds__(V * NV > 16 ? 512 : 1024) void ln_bwd_row(
     const TX* __restrict__ x, const TG* __restrict__ gy, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const float* __restrict__ gamma,
     const TG* __restrict__ gsum, TO* __restrict__ gx, float* __restrict__ partial, int C,
     int64_t rows, int tpr) {
-    extern __shared__ __attribute__((aligned(16))) float red[];
+    extern __shared__ __attribute__((aligned(16))) float lds[];   // 16 floats, then gamma or the sums
+    float* red = lds;
+    float* vec = lds + 16;
     const int t = threadIdx.x & (tpr - 1);
     const int slots = blockDim.x / tpr, slot = threadIdx.x / tpr;
-    float dg[NV][V], db[NV][V], ga[NV][V];
+    float dg[NV][V], db[NV][V];
     int nc[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + t) * V;
-        nc[j] = max(0, min(V, C - c));
+        nc[j] = max(0, min(V, C - (j * tpr + t) * V));
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            dg[j][e] = db[j][e] = 0.0f;
-            ga[j][e] = e < nc[j] ? (gamma ? gamma[c + e] : 1.0f) : 0.0f;
-        }
+        for (int e = 0; e < V; ++e) dg[j][e] = db[j][e] = 0.0f;
     }
+    // padded to whole vectors with zeros: channels past C add nothing
+    for (int c = threadIdx.x; c < NV * tpr * V; c += blockDim.x)
+        vec[c] = c < C ? (gamma ? gamma[c] : 1.0f) : 0.0f;
+    __syncthreads();
     const float rc = 1.0f / (float)C;
     // every thread takes part in each step's sums, with zeros past the last row
     for (int64_t row0 = (int64_t)blockIdx.x * slots; row0 < rows;
@@ -708,19 +718,21 @@ __global__ __launch_bounds__(1024) void ln_bwd_row(
             }
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const float* ga = vec + (j * tpr + t) * V;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float gr = vg[j].get(e);
+                const float gr = vg[j].get(e);   // zero past C
                 const float h = (vx[j].get(e) - mu) * r;
-                const float q = gr * ga[j][e];
-                if (e < nc[j]) {
-                    s1 += q;
-                    s2 += q * h;
-                    dg[j][e] += gr * h;
-                    db[j][e] += gr;
-                }
+                const float q = gr * ga[e];
+                s1 += q;
+                s2 += q * h;
+                dg[j][e] += gr * h;
+                db[j][e] += gr;
             }
+            vx[j].keep_packed();
+            vg[j].keep_packed();
+        }
         s1 = row_sum(s1, tpr, red) * rc;
         s2 = row_sum(s2, tpr, red) * rc;
         if (gx != nullptr && active) {
@@ -728,11 +740,12 @@ __global__ __launch_bounds__(1024) void ln_bwd_row(
             for (int j = 0; j < NV; ++j)
                 if (nc[j] > 0) {
                     const int c = (j * tpr + t) * V;
+                    const float* ga = vec + c;
                     float f[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float h = (vx[j].get(e) - mu) * r;
-                        f[e] = r * (vg[j].get(e) * ga[j][e] - s1 - h * s2);
+                        f[e] = r * (vg[j].get(e) * ga[e] - s1 - h * s2);
                     }
                     if (gsum != nullptr) {
                         Pack<TG, V> k;
@@ -770,22 +783,26 @@ __global__ __launch_bounds__(1024) void ln_bwd_row(
                 dg[j][e] += __shfl_xor(dg[j][e], m);
                 db[j][e] += __shfl_xor(db[j][e], m);
             }
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6, lane = threadIdx.x & 63;
-    for (int w = 0; w < waves; ++w) {
-        if (w == wave && lane < tpr)
+    __syncthreads();   // gamma has been read
+    // then the waves (or groups of tpr / 64 waves) one after another
+    const int turn = tpr < 64 ? threadIdx.x >> 6 : slot;
+    const int turns = tpr < 64 ? blockDim.x >> 6 : slots;
+    const bool holds = tpr >= 64 || (threadIdx.x & 63) < tpr;
+    for (int w = 0; w < turns; ++w) {
+        if (w == turn && holds)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * tpr + t) * V;
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     if (e < nc[j]) {
-                        red[c + e] = dg[j][e] + (w ? red[c + e] : 0.0f);
-                        red[C + c + e] = db[j][e] + (w ? red[C + c + e] : 0.0f);
+                        vec[c + e] = dg[j][e] + (w ? vec[c + e] : 0.0f);
+                        vec[C + c + e] = db[j][e] + (w ? vec[C + c + e] : 0.0f);
                     }
             }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) row[i] = red[i];
+    for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) row[i] = vec[i];
 }
 
 // gx of rows too long for the registers: two walks, a workgroup a row.
@@ -831,22 +848,25 @@ __global__ __launch_bounds__(256) void ln_bwd_row_params_walk(
     partial[(size_t)blockIdx.y * 2 * C + C + c] = q;
 }
 
-// ggamma and gbeta from partial[n][2][C]: 16 columns a workgroup, the rows in
-// 16 interleaved slices, added in a fixed order.
+// ggamma and gbeta from partial[n][2][C]: 8 columns a workgroup, the rows in 32
+// interleaved slices, added in a fixed order.
 __global__ __launch_bounds__(256) void ln_reduce_params(const float* __restrict__ partial, int n,
                                                         int C, float* __restrict__ ggamma,
                                                         float* __restrict__ gbeta) {
-    __shared__ float red[16][17];
-    const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    const int64_t i = (int64_t)blockIdx.x * 16 + col;
+    __shared__ float red[32][9];
+    const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    const int64_t i = (int64_t)blockIdx.x * 8 + col;
     float a = 0.0f;
-    if (i < 2 * (int64_t)C)
-        for (int k = slice; k < n; k += 16) a += partial[(size_t)k * 2 * C + i];
+    if (i < 2 * (int64_t)C) {
+#pragma unroll 8
+        for (int k = slice; k < n; k += 32) a += partial[(size_t)k * 2 * C + i];
+    }
     red[slice][col] = a;
     __syncthreads();
     if (slice == 0 && i < 2 * (int64_t)C) {
         a = 0.0f;
-        for (int k = 0; k < 16; ++k) a += red[k][col];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) a += red[k][col];
         if (i < C) {
             if (ggamma) ggamma[i] = a;
         } else if (gbeta) {
@@ -860,7 +880,6 @@ __global__ __launch_bounds__(256) void ln_reduce_params(const float* __restrict_
 // ---------------------------------------------------------------------------
 constexpr int kMaxWaves = 16;
 constexpr int kFwdMaxCpw = 32, kBwdMaxCpw = 16;
-constexpr int kBwdRowV = 4;
 
 // Channels a wave holds and the waves over the channels.
 struct FieldShape {
@@ -976,29 +995,63 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
     return done("ln_fwd_field");
 }
 
-// partial rows of the parameter sums; also the launcher's grid
+// The backward kernel's: rows share a workgroup as long as that leaves one for
+// each of 256 compute units, since each workgroup leaves a row of partial sums.
+struct BwdRowShape : RowShape {
+    int slots = 0;
+    int grid = 0;
+};
+
+BwdRowShape bwd_row_shape(int C, int64_t rows, int v) {
+    BwdRowShape r;
+    static_cast<RowShape&>(r) = row_shape(C, rows, v);
+    if (r.nv == 0 || C > 16384) {   // past 16 channels a lane of 1024
+        r.nv = 0;
+        return r;
+    }
+    if (C > 8192 && r.tpr < 1024) {   // the slots' sums would need more than 64 KB of LDS
+        r.tpr = 1024;
+        r.nv = 1;
+        while ((int64_t)r.tpr * r.nv * v < C) r.nv *= 2;
+    }
+    r.slots = std::max(1, 256 / r.tpr);
+    // 32 channels a lane and their sums take more than 128 registers
+    const int most = v * r.nv > 16 ? 512 : 1024;
+    while (r.slots * 2 * r.tpr <= most && rows >= (int64_t)256 * 2 * r.slots) r.slots *= 2;
+    r.threads = r.slots * r.tpr;
+    r.grid = (int)std::min<int64_t>(r.threads >= 512 ? 256 : 512, cdiv(rows, r.slots));
+    return r;
+}
+
+constexpr int kBwdFieldGrid = 512;
+
+// at most this many rows of partial parameter sums
 int bwd_partial_rows(int64_t outer, int C, int64_t inner) {
     if (inner == 1) {
-        const RowShape r = row_shape(C, outer, kBwdRowV);
-        if (r.nv == 0) return (int)std::min<int64_t>(64, outer);
-        return (int)std::min<int64_t>(512, cdiv(outer, r.threads / r.tpr));
+        int n = 0;
+        for (int v : {4, 8}) {   // whichever vector length the types give
+            const BwdRowShape r = bwd_row_shape(C, outer, v);
+            n = std::max(n, r.nv == 0 ? (int)std::min<int64_t>(64, outer) : r.grid);
+        }
+        return n;
     }
     const FieldShape f = field_shape(C, kBwdMaxCpw);
     if (f.cpw == 0) return (int)std::min<int64_t>(64, cdiv(outer * inner, 256));
-    return 1024 * f.wp;   // at most: the grid is capped at 1024 workgroups
+    return (int)std::min<int64_t>(kBwdFieldGrid, cdiv(outer * inner, 64 * f.wp)) * f.wp;
 }
 
 template <typename TX, typename TG, typename TO>
 int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, const float* gamma,
               const TG* gsum, TO* gx, float* ggamma, float* gbeta, float* partial, int64_t outer,
               int C, int64_t inner, hipStream_t st) {
-    // 32 registers each of x and gy at 16 channels a wave
+    // points a lane: 4 bytes of each tensor at 16 channels a wave, else 8
     constexpr int V = sizeof(TX) + sizeof(TG) == 4 ? 4 : 2;
+    constexpr int VR = sizeof(TX) + sizeof(TG) == 4 ? 8 : 4;   // row kernel
     const bool params = ggamma != nullptr || gbeta != nullptr;
     float* part = params ? partial : nullptr;
     int n = 0;
     if (inner == 1) {
-        const RowShape r = row_shape(C, outer, kBwdRowV);
+        const BwdRowShape r = bwd_row_shape(C, outer, VR);
         if (r.nv == 0) {
             if (outer > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many rows");
             if (gx != nullptr) {
@@ -1016,12 +1069,13 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
                 if (int rc = done("ln_bwd_row_params_walk")) return rc;
             }
         } else {
-            const int slots = r.threads / r.tpr;
-            n = (int)std::min<int64_t>(512, cdiv(outer, slots));
-            const size_t lds = std::max<size_t>(64, slots > 1 ? (size_t)2 * C * sizeof(float) : 0);
+            n = r.grid;
+            const size_t lds =
+                (16 + std::max<size_t>((size_t)r.nv * r.tpr * VR, r.slots > 1 ? 2 * (size_t)C : 0)) *
+                sizeof(float);
             KernelTimer timer("ln_bwd_row", st);
-#define DISCO_LN(NV)                                                                              \
-    hipLaunchKernelGGL((ln_bwd_row<TX, TG, TO, kBwdRowV, NV>), dim3(n), dim3(r.threads), lds, st, x, gy, \
+#define DISCO_LN(NV)                                                                               \
+    hipLaunchKernelGGL((ln_bwd_row<TX, TG, TO, VR, NV>), dim3(n), dim3(r.threads), lds, st, x, gy, \
                        mean, rstd, gamma, gsum, gx, part, C, outer, r.tpr)
             if (r.nv == 1) DISCO_LN(1);
             else if (r.nv == 2) DISCO_LN(2);
@@ -1049,28 +1103,28 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
                 if (int rc = done("ln_bwd_params_walk")) return rc;
             }
         } else {
-            const bool wide = inner >= V && outer * cdiv(inner, V) >= (int64_t)512 * 64 * f.wp;
-            const int VV = wide ? V : 1;
+            const int vw = f.cpw == 16 ? V / 2 : V;
+            const bool wide = inner >= vw && outer * cdiv(inner, vw) >= (int64_t)512 * 64 * f.wp;
+            const int VV = wide ? vw : 1;
             const int64_t groups = cdiv(inner, VV), total = outer * groups;
             const int64_t tiles = cdiv(total, 64 * f.wp);
-            const int grid = (int)std::min<int64_t>(1024, tiles);
+            const int grid = (int)std::min<int64_t>(kBwdFieldGrid, tiles);
             n = grid * f.wp;
             const size_t lds = f.wc > 1 ? (size_t)2 * f.wc * f.wp * 128 * VV * sizeof(float) : 0;
             KernelTimer timer("ln_bwd_field", st);
-#define DISCO_LN(VW, CPW)                                                                       \
-    hipLaunchKernelGGL((ln_bwd_field<TX, TG, TO, VW, CPW>), dim3(grid), dim3(64, f.wc, f.wp),   \
-                       lds, st, x, gy, mean, rstd, gamma, gsum, gx, part, C, inner, groups, total, \
-                       tiles)
-#define DISCO_LN_V(CPW)             \
-    do {                            \
-        if (wide) DISCO_LN(V, CPW); \
-        else DISCO_LN(1, CPW);      \
+#define DISCO_LN(VW, CPW, WAVES)                                                                \
+    hipLaunchKernelGGL((ln_bwd_field<TX, TG, TO, VW, CPW, WAVES>), dim3(grid),           \
+                       dim3(64, f.wc, f.wp), lds, st, x, gy, mean, rstd, gamma, gsum, gx, part, C, \
+                       inner, groups, total, tiles)
+#define DISCO_LN_V(VW, CPW, WAVES)             \
+    do {                                       \
+        if (wide) DISCO_LN(VW, CPW, WAVES);    \
+        else DISCO_LN(1, CPW, WAVES);          \
     } while (0)
-            switch (f.cpw) {
-                case 4: DISCO_LN_V(4); break;
-                case 8: DISCO_LN_V(8); break;
-                default: DISCO_LN_V(16); break;
-            }
+            if (f.cpw == 4) DISCO_LN_V(V, 4, 8);
+            else if (f.cpw == 8) DISCO_LN_V(V, 8, 8);
+            else if (f.wc <= 8) DISCO_LN_V(V / 2, 16, 8);
+            else DISCO_LN_V(V / 2, 16, 16);
 #undef DISCO_LN_V
 #undef DISCO_LN
             if (int rc = done("ln_bwd_field")) return rc;
@@ -1078,7 +1132,7 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
     }
     if (!params) return DISCO_OK;
     KernelTimer timer("ln_reduce_params", st);
-    hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(2 * (int64_t)C, 16)), dim3(256), 0, st,
+    hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(2 * (int64_t)C, 8)), dim3(256), 0, st,
                        partial, n, C, ggamma, gbeta);
     return done("ln_reduce_params");
 }
