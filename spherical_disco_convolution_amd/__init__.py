@@ -529,12 +529,13 @@ def _f32_ptr(t, name, shape):
     return t.data_ptr()
 
 
-def _workspace(nbytes, device, stream):
-    """Scratch for one call: the allocator keeps it until the call's stream is
-    done with it."""
-    torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None and nbytes:
+def _workspace(nbytes, like, stream):
+    """Scratch for one call on like's device (None for no bytes): the allocator
+    keeps it until the call's stream is done with it."""
+    if nbytes == 0:
+        return None
+    ws = like.new_empty(nbytes, dtype=_torch().uint8)
+    if stream is not None:
         ws.record_stream(stream)
     return ws
 
@@ -601,13 +602,13 @@ def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need
         nws = _lib.disco_layer_norm_bwd_workspace(outer, C, inner)
         if nws < 0:
             _check(nws, "layer_norm_bwd")
-        ws = _workspace(nws, x.device, stream)
+        ws = _workspace(nws, x, stream)
     _check(_lib.disco_layer_norm_bwd(
         x.data_ptr(), _dtype_code(x), gy.data_ptr(), _dtype_code(gy), mptr, rptr, gptr,
         gsum.data_ptr() if gsum is not None else None,
         gx.data_ptr() if need_gx else None, _dtype_code(gx) if need_gx else F32,
         gg.data_ptr() if need_gparams else None, gb.data_ptr() if need_gparams else None,
-        ws.data_ptr() if need_gparams else None, nws, outer, C, inner, _stream(stream)),
+        ws.data_ptr() if ws is not None else None, nws, outer, C, inner, _stream(stream)),
         "layer_norm_bwd")
     return gx, gg, gb
 
@@ -624,11 +625,11 @@ def _coeffs(coeffs):
     return (ctypes.c_float * 3)(*coeffs)
 
 
-def _ortho_workspace(batch, rows, cols, device, stream, what):
+def _ortho_workspace(batch, rows, cols, like, stream, what):
     n = _lib.disco_orthogonalize_workspace(batch, rows, cols)
     if n < 0:
         _check(n, what)
-    return _workspace(n, device, stream), n
+    return _workspace(n, like, stream), n
 
 
 def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps: float = 1e-7,
@@ -644,12 +645,14 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
     batch = m.shape[0] if m.dim() == 3 else 1
     rows, cols = m.shape[-2:]
     if out is None:
-        out = torch.empty(m.shape, dtype=m.dtype if out_dtype is None else out_dtype, device=m.device)
-    _need(out, "out", m.shape)
-    ws, nws = _ortho_workspace(batch, rows, cols, m.device, stream, "orthogonalize")
+        out = torch.empty_like(m, dtype=m.dtype if out_dtype is None else out_dtype)
+    else:
+        _need(out, "out", m.shape)
+    ws, nws = _ortho_workspace(batch, rows, cols, m, stream, "orthogonalize")
     _check(_lib.disco_orthogonalize(m.data_ptr(), _dtype_code(m), out.data_ptr(), _dtype_code(out),
-                                    batch, rows, cols, steps, _coeffs(coeffs), eps, ws.data_ptr(),
-                                    nws, _stream(stream)), "orthogonalize")
+                                    batch, rows, cols, steps, _coeffs(coeffs), eps,
+                                    ws.data_ptr() if ws is not None else None, nws,
+                                    _stream(stream)), "orthogonalize")
     return out
 
 
@@ -688,15 +691,15 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
     if scale is None:
         scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
     if w16 is None and need_bf16_copy:
-        w16 = torch.empty(w.shape, dtype=torch.bfloat16, device=w.device)
+        w16 = torch.empty_like(w, dtype=torch.bfloat16)
     if w16 is not None:
         _need(w16, "w16", w.shape)
         if w16.dtype != torch.bfloat16:
             raise ValueError("w16 must be bfloat16")
-    ws, nws = _ortho_workspace(groups, rows, cols, w.device, stream, "muon_step")
+    ws, nws = _ortho_workspace(groups, rows, cols, w, stream, "muon_step")
     _check(_lib.disco_muon_step(
         grad.data_ptr(), _dtype_code(grad), mptr, _f32_ptr(momentum_out, "momentum_out", w.shape),
         w.data_ptr(), _dtype_code(w), w_out.data_ptr(), w16.data_ptr() if w16 is not None else None,
         lr, beta, int(nesterov), weight_decay, scale, groups, rows, cols, steps, _coeffs(coeffs), eps,
-        ws.data_ptr(), nws, _stream(stream)), "muon_step")
+        ws.data_ptr() if ws is not None else None, nws, _stream(stream)), "muon_step")
     return w_out, momentum_out, w16

@@ -76,7 +76,21 @@ struct Sink {
     float keep, rate;     // w_out = keep * w - rate * o
 };
 
-__device__ __forceinline__ void sink_store(const Sink& s, int64_t i, float o) {
+// The sink of one batch entry, whose first element is `base`.
+__device__ __forceinline__ Sink sink_from(Sink s, int64_t base) {
+    const int64_t bytes = base * (s.bf16 ? 2 : 4);
+    if (s.o != nullptr) {
+        s.o = static_cast<char*>(s.o) + bytes;
+    } else {
+        s.w = static_cast<const char*>(s.w) + bytes;
+        s.w_out = static_cast<char*>(s.w_out) + bytes;
+        if (s.w16 != nullptr) s.w16 += base;
+    }
+    return s;
+}
+
+template <typename I>
+__device__ __forceinline__ void sink_store(const Sink& s, I i, float o) {
     if (s.o != nullptr) {
         if (s.bf16) store_f(static_cast<bf16_t*>(s.o), i, o);
         else static_cast<float*>(s.o)[i] = o;
@@ -358,6 +372,433 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_product(Product p) {
             }
 }
 
+// ---------------------------------------------------------------------------
+// Small matrices: the whole iteration in one workgroup per matrix
+// ---------------------------------------------------------------------------
+// X stays in registers.  A wave owns CB blocks of 32 columns with all 32 MT rows
+// in the matrix core's output layout (lane: column lane % 32; element 4 q + r:
+// row 8 q + 4 (lane / 32) + r).  Eight consecutive elements of that layout are
+// a valid operand of P X when P is read with the same permutation of the summed
+// rows, so the products chain without moving X.  X X^T sums over columns, which
+// lie across lanes: each wave turns its block over in its own piece of LDS
+// (transposing reads), the waves' partial sums meet in LDS, and A and P live
+// there too.  Always three products: a step is a few hundred matrix
+// instructions and the barriers and LDS round trips around them cost as much.
+typedef __attribute__((address_space(3))) halfx4 lds_halfx4;
+typedef int16_t v4i16_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16_t lds_v4i16;
+
+__device__ __forceinline__ floatx16 mfma3(halfx8 uh, halfx8 ul, halfx8 vh, halfx8 vl, floatx16 acc) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ul, vh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(uh, vl, acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(uh, vh, acc, 0, 0, 0);
+}
+
+// Fragment of a 32-wide block from LDS rows [k][i] (i contiguous): lane gets
+// i = lane % 32, k = 8 (lane / 32) .. + 7.  `at`: address of k = 0, i = 0.
+__device__ __forceinline__ halfx8 read_turned(uint32_t at, int stride, int lane) {
+    const int s = lane & 15, g = lane >> 4;
+    const uint32_t p = at + (uint32_t)((8 * (g >> 1) + (s >> 2)) * stride +
+                                       2 * (16 * (g & 1) + 4 * (s & 3)));
+    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)p);
+    const v4i16_t hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(p + 4 * stride));
+    return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Elements at .. at + 3 of a `total`-element tensor, at any element alignment;
+// what lies past the end reads as zero and is not written.
+__device__ __forceinline__ void load4(const float* p, int at, int total, float* v) {
+    struct __attribute__((packed, aligned(4))) U { float e[4]; };
+    if (at + 4 <= total) {
+        const U u = *reinterpret_cast<const U*>(p + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = u.e[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? p[at + e] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load4(const bf16_t* p, int at, int total, float* v) {
+    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
+    if (at + 4 <= total) {
+        const U u = *reinterpret_cast<const U*>(p + at);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            v[2 * e] = __uint_as_float(u.e[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u.e[e] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? bf16_to_f32(p[at + e]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store4(float* p, int at, int total, const float* v) {
+    struct __attribute__((packed, aligned(4))) U { float e[4]; };
+    if (at + 4 <= total) {
+        *reinterpret_cast<U*>(p + at) = U{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at + e < total) p[at + e] = v[e];
+    }
+}
+
+__device__ __forceinline__ void store4(bf16_t* p, int at, int total, const float* v) {
+    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
+    if (at + 4 <= total) {
+        U u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            u.e[e] = (uint32_t)f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16);
+        *reinterpret_cast<U*>(p + at) = u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at + e < total) store_f(p, at + e, v[e]);
+    }
+}
+
+template <int MT>
+struct SmallCfg {
+    static constexpr int M = 32 * MT;
+    static constexpr int NT = MT * (MT + 1) / 2;     // lower-triangle tiles
+    static constexpr int TURN = 2 * M + 8;           // bytes of a column while turned over
+    static constexpr int ROW_A = 2 * M + 16;         // bytes of a row of A: 16-byte reads
+    static constexpr int ROW_P = 2 * M + 8;          // of P: 8-byte reads
+    // a wave's piece: its columns (hi, lo), then its partial sums
+    static constexpr int PIECE = (2 * 32 * TURN > NT * 4096 ? 2 * 32 * TURN : NT * 4096);
+    static constexpr int A_BYTES = 2 * M * ROW_A, P_BYTES = 2 * M * ROW_P;
+    // A, P and the pieces; X in float32 before and after them
+    static size_t lds(int waves, int m, int n) {
+        return 256 + std::max((size_t)A_BYTES + P_BYTES + (size_t)waves * PIECE, (size_t)m * (n | 1) * 4);
+    }
+};
+
+template <typename T, int MT, int CB>
+__global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in, float* buf_out,
+                                                Sink sink, int m, int n, int tall, int steps,
+                                                float ca, float cb, float cc, float eps) {
+    using C = SmallCfg<MT>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds_raw[];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)&lds_raw[0];
+    double* red = reinterpret_cast<double*>(lds_raw);
+    const uint32_t A_at = lds0 + 256, P_at = A_at + C::A_BYTES;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int l32 = lane & 31, lg = lane >> 5;
+    const uint32_t piece = P_at + C::P_BYTES + (uint32_t)(wave * C::PIECE);
+    // 32-bit offsets from here on: at most 64 x 1024 elements
+    const int64_t base = (int64_t)blockIdx.x * m * n;
+    const T* in = static_cast<const T*>(src.m) + base;
+    const float* old = buf_out ? buf_in + base : nullptr;
+    float* fresh = buf_out ? buf_out + base : nullptr;
+    const Sink to = sink_from(sink, base);
+
+    // ---- X_0: through LDS as rows of X, in a short loop of whole reads (the
+    // unrolled alternative, each lane reading its own elements, costs 15 us more
+    // at 64 x 448, most of it fetching instructions that run once) ----
+    typedef __attribute__((address_space(3))) float lds_float;
+    const int ld = n | 1;   // odd: both orders of access spread over the banks
+    const uint32_t x_at = lds0 + 256;
+    double acc2 = 0.0;
+    const int total = m * n, width = tall ? m : n;   // of a row in memory
+    const float rwidth = 1.0f / (float)width;
+    // LDS place of element `at` and of the ones after it in its row
+    auto place = [&](int at, int& q, int& r) {
+        q = (int)(((float)at + 0.5f) * rwidth);   // at < 2^16: exact
+        r = at - q * width;
+    };
+    auto slot = [&](int q, int r) {
+        return (lds_float*)(uintptr_t)(x_at + 4u * (uint32_t)(tall ? r * ld + q : q * ld + r));
+    };
+    constexpr int K = 8;   // reads of four elements in flight
+    for (int at0 = 4 * threadIdx.x; at0 < total; at0 += 4 * K * blockDim.x) {
+        float v[K][4], o[K][4];
+#pragma unroll
+        for (int k = 0; k < K; ++k) load4(in, at0 + 4 * k * (int)blockDim.x, total, v[k]);
+        if (fresh != nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) load4(old, at0 + 4 * k * (int)blockDim.x, total, o[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = at0 + 4 * k * (int)blockDim.x;
+            if (at >= total) break;
+            int q, r;
+            place(at, q, r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (at + e >= total) break;
+                float u = v[k][e];
+                if (fresh != nullptr) {
+                    const float b = src.beta * o[k][e] + u;
+                    fresh[at + e] = b;
+                    u = src.nesterov ? u + src.beta * b : b;
+                }
+                acc2 += (double)u * (double)u;
+                *slot(q, r) = u;
+                if (++r == width) {
+                    r = 0;
+                    ++q;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) acc2 += __shfl_xor(acc2, k);
+    if (lane == 0) red[wave] = acc2;
+    __syncthreads();
+    acc2 = 0.0;
+    for (int w = 0; w < W; ++w) acc2 += red[w];
+    const double inv = 1.0 / (sqrt(acc2) + (double)eps) * (double)kSX;
+
+    // hi and lo parts: [column block][row tile][half of 16 rows]
+    halfx8 xh[CB][MT][2], xl[CB][MT][2];
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
+                const int j = 32 * (wave + W * c) + l32;
+                const bool ok = i < m && j < n;
+                const float v = *(const lds_float*)(uintptr_t)(x_at + 4u * (uint32_t)(ok ? i * ld + j : 0));
+                const Pair p = split(ok ? (float)((double)v * inv) : 0.0f);
+                xh[c][a][e >> 3][e & 7] = p.h;
+                xl[c][a][e >> 3][e & 7] = p.l;
+            }
+    __syncthreads();   // the pieces lie where X_0 lay
+
+    for (int t = 0; t < steps; ++t) {
+        // ---- this wave's part of X X^T, lower tiles ----
+        floatx16 g[C::NT];
+#pragma unroll
+        for (int k = 0; k < C::NT; ++k)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[k][e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = piece + (uint32_t)(l32 * C::TURN + 2 * (32 * a + 8 * q + 4 * lg));
+                    const halfx8 h = xh[c][a][q >> 1], l = xl[c][a][q >> 1];
+                    halfx4 h4, l4;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        h4[r] = h[4 * (q & 1) + r];
+                        l4[r] = l[4 * (q & 1) + r];
+                    }
+                    *(lds_halfx4*)(uintptr_t)at = h4;
+                    *(lds_halfx4*)(uintptr_t)(at + 32 * C::TURN) = l4;
+                }
+            // one wave's LDS accesses are carried out in order; the fence keeps
+            // the compiler from moving the reads up
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                halfx8 fh[MT], fl[MT];
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const uint32_t at = piece + (uint32_t)(16 * kc * C::TURN + 64 * a);
+                    fh[a] = read_turned(at, C::TURN, lane);
+                    fl[a] = read_turned(at + 32 * C::TURN, C::TURN, lane);
+                }
+                int k = 0;
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b <= a; ++b, ++k) g[k] = mfma3(fh[a], fl[a], fh[b], fl[b], g[k]);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        typedef float floatx4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) floatx4 lds_floatx4;
+#pragma unroll
+        for (int k = 0; k < C::NT; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const floatx4 v = {g[k][4 * q], g[k][4 * q + 1], g[k][4 * q + 2], g[k][4 * q + 3]};
+                *(lds_floatx4*)(uintptr_t)(piece + (uint32_t)(k * 4096 + q * 1024 + lane * 16)) = v;
+            }
+        __syncthreads();
+        // ---- A: the waves' parts added, both triangles, hi and lo ----
+        const uint32_t piece0 = P_at + C::P_BYTES;
+        for (int pos = threadIdx.x; pos < C::NT * 256; pos += blockDim.x) {
+            floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int w = 0; w < W; ++w)
+                v += *(const lds_floatx4*)(uintptr_t)(piece0 + (uint32_t)(w * C::PIECE + pos * 16));
+            const int k = pos >> 8, q = (pos >> 6) & 3, pl = pos & 63;
+            const int a = k == 0 ? 0 : 1, b = k == 2 ? 1 : 0;   // (0,0) (1,0) (1,1)
+            const int i = 32 * a + 8 * q + 4 * (pl >> 5), j = 32 * b + (pl & 31);
+            halfx4 h, l;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const Pair p = split(v[r] * (kSA / (kSX * kSX)));
+                h[r] = p.h;
+                l[r] = p.l;
+            }
+            // [j][i]: four neighbours; [i][j] too where the tile is not diagonal
+            const uint32_t at = A_at + (uint32_t)(j * C::ROW_A + 2 * i);
+            *(lds_halfx4*)(uintptr_t)at = h;
+            *(lds_halfx4*)(uintptr_t)(at + C::M * C::ROW_A) = l;
+            if (a != b) {
+                typedef __attribute__((address_space(3))) half_t lds_half;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t at2 = A_at + (uint32_t)((i + r) * C::ROW_A + 2 * j);
+                    *(lds_half*)(uintptr_t)at2 = h[r];
+                    *(lds_half*)(uintptr_t)(at2 + C::M * C::ROW_A) = l[r];
+                }
+            }
+        }
+        __syncthreads();
+        // ---- P = b A + c A^2, a tile per wave ----
+        for (int tile = wave; tile < MT * MT; tile += W) {
+            const int a = tile / MT, b = tile % MT;
+            floatx16 acc;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll
+            for (int kc = 0; kc < 2 * MT; ++kc) {
+                const uint32_t u = A_at + (uint32_t)((32 * a + l32) * C::ROW_A + 32 * kc + 16 * lg);
+                const uint32_t v = A_at + (uint32_t)((32 * b + l32) * C::ROW_A + 32 * kc + 16 * lg);
+                const halfx8 uh = *(const lds_halfx8*)(uintptr_t)u;
+                const halfx8 ul = *(const lds_halfx8*)(uintptr_t)(u + C::M * C::ROW_A);
+                const halfx8 vh = *(const lds_halfx8*)(uintptr_t)v;
+                const halfx8 vl = *(const lds_halfx8*)(uintptr_t)(v + C::M * C::ROW_A);
+                acc = mfma3(uh, ul, vh, vl, acc);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 32 * a + 8 * q + 4 * lg, j = 32 * b + l32;
+                const uint32_t at = A_at + (uint32_t)(j * C::ROW_A + 2 * i);
+                const halfx4 ah = *(const lds_halfx4*)(uintptr_t)at;
+                const halfx4 al = *(const lds_halfx4*)(uintptr_t)(at + C::M * C::ROW_A);
+                halfx4 h, l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const Pair p = split(cb * (kSP / kSA) * ((float)ah[r] + (float)al[r]) +
+                                         cc * (kSP / (kSA * kSA)) * acc[4 * q + r]);
+                    h[r] = p.h;
+                    l[r] = p.l;
+                }
+                const uint32_t pt = P_at + (uint32_t)(j * C::ROW_P + 2 * i);
+                *(lds_halfx4*)(uintptr_t)pt = h;
+                *(lds_halfx4*)(uintptr_t)(pt + C::M * C::ROW_P) = l;
+            }
+        }
+        __syncthreads();
+        // ---- X <- a X + P X ----
+        floatx16 y[CB][MT];
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[c][a][e] = 0.0f;
+#pragma unroll
+        for (int kc = 0; kc < 2 * MT; ++kc)
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                // rows 16 kc + 4 lg .. + 3 and + 8: the order X's elements have
+                const uint32_t at = P_at + (uint32_t)((32 * a + l32) * C::ROW_P + 32 * kc + 8 * lg);
+                const halfx4 h0 = *(const lds_halfx4*)(uintptr_t)at;
+                const halfx4 h1 = *(const lds_halfx4*)(uintptr_t)(at + 16);
+                const halfx4 l0 = *(const lds_halfx4*)(uintptr_t)(at + C::M * C::ROW_P);
+                const halfx4 l1 = *(const lds_halfx4*)(uintptr_t)(at + C::M * C::ROW_P + 16);
+                const halfx8 ph = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+                const halfx8 pl = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    y[c][a] = mfma3(ph, pl, xh[c][kc >> 1][kc & 1], xl[c][kc >> 1][kc & 1], y[c][a]);
+            }
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const Pair p = split(
+                        ca * ((float)xh[c][a][e >> 3][e & 7] + (float)xl[c][a][e >> 3][e & 7]) +
+                        y[c][a][e] * (1.0f / kSP));
+                    xh[c][a][e >> 3][e & 7] = p.h;
+                    xl[c][a][e >> 3][e & 7] = p.l;
+                }
+    }
+    // ---- result: back through LDS, written as it lies in memory ----
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
+                const int j = 32 * (wave + W * c) + l32;
+                if (i < m && j < n)
+                    *(lds_float*)(uintptr_t)(x_at + 4u * (uint32_t)(i * ld + j)) =
+                        ((float)xh[c][a][e >> 3][e & 7] + (float)xl[c][a][e >> 3][e & 7]) * (1.0f / kSX);
+            }
+    __syncthreads();
+    for (int at0 = 4 * threadIdx.x; at0 < total; at0 += 4 * K * blockDim.x) {
+        float w[K][4];
+        if (to.o == nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int at = at0 + 4 * k * (int)blockDim.x;
+                if (to.bf16) load4(static_cast<const bf16_t*>(to.w), at, total, w[k]);
+                else load4(static_cast<const float*>(to.w), at, total, w[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = at0 + 4 * k * (int)blockDim.x;
+            if (at >= total) break;
+            int q, r;
+            place(at, q, r);
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = at + e < total ? *slot(q, r) : 0.0f;
+                if (++r == width) {
+                    r = 0;
+                    ++q;
+                }
+            }
+            if (to.o == nullptr) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = to.keep * w[k][e] - to.rate * f[e];
+            }
+            void* out = to.o ? to.o : to.w_out;
+            if (to.bf16) store4(static_cast<bf16_t*>(out), at, total, f);
+            else store4(static_cast<float*>(out), at, total, f);
+            if (to.o == nullptr && to.w16 != nullptr) store4(to.w16, at, total, f);
+        }
+    }
+}
+
+// Column blocks a wave takes (0: the matrix is not small) and the waves.
+struct SmallShape {
+    int mt = 0, cb = 0, waves = 0;
+};
+
+SmallShape small_shape(int m, int n) {
+    SmallShape s;
+    const int blocks = (n + 31) / 32, mt = (m + 31) / 32;
+    if (mt > 2 || blocks > (mt == 1 ? 32 : 16)) return s;
+    s.mt = mt;
+    s.cb = 1;
+    while (s.cb * 8 < blocks) s.cb *= 2;
+    // at least a wave for each tile of A, also where there are fewer columns
+    s.waves = std::max(mt * mt, (blocks + s.cb - 1) / s.cb);
+    return s;
+}
+
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Where everything of a call lies in its workspace.
@@ -419,11 +860,63 @@ int launch_product(bool three, const Product& p, int tiles, int batch, hipStream
 }  // namespace
 
 size_t orthogonalize_workspace(int batch, int rows, int cols) {
+    if (small_shape(std::min(rows, cols), std::max(rows, cols)).cb != 0) return 0;
     return layout(batch, rows, cols).bytes;
 }
 
+namespace {
+
+template <typename T, int MT, int CB>
+int launch_small(const OrthoCall& c, const Sink& sink, int waves, hipStream_t st) {
+    const size_t lds =
+        SmallCfg<MT>::lds(waves, std::min(c.rows, c.cols), std::max(c.rows, c.cols));
+    if (lds > 65536) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&ns_small<T, MT, CB>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) {
+            (void)hipGetLastError();
+            return set_error(DISCO_EHIP, "ns_small: %zu bytes of LDS refused: %s", lds,
+                             hipGetErrorString(e));
+        }
+    }
+    const Source src{c.m, c.momentum_out, c.beta, c.nesterov};
+    const int tall = c.rows > c.cols;
+    KernelTimer timer("ns_small", st);
+    hipLaunchKernelGGL((ns_small<T, MT, CB>), dim3(c.batch), dim3(64 * waves), lds, st, src,
+                       c.momentum, c.momentum_out, sink, std::min(c.rows, c.cols),
+                       std::max(c.rows, c.cols), tall, c.steps, c.coeffs[0], c.coeffs[1],
+                       c.coeffs[2], c.eps);
+    return done("ns_small");
+}
+
+template <typename T>
+int launch_small(const OrthoCall& c, const Sink& sink, const SmallShape& s, hipStream_t st) {
+    if (s.mt == 1) {
+        if (s.cb == 1) return launch_small<T, 1, 1>(c, sink, s.waves, st);
+        if (s.cb == 2) return launch_small<T, 1, 2>(c, sink, s.waves, st);
+        return launch_small<T, 1, 4>(c, sink, s.waves, st);
+    }
+    if (s.cb == 1) return launch_small<T, 2, 1>(c, sink, s.waves, st);
+    return launch_small<T, 2, 2>(c, sink, s.waves, st);
+}
+
+}  // namespace
+
 int launch_orthogonalize(const OrthoCall& c, void* stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
+    Sink sink{};
+    sink.o = c.o;
+    sink.bf16 = c.out_dtype == DISCO_BF16;
+    sink.w = c.w;
+    sink.w_out = c.w_out;
+    sink.w16 = static_cast<bf16_t*>(c.w16);
+    sink.keep = c.keep;
+    sink.rate = c.rate;
+    const SmallShape small = small_shape(std::min(c.rows, c.cols), std::max(c.rows, c.cols));
+    if (small.cb != 0)
+        return c.m_dtype == DISCO_F32 ? launch_small<float>(c, sink, small, st)
+                                      : launch_small<bf16_t>(c, sink, small, st);
+
     const Layout l = layout(c.batch, c.rows, c.cols);
     char* ws = static_cast<char*>(c.workspace);
     double* partial = reinterpret_cast<double*>(ws + l.partial);
@@ -456,15 +949,6 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
                                c.eps, l.m, l.n, l.mp, l.np, l.tall, X, XT[0], l.xplane);
         if (int rc = done("ns_load")) return rc;
     }
-    Sink sink{};
-    sink.o = c.o;
-    sink.bf16 = c.out_dtype == DISCO_BF16;
-    sink.w = c.w;
-    sink.w_out = c.w_out;
-    sink.w16 = static_cast<bf16_t*>(c.w16);
-    sink.keep = c.keep;
-    sink.rate = c.rate;
-
     const int tm = l.mp / 64, tn = l.np / 64;
     // A bfloat16 result takes single float16 products in all but the last two
     // steps: 2e-4 to 1e-3 off before its own rounding of 1.7e-3 (three products

@@ -208,12 +208,12 @@ int disco_orthogonalize(const void* m, int m_dtype, void* o, int o_dtype, int32_
     int rc = check_ortho(batch, rows, cols, steps, coeffs, eps, call.coeffs, &n);
     if (rc != DISCO_OK || n == 0) return rc;
     const int64_t need = (int64_t)orthogonalize_workspace(batch, rows, cols);
-    if (workspace == nullptr || workspace_bytes < need)
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return set_error(DISCO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                          (long long)(workspace ? workspace_bytes : 0), (long long)need);
     const int sm = dtype_size(m_dtype), so = dtype_size(o_dtype);
     const Arg ins[] = {{"m", m, n * sm, sm, true}};
-    const Arg outs[] = {{"o", o, n * so, so, true}, {"workspace", workspace, need, 16, true}};
+    const Arg outs[] = {{"o", o, n * so, so, true}, {"workspace", need ? workspace : nullptr, need, 16, need > 0}};
     if ((rc = check_args(ins, 1, outs, 2)) != DISCO_OK) return rc;
     call.m = m;
     call.m_dtype = m_dtype;
@@ -248,7 +248,7 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
     int rc = check_ortho(batch, rows, cols, steps, coeffs, eps, call.coeffs, &n);
     if (rc != DISCO_OK || n == 0) return rc;
     const int64_t need = (int64_t)orthogonalize_workspace(batch, rows, cols);
-    if (workspace == nullptr || workspace_bytes < need)
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return set_error(DISCO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                          (long long)(workspace ? workspace_bytes : 0), (long long)need);
     const int sg = dtype_size(grad_dtype), sw = dtype_size(w_dtype);
@@ -258,7 +258,7 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
     const Arg outs[] = {{"momentum_out", momentum_out, n * 4, 4, true, 1},
                         {"w_out", w_out, n * sw, sw, true, 2},
                         {"w16", w16, n * 2, 2, false},
-                        {"workspace", workspace, need, 16, true}};
+                        {"workspace", need ? workspace : nullptr, need, 16, need > 0}};
     if ((rc = check_args(ins, 3, outs, 4)) != DISCO_OK) return rc;
     call.m = grad;
     call.m_dtype = grad_dtype;

@@ -276,9 +276,10 @@ def test_refusals(sdc):
     with pytest.raises(ValueError):
         sdc.muon_step(w.to(BF16), g, b, 0.1, need_bf16_copy=True)
     lib = sdc._lib
+    m = update(1, 2, 200, 300)   # small matrices need no workspace
     o = torch.empty_like(m)
-    need = lib.disco_orthogonalize_workspace(2, 8, 12)
+    need = lib.disco_orthogonalize_workspace(2, 200, 300)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    assert lib.disco_orthogonalize(m.data_ptr(), 0, o.data_ptr(), 0, 2, 8, 12, 5, None, 1e-7,
+    assert lib.disco_orthogonalize(m.data_ptr(), 0, o.data_ptr(), 0, 2, 200, 300, 5, None, 1e-7,
                                    ws.data_ptr(), need - 1, None) == sdc.DISCO_EINVAL
     assert "workspace" in lib.disco_last_error().decode()
