@@ -32,9 +32,11 @@ namespace {
 typedef _Float16 half_t;
 typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) halfx8 lds_halfx8;
+typedef __attribute__((address_space(3))) halfx4 lds_halfx4;
 
 // powers of two that X, A and P are stored times
 constexpr float kSX = 4096.0f, kSA = 4096.0f, kSP = 2048.0f;
@@ -58,13 +60,6 @@ struct Source {
     float beta;
     int nesterov;
 };
-
-template <typename T>
-__device__ __forceinline__ float source_at(const Source& s, int64_t i) {
-    if (s.buf == nullptr) return load_f(static_cast<const T*>(s.m), i);
-    if (!s.nesterov) return s.buf[i];
-    return load_f(static_cast<const T*>(s.m), i) + s.beta * s.buf[i];
-}
 
 // What becomes of the orthogonalised matrix.
 struct Sink {
@@ -106,40 +101,111 @@ __device__ __forceinline__ void sink_store(const Sink& s, I i, float o) {
     }
 }
 
+// Elements at .. at + 3 of a `total`-element tensor, at any element alignment;
+// what lies past the end reads as zero and is not written.
+__device__ __forceinline__ void load4(const float* p, int64_t at, int64_t total, float* v) {
+    struct __attribute__((packed, aligned(4))) U { float e[4]; };
+    if (at + 4 <= total) {
+        const U u = *reinterpret_cast<const U*>(p + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = u.e[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? p[at + e] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load4(const bf16_t* p, int64_t at, int64_t total, float* v) {
+    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
+    if (at + 4 <= total) {
+        const U u = *reinterpret_cast<const U*>(p + at);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            v[2 * e] = __uint_as_float(u.e[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u.e[e] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? bf16_to_f32(p[at + e]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store4(float* p, int64_t at, int64_t total, const float* v) {
+    struct __attribute__((packed, aligned(4))) U { float e[4]; };
+    if (at + 4 <= total) {
+        *reinterpret_cast<U*>(p + at) = U{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at + e < total) p[at + e] = v[e];
+    }
+}
+
+__device__ __forceinline__ void store4(bf16_t* p, int64_t at, int64_t total, const float* v) {
+    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
+    if (at + 4 <= total) {
+        U u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            u.e[e] = (uint32_t)f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16);
+        *reinterpret_cast<U*>(p + at) = u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at + e < total) store_f(p, at + e, v[e]);
+    }
+}
+
 // Advances the momentum (where there is one) and sums the squares of the
 // update in float64: no overflow for any float32 matrix.  partial[batch][gridDim.x].
 template <typename T>
-__global__ __launch_bounds__(256) void ns_norm(Source src, const float* buf_in,
-                                               float* buf_out, int64_t n,
-                                               double* __restrict__ partial) {
-    __shared__ double red[4];
+__global__ __launch_bounds__(1024) void ns_norm(Source src, const float* buf_in, float* buf_out,
+                                                int64_t n, double* __restrict__ partial) {
+    __shared__ double red[16];
     const int64_t base = (int64_t)blockIdx.y * n;
+    const T* m = static_cast<const T*>(src.m) + base;
+    const float* old = buf_out ? buf_in + base : nullptr;
+    float* fresh = buf_out ? buf_out + base : nullptr;
     double acc = 0.0;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v;
-        if (buf_out != nullptr) {
-            const float g = load_f(static_cast<const T*>(src.m), base + i);
-            const float b = src.beta * buf_in[base + i] + g;
-            buf_out[base + i] = b;
-            v = src.nesterov ? g + src.beta * b : b;
-        } else {
-            v = load_f(static_cast<const T*>(src.m), base + i);
+    constexpr int K = 4;
+    const int64_t stride = (int64_t)gridDim.x * 4096;
+    for (int64_t at0 = (int64_t)blockIdx.x * 4096 + 4 * threadIdx.x; at0 < n; at0 += K * stride) {
+        float v[K][4], o[K][4];
+#pragma unroll
+        for (int k = 0; k < K; ++k) load4(m, min(at0 + k * stride, n), n, v[k]);
+        if (fresh != nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) load4(old, min(at0 + k * stride, n), n, o[k]);
         }
-        acc += (double)v * (double)v;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (fresh != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[k][e] = src.beta * o[k][e] + v[k][e];
+                    v[k][e] = src.nesterov ? v[k][e] + src.beta * o[k][e] : o[k][e];
+                }
+                store4(fresh, min(at0 + k * stride, n), n, o[k]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc += (double)v[k][e] * (double)v[k][e];   // zero past the end
+        }
     }
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) acc += __shfl_xor(acc, m);
+    for (int k = 32; k > 0; k >>= 1) acc += __shfl_xor(acc, k);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
     __syncthreads();
-    if (threadIdx.x == 0)
-        partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+    if (threadIdx.x == 0) {
+        acc = 0.0;
+        for (int k = 0; k < 16; ++k) acc += red[k];
+        partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = acc;
+    }
 }
 
 // 1 / (|M|_F + eps) of this batch entry, on every thread of a 256-thread group.
 __device__ __forceinline__ double inv_norm(const double* partial, int nparts, float eps,
                                            double* red) {
-    double acc = 0.0;
-    for (int k = threadIdx.x; k < nparts; k += 256) acc += partial[k];
+    double acc = (int)threadIdx.x < nparts ? partial[threadIdx.x] : 0.0;
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) acc += __shfl_xor(acc, m);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
@@ -155,114 +221,346 @@ __global__ __launch_bounds__(256) void ns_load(Source src, const double* __restr
                                                int tall, half_t* __restrict__ X,
                                                half_t* __restrict__ XT, size_t xplane) {
     __shared__ double red[4];
-    __shared__ float tile[64][65];   // [i][j] of X
+    __shared__ float tile[64][65];   // rows and columns as in memory
     const int b = blockIdx.z;
-    const double inv = inv_norm(partial + (size_t)b * nparts, nparts, eps, red);
     const int64_t base = (int64_t)b * m * n;
     const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    const int lo = threadIdx.x & 63, hi = threadIdx.x >> 6;
-    for (int k = hi; k < 64; k += 4) {
-        const int i = tall ? lo : k, j = tall ? k : lo;
-        float v = 0.0f;
-        if (i0 + i < m && j0 + j < n) {
-            const int64_t at = tall ? (int64_t)(j0 + j) * m + i0 + i : (int64_t)(i0 + i) * n + j0 + j;
-            v = (float)((double)source_at<T>(src, base + at) * inv) * kSX;
+    // rows of `width` elements in memory; this tile starts at (r0, c0) of them
+    const int rows = tall ? n : m, width = tall ? m : n, r0 = tall ? j0 : i0, c0 = tall ? i0 : j0;
+    float v[4][4], g[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 16 * k + (threadIdx.x >> 4), c = c0 + 4 * (threadIdx.x & 15);
+        const int64_t row = base + (int64_t)min(r, rows - 1) * width;
+        const int len = r < rows ? width : 0;
+        if (src.buf != nullptr) {
+            load4(src.buf + row, min(c, len), len, v[k]);
+            if (src.nesterov) load4(static_cast<const T*>(src.m) + row, min(c, len), len, g[k]);
+        } else {
+            load4(static_cast<const T*>(src.m) + row, min(c, len), len, v[k]);
         }
-        tile[i][j] = v;
     }
+    const double inv = inv_norm(partial + (size_t)b * nparts, nparts, eps, red) * (double)kSX;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float f = v[k][e];
+            if (src.buf != nullptr && src.nesterov) f = g[k][e] + src.beta * f;
+            tile[16 * k + (threadIdx.x >> 4)][4 * (threadIdx.x & 15) + e] = (float)((double)f * inv);
+        }
     __syncthreads();
-    half_t* x = X + (size_t)b * 2 * xplane;
-    half_t* xt = XT + (size_t)b * 2 * xplane;
-    for (int k = hi; k < 64; k += 4) {
-        const Pair p = split(tile[k][lo]);
-        const size_t at = (size_t)(i0 + k) * np + j0 + lo;
-        x[at] = p.h;
-        x[xplane + at] = p.l;
-        const Pair q = split(tile[lo][k]);
-        const size_t att = (size_t)(j0 + k) * mp + i0 + lo;
-        xt[att] = q.h;
-        xt[xplane + att] = q.l;
+    // eight neighbours a thread, along the rows in memory and across them
+    half_t* along = (tall ? XT : X) + (size_t)b * 2 * xplane;
+    half_t* across = (tall ? X : XT) + (size_t)b * 2 * xplane;
+    const int ld_along = tall ? mp : np, ld_across = tall ? np : mp;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = 32 * k + (threadIdx.x >> 3), c = 8 * (threadIdx.x & 7);
+        halfx8 h, l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const Pair p = split(tile[r][c + e]);
+            h[e] = p.h;
+            l[e] = p.l;
+        }
+        half_t* q = along + (size_t)(r0 + r) * ld_along + c0 + c;
+        *reinterpret_cast<halfx8*>(q) = h;
+        *reinterpret_cast<halfx8*>(q + xplane) = l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const Pair p = split(tile[c + e][r]);
+            h[e] = p.h;
+            l[e] = p.l;
+        }
+        q = across + (size_t)(c0 + r) * ld_across + r0 + c;
+        *reinterpret_cast<halfx8*>(q) = h;
+        *reinterpret_cast<halfx8*>(q + xplane) = l;
     }
 }
 
 enum Epilogue { kGram, kPoly, kStep, kLast };
 
 // One product of the iteration, U V^T with both operands [rows][K], as hi and
-// lo planes.
+// lo planes.  Row counts and K are multiples of 64.
 struct Product {
     const half_t *u, *v;      // hi planes of batch entry 0; lo planes at + plane
     size_t u_plane, v_plane;  // elements of a plane; a batch entry has two
-    int K;                    // summed length, a multiple of 64; also the row stride
-    int tiles_j;              // tiles along j (kStep, kLast)
+    int K;                    // summed length, also the row stride of u and v
+    int rows_u, rows_v;
+    int tiles_i, tiles_j;     // tiles along i and j
+    int splits;               // workgroups that share a tile's sum
+    float* part;              // [batch][tile][split][BM * BN] where splits > 1
     // results and other operands
     half_t *out, *out_t;      // [i][j] and [j][i] (hi, lo); kGram / kPoly: one symmetric matrix
-    const half_t* add;        // kPoly: A; kStep, kLast: X^T as [j][i]
+    const half_t* add;        // kPoly: A; kStep: X^T as [j][i], or NULL
     size_t o_plane, add_plane;
     int ld_out, ld_t;         // row strides of out and out_t (and add)
     int lo_out, lo_t;         // whether the lo planes of out, out_t are wanted
     float ca, cb;             // factors of `add` and of the accumulated product
+    float diagonal;           // added where i == j (kPoly)
     int m, n, tall;           // kLast: true sizes and orientation
     Sink sink;
 };
 
-// BM x BN tile of a product, WM x WN waves, NS stages of 64-deep slices in LDS.
-// Slices arrive by direct-to-LDS loads; 16-byte slot s of a 128-byte row r
-// holds chunk s ^ (r & 7), so the 16-byte fragment reads of eight neighbouring
-// rows fall on distinct banks.
-template <int BM, int BN, int WM, int WN, int NP, int NS, Epilogue E>
-__global__ __launch_bounds__(64 * WM * WN) void ns_product(Product p) {
+// A wave's TM x TN block of 32 x 32 tiles, one plane, between the matrix core's
+// layout and rows in memory, through the wave's own piece of LDS at `at`.  One
+// wave's LDS accesses are carried out in order; the fences keep the compiler
+// from reordering them.
+template <int TM, int TN>
+struct BlockIO {
+    static constexpr int ROW_T = TM * 64 + 16, ROW = TN * 64 + 16;   // bytes of a padded row
+    static constexpr int BYTES = TN * 32 * ROW_T > TM * 32 * ROW ? TN * 32 * ROW_T : TM * 32 * ROW;
+
+    // 16-byte pieces of R rows of 8 C elements, row r at g + r * ld
+    template <int R, int C, bool LOAD>
+    static __device__ __forceinline__ void move(half_t* g, size_t ld, int rows, int cols,
+                                                uint32_t at, int row_bytes, int lane) {
+#pragma unroll 4
+        for (int it = 0; it < (R * C + 63) / 64; ++it) {
+            const int idx = it * 64 + lane, r = idx / C, c = idx % C;
+            if ((R * C % 64 == 0 || idx < R * C) && r < rows && 8 * c < cols) {
+                half_t* q = g + (size_t)r * ld + 8 * c;
+                lds_halfx8* l = (lds_halfx8*)(uintptr_t)(at + (uint32_t)(r * row_bytes + 16 * c));
+                if constexpr (LOAD) *l = *reinterpret_cast<const halfx8*>(q);
+                else *reinterpret_cast<halfx8*>(q) = *l;
+            }
+        }
+    }
+
+    // where rows 8 q + 4 lg .. + 3 of tile row a, column l32 of tile column c lie
+    static __device__ __forceinline__ uint32_t cell_t(uint32_t at, int a, int c, int q, int lane) {
+        return at + (uint32_t)((c * 32 + (lane & 31)) * ROW_T + 2 * (a * 32 + 8 * q + 4 * (lane >> 5)));
+    }
+};
+
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// What becomes of a wave's block of sums whose first row and column are ib and jb.
+template <int TM, int TN, Epilogue E>
+__device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN], int b, int ib, int jb,
+                                       bool off_diagonal, uint32_t piece, int lane) {
+    using IO = BlockIO<TM, TN>;
+    const int l32 = lane & 31, lg = lane >> 5;
+    // lane: column j = lane % 32, rows i = 8 (e / 4) + 4 (lane / 32) + e % 4
+    const int rows_i = p.rows_u - ib, rows_j = p.rows_v - jb;   // of it inside the matrix
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+        for (int c = 0; c < TN; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[a][c][e] *= p.cb;
+    if constexpr (E == kPoly || E == kStep) {
+        if (p.add != nullptr) {
+            half_t* add = const_cast<half_t*>(p.add) + (size_t)b * 2 * p.add_plane + (size_t)jb * p.ld_t + ib;
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl) {
+                IO::template move<TN * 32, TM * 4, true>(add + (size_t)pl * p.add_plane, p.ld_t, rows_j,
+                                                         rows_i, piece, IO::ROW_T, lane);
+                wave_fence();
+#pragma unroll
+                for (int a = 0; a < TM; ++a)
+#pragma unroll
+                    for (int c = 0; c < TN; ++c)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const halfx4 x = *(const lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[a][c][4 * q + e] += p.ca * (float)x[e];
+                        }
+                wave_fence();
+            }
+        }
+    }
+    if constexpr (E == kPoly) {
+        if (p.diagonal != 0.0f)
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int c = 0; c < TN; ++c)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (ib + 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3) == jb + 32 * c + l32)
+                            acc[a][c][e] += p.diagonal;
+    }
+    if constexpr (E == kLast) {
+        const int64_t at0 = (int64_t)b * p.m * p.n;
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int c = 0; c < TN; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = ib + 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3), j = jb + 32 * c + l32;
+                    if (i < p.m && j < p.n)
+                        sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i : (int64_t)i * p.n + j),
+                                   acc[a][c][e]);
+                }
+    } else {
+        half_t* out = p.out + (size_t)b * 2 * p.o_plane + (size_t)ib * p.ld_out + jb;
+        half_t* out_t = p.out_t + (size_t)b * 2 * p.o_plane + (size_t)jb * p.ld_t + ib;
+        // a symmetric result's diagonal tiles are whole already
+        const bool both = E == kStep || off_diagonal;
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl) {
+            if (pl == 1 && !p.lo_t && !p.lo_out) break;
+            if (pl == 0 || p.lo_t) {
+#pragma unroll
+                for (int a = 0; a < TM; ++a)
+#pragma unroll
+                    for (int c = 0; c < TN; ++c)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            halfx4 h;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const Pair s = split(acc[a][c][4 * q + e]);
+                                h[e] = pl ? s.l : s.h;
+                            }
+                            *(lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane) = h;
+                        }
+                wave_fence();
+                IO::template move<TN * 32, TM * 4, false>(out_t + (size_t)pl * p.o_plane, p.ld_t, rows_j,
+                                                          rows_i, piece, IO::ROW_T, lane);
+                wave_fence();
+            }
+            if (both && (pl == 0 || p.lo_out)) {
+                typedef __attribute__((address_space(3))) half_t lds_half;
+#pragma unroll
+                for (int a = 0; a < TM; ++a)
+#pragma unroll
+                    for (int c = 0; c < TN; ++c)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const Pair s = split(acc[a][c][e]);
+                            const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
+                            *(lds_half*)(uintptr_t)(piece + (uint32_t)(i * IO::ROW + 2 * (32 * c + l32))) =
+                                pl ? s.l : s.h;
+                        }
+                wave_fence();
+                IO::template move<TM * 32, TN * 4, false>(out + (size_t)pl * p.o_plane, p.ld_out, rows_i,
+                                                          rows_j, piece, IO::ROW, lane);
+                wave_fence();
+            }
+        }
+    }
+}
+
+// Workgroups go to the eight dies in turn; this gives each die a run of
+// neighbouring numbers, so that the tiles it holds share operands in its L2.
+__device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t total) {
+    const uint32_t die = id & 7, q = total >> 3, r = total & 7;
+    return die * q + min(die, r) + (id >> 3);
+}
+
+// Tile number -> tile row and column, by bands of kBand tile rows, column by
+// column within a band, so that neighbouring numbers form squares: with
+// die_order the products of 4096 x 4096 fetch a quarter less time (a die's 64
+// tiles of 128 read 16 row panels instead of up to 34).  Symmetric results have
+// the lower triangle only.
+constexpr int kBand = 8;
+
+template <Epilogue E>
+__device__ __forceinline__ void tile_of(int tile, int tiles_i, int tiles_j, int& ti, int& tj) {
+    if constexpr (E == kGram || E == kPoly) {
+        int row = (int)((sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
+        while ((row + 1) * (row + 2) / 2 <= tile) ++row;
+        while (row * (row + 1) / 2 > tile) --row;
+        const int first = row / kBand * kBand, rows = min(kBand, tiles_i - first);
+        int rest = tile - first * (first + 1) / 2;
+        if (rest < (first + 1) * rows) {   // columns that cross the whole band
+            tj = rest / rows;
+            ti = first + rest - tj * rows;
+            return;
+        }
+        rest -= (first + 1) * rows;
+        tj = first + 1;
+        int height = rows - 1;
+        while (rest >= height) {
+            rest -= height;
+            ++tj;
+            --height;
+        }
+        ti = tj + rest;
+    } else {
+        const int band = tile / (kBand * tiles_j), first = band * kBand;
+        const int rows = min(kBand, tiles_i - first), rest = tile - first * tiles_j;
+        tj = rest / rows;
+        ti = first + rest - tj * rows;
+    }
+}
+
+// BM x BN tile of a product, WM x WN waves, NS stages of BK-deep slices in LDS.
+// Slices arrive by direct-to-LDS loads, 1 KB each.  A row of a slice is CH = BK / 8
+// chunks of 16 bytes, and its slot s holds chunk s ^ (r / (16 / CH)) % CH: the
+// 16-byte fragment reads of 16 neighbouring rows fall on all 64 banks once.
+// Fragments are read one 16-deep step ahead of the products that use them, and
+// the barrier between two slices stands before the last step's products, so
+// that they cover the first reads of the next slice.
+//
+// `splits` workgroups may share a tile along K: each leaves its sum in `part` for
+// ns_join.  (The last of them could add the parts itself, but the fence that
+// makes them visible writes back a die's whole L2: 65 us against 24 with the
+// second launch at 1024 x 4096.)
+template <int BM, int BN, int WM, int WN, int NP, int BK, int NS, Epilogue E>
+__global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * (NP == 3 ? 2 : 1) * 2 * BK > 81920 ? 1 : 2) void ns_product(
+    Product p) {
     constexpr int W = WM * WN;
     constexpr int PL = NP == 3 ? 2 : 1;                      // planes of an operand
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    constexpr int UNITS = (BM + BN) * PL / 8, OPS = UNITS / W;
-    constexpr int STAGE = (BM + BN) * PL * 128;
-    static_assert(UNITS % W == 0, "whole loads per wave");
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE];
+    constexpr int CH = BK / 8, RPU = 64 / CH;                // chunks a row, rows a load
+    constexpr int ROWB = 2 * BK, KS = BK / 16;
+    constexpr int UNITS = (BM + BN) * PL / RPU, OPS = UNITS / W;
+    constexpr int STAGE = (BM + BN) * PL * ROWB;
+    using IO = BlockIO<TM, TN>;
+    constexpr int PIECE = (IO::BYTES + 15) / 16 * 16;
+    static_assert(UNITS % W == 0 && BM % RPU == 0 && BN % RPU == 0, "whole loads per wave");
+    static_assert(TM * WM * 32 == BM && TN * WN * 32 == BN, "whole tiles per wave");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE > W * PIECE ? NS * STAGE : W * PIECE];
 
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
-    const int b = blockIdx.y;
+    const uint32_t id = die_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+    const int b = (int)(id / gridDim.x), shared = (int)(id - b * gridDim.x);
+    const int tile = shared / p.splits, part = shared - tile * p.splits;
     int ti, tj;
-    if constexpr (E == kGram || E == kPoly) {
-        // lower triangle, row by row
-        const int t = blockIdx.x;
-        ti = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
-        while (ti * (ti + 1) / 2 > t) --ti;
-        tj = t - ti * (ti + 1) / 2;
-    } else {
-        ti = blockIdx.x / p.tiles_j;
-        tj = blockIdx.x % p.tiles_j;
-    }
+    tile_of<E>(tile, p.tiles_i, p.tiles_j, ti, tj);
     const int i0 = ti * BM, j0 = tj * BN;
     const half_t* u = p.u + (size_t)b * 2 * p.u_plane;
     const half_t* v = p.v + (size_t)b * 2 * p.v_plane;
+
+    // this workgroup's slices
+    const int nk_all = p.K / BK;
+    const int k_lo = (int)((int64_t)nk_all * part / p.splits);
+    const int nk = (int)((int64_t)nk_all * (part + 1) / p.splits) - k_lo;
 
     const half_t* src[OPS];
 #pragma unroll
     for (int o = 0; o < OPS; ++o) {
         const int unit = o * W + wave;
-        const int plane_units_u = BM / 8, plane_units_v = BN / 8;
+        constexpr int UU = BM / RPU, UV = BN / RPU;
         const half_t* q;
-        int row;
-        if (unit < PL * plane_units_u) {
-            const int pl = unit / plane_units_u;
-            row = i0 + (unit - pl * plane_units_u) * 8;
-            q = u + (size_t)pl * p.u_plane;
+        int row;   // within the tile; rows past the matrix repeat its last one
+        if (unit < PL * UU) {
+            const int pl = unit / UU;
+            row = (unit - pl * UU) * RPU + lane / CH;
+            q = u + (size_t)pl * p.u_plane + (size_t)min(i0 + row, p.rows_u - 1) * p.K;
         } else {
-            const int uv = unit - PL * plane_units_u, pl = uv / plane_units_v;
-            row = j0 + (uv - pl * plane_units_v) * 8;
-            q = v + (size_t)pl * p.v_plane;
+            const int pl = (unit - PL * UU) / UV;
+            row = (unit - PL * UU - pl * UV) * RPU + lane / CH;
+            q = v + (size_t)pl * p.v_plane + (size_t)min(j0 + row, p.rows_v - 1) * p.K;
         }
-        src[o] = q + (size_t)(row + (lane >> 3)) * p.K + 8 * ((lane & 7) ^ (lane >> 3));
+        src[o] = q + 8 * ((lane % CH) ^ ((row / (16 / CH)) % CH)) + (size_t)k_lo * BK;
     }
     const uint32_t ring_at = (uint32_t)(uintptr_t)(lds_u8*)&ring[0];
-    const int nk = p.K / 64;
+    // load o of slice k
+    auto issue_one = [&](int k, int o) {
+        dma_lds16(src[o] + (size_t)k * BK,
+                  ring_at + (uint32_t)((k % NS) * STAGE) + (uint32_t)((o * W + wave) * 1024));
+    };
     auto issue = [&](int k) {
-        const uint32_t st = ring_at + (uint32_t)((k % NS) * STAGE);
 #pragma unroll
-        for (int o = 0; o < OPS; ++o)
-            dma_lds16(src[o] + (size_t)k * 64, st + (uint32_t)((o * W + wave) * 1024));
+        for (int o = 0; o < OPS; ++o) issue_one(k, o);
     };
 
     floatx16 acc[TM][TN];
@@ -275,101 +573,131 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_product(Product p) {
 
     const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, lg = lane >> 5;
     const lds_u8* base = (const lds_u8*)&ring[0];
-    const uint32_t row_u = (uint32_t)((wm * TM * 32 + l32) * 128);
-    const uint32_t row_v = (uint32_t)(BM * PL * 128 + (wn * TN * 32 + l32) * 128);
-
-    const int pre = min(NS - 1, nk);
-    for (int k = 0; k < pre; ++k) issue(k);
-    for (int k = 0; k < nk; ++k) {
-        // slice k has landed when at most the later slices' loads are out
-        if (k + NS - 1 <= nk) wait_vmcnt<OPS*(NS - 2)>();
-        else wait_vmcnt<0>();
-        __syncthreads();
-        if (k + NS - 1 < nk) issue(k + NS - 1);   // into the stage read at slice k - 1
+    const uint32_t row_u = (uint32_t)((wm * TM * 32 + l32) * ROWB);
+    const uint32_t row_v = (uint32_t)(BM * PL * ROWB + (wn * TN * 32 + l32) * ROWB);
+    halfx8 fu[2][TM][PL], fv[2][TN][PL];
+    auto fetch = [&](int set, int k, int ks) {
         const lds_u8* st = base + (k % NS) * STAGE;
+        // the tiles' rows differ by multiples of 32: one swizzle for all
+        const uint32_t ch = (uint32_t)(16 * ((2 * ks + lg) ^ ((l32 / (16 / CH)) % CH)));
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t ch = (uint32_t)(16 * ((2 * ks + lg) ^ (l32 & 7)));
-            halfx8 fu[TM][PL], fv[TN][PL];
+        for (int a = 0; a < TM; ++a)
 #pragma unroll
-            for (int a = 0; a < TM; ++a)
+            for (int q = 0; q < PL; ++q)
+                fu[set][a][q] = *(const lds_halfx8*)(st + row_u + ch + (q * BM + a * 32) * ROWB);
 #pragma unroll
-                for (int q = 0; q < PL; ++q)
-                    fu[a][q] = *(const lds_halfx8*)(st + row_u + ch + q * BM * 128 + a * 4096);
+        for (int c = 0; c < TN; ++c)
 #pragma unroll
-            for (int c = 0; c < TN; ++c)
+            for (int q = 0; q < PL; ++q)
+                fv[set][c][q] = *(const lds_halfx8*)(st + row_v + ch + (q * BN + c * 32) * ROWB);
+    };
+    // One 16-deep step's products.  The next slice's loads go out between them,
+    // evenly over the slice: issued in a row they hold up the wave, and with it
+    // the matrix core, for as long as the products take.
+    constexpr int PRODUCTS = TM * TN * NP;   // of one step
+    // two stages: before the last step, which waits for them
+    constexpr int SPREAD = PRODUCTS * (NS == 2 ? KS - 1 : KS);
+    auto multiply = [&](int set, int ks, int load_k, bool load) {
+        int n = ks * PRODUCTS;   // products of the slice so far
 #pragma unroll
-                for (int q = 0; q < PL; ++q)
-                    fv[c][q] = *(const lds_halfx8*)(st + row_v + ch + q * BN * 128 + c * 4096);
+        for (int part = NP == 3 ? 0 : 2; part < 3; ++part)   // lo hi, hi lo, hi hi
 #pragma unroll
             for (int a = 0; a < TM; ++a)
 #pragma unroll
                 for (int c = 0; c < TN; ++c) {
-                    if constexpr (NP == 3) {
-                        acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fu[a][1], fv[c][0],
-                                                                          acc[a][c], 0, 0, 0);
-                        acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fu[a][0], fv[c][1],
-                                                                          acc[a][c], 0, 0, 0);
+                    acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        fu[set][a][part == 0 ? PL - 1 : 0], fv[set][c][part == 1 ? PL - 1 : 0], acc[a][c],
+                        0, 0, 0);
+                    const int o0 = min(n * OPS / SPREAD, OPS), o1 = min((n + 1) * OPS / SPREAD, OPS);
+                    ++n;
+                    if (load && o1 > o0) {
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int o = o0; o < o1; ++o) issue_one(load_k, o);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fu[a][0], fv[c][0],
-                                                                      acc[a][c], 0, 0, 0);
                 }
+    };
+
+    const int ahead = min(NS - 1, nk);
+    for (int k = 0; k < ahead; ++k) issue(k);
+    // slice k has landed when at most the loads of the NS - 2 after it are out
+    if (ahead == NS - 1) wait_vmcnt<OPS*(NS - 2)>();
+    else wait_vmcnt<0>();
+    __syncthreads();
+    fetch(0, 0, 0);
+    for (int k = 0; k < nk; ++k) {
+        const bool more = k + 1 < nk;
+        const bool issued = k + NS - 1 < nk;   // into the stage that everyone has left
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS) {
+                fetch((ks + 1) & 1, k, ks + 1);
+            } else if (more) {
+                // the loads of this slice's products so far are the youngest
+                if (issued) wait_vmcnt<NS == 2 ? 0 : OPS*(NS - 3) + OPS*(KS - 1) / KS>();
+                else wait_vmcnt<0>();
+                __syncthreads();
+                fetch(KS & 1, k + 1, 0);
+            }
+            multiply(ks & 1, ks, k + NS - 1, issued);
         }
+        static_assert(KS % 2 == 0, "the next slice starts on set 0");
     }
 
-    // lane: column j = lane % 32, rows i = 8 (e / 4) + 4 (lane / 32) + e % 4
-    half_t* out = p.out + (size_t)b * 2 * p.o_plane;
-    half_t* out_t = p.out_t + (size_t)b * 2 * p.o_plane;
-    const half_t* add = p.add + (size_t)b * 2 * p.add_plane;
+    if (p.splits > 1) {
+        // in the accumulators' own order: every access is whole
+        float* mine = p.part + ((size_t)b * gridDim.x + shared) * (BM * BN);
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int c = 0; c < TN; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    reinterpret_cast<floatx4*>(mine)[((wave * TM + a) * TN + c) * 256 + q * 64 + lane] =
+                        floatx4{acc[a][c][4 * q], acc[a][c][4 * q + 1], acc[a][c][4 * q + 2],
+                                acc[a][c][4 * q + 3]};
+        return;
+    }
+    __syncthreads();   // the ring is free
+    finish<TM, TN, E>(p, acc, b, i0 + wm * TM * 32, j0 + wn * TN * 32, ti != tj,
+                      ring_at + (uint32_t)(wave * PIECE), lane);
+}
+
+// Adds the parts of a tile that `splits` workgroups computed, in order, and
+// finishes it: a wave for each wave's block of the tile.
+template <int BM, int BN, int WM, int WN, Epilogue E>
+__global__ __launch_bounds__(64) void ns_join(Product p) {
+    constexpr int W = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[(BlockIO<TM, TN>::BYTES + 15) / 16 * 16];
+    const int lane = threadIdx.x, b = blockIdx.y;
+    const int tile = blockIdx.x / W, wave = blockIdx.x - tile * W;
+    int ti, tj;
+    tile_of<E>(tile, p.tiles_i, p.tiles_j, ti, tj);
+    const size_t first = ((size_t)b * (gridDim.x / W) + tile) * p.splits;
+    floatx16 acc[TM][TN];
 #pragma unroll
     for (int a = 0; a < TM; ++a)
 #pragma unroll
         for (int c = 0; c < TN; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int i = i0 + (wm * TM + a) * 32 + 8 * q + 4 * lg;
-                const int j = j0 + (wn * TN + c) * 32 + l32;
-                const size_t at_t = (size_t)j * p.ld_t + i;
-                float f[4];
+            for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.0f;
+    for (int t = 0; t < p.splits; ++t) {
+        const floatx4* from = reinterpret_cast<const floatx4*>(p.part + (first + t) * (BM * BN));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = p.cb * acc[a][c][4 * q + e];
-                if constexpr (E != kGram) {
-                    const halfx4 xh = *reinterpret_cast<const halfx4*>(add + at_t);
-                    const halfx4 xl = *reinterpret_cast<const halfx4*>(add + p.add_plane + at_t);
+        for (int a = 0; a < TM; ++a)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] += p.ca * ((float)xh[e] + (float)xl[e]);
+            for (int c = 0; c < TN; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const floatx4 f = from[((wave * TM + a) * TN + c) * 256 + q * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[a][c][4 * q + e] += f[e];
                 }
-                if constexpr (E == kLast) {
-                    if (j < p.n) {
-                        const int64_t at0 = (int64_t)b * p.m * p.n;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i + e < p.m)
-                                sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i + e
-                                                                : (int64_t)(i + e) * p.n + j),
-                                           f[e]);
-                    }
-                } else {
-                    halfx4 h, l;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const Pair s = split(f[e]);
-                        h[e] = s.h;
-                        l[e] = s.l;
-                    }
-                    *reinterpret_cast<halfx4*>(out_t + at_t) = h;
-                    if (p.lo_t) *reinterpret_cast<halfx4*>(out_t + p.o_plane + at_t) = l;
-                    // a symmetric result's diagonal tiles are whole already
-                    if ((E == kStep) || ti != tj) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const size_t at = (size_t)(i + e) * p.ld_out + j;
-                            out[at] = h[e];
-                            if (p.lo_out) out[p.o_plane + at] = l[e];
-                        }
-                    }
-                }
-            }
+    }
+    const int wm = wave / WN, wn = wave % WN;
+    finish<TM, TN, E>(p, acc, b, ti * BM + wm * TM * 32, tj * BN + wn * TN * 32, ti != tj,
+                      (uint32_t)(uintptr_t)(lds_u8*)&lds[0], lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -384,7 +712,6 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_product(Product p) {
 // (transposing reads), the waves' partial sums meet in LDS, and A and P live
 // there too.  Always three products: a step is a few hundred matrix
 // instructions and the barriers and LDS round trips around them cost as much.
-typedef __attribute__((address_space(3))) halfx4 lds_halfx4;
 typedef int16_t v4i16_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16_t lds_v4i16;
 
@@ -404,61 +731,6 @@ __device__ __forceinline__ halfx8 read_turned(uint32_t at, int stride, int lane)
     const v4i16_t hi =
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(p + 4 * stride));
     return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-// Elements at .. at + 3 of a `total`-element tensor, at any element alignment;
-// what lies past the end reads as zero and is not written.
-__device__ __forceinline__ void load4(const float* p, int at, int total, float* v) {
-    struct __attribute__((packed, aligned(4))) U { float e[4]; };
-    if (at + 4 <= total) {
-        const U u = *reinterpret_cast<const U*>(p + at);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = u.e[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? p[at + e] : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void load4(const bf16_t* p, int at, int total, float* v) {
-    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
-    if (at + 4 <= total) {
-        const U u = *reinterpret_cast<const U*>(p + at);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            v[2 * e] = __uint_as_float(u.e[e] << 16);
-            v[2 * e + 1] = __uint_as_float(u.e[e] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = at + e < total ? bf16_to_f32(p[at + e]) : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void store4(float* p, int at, int total, const float* v) {
-    struct __attribute__((packed, aligned(4))) U { float e[4]; };
-    if (at + 4 <= total) {
-        *reinterpret_cast<U*>(p + at) = U{{v[0], v[1], v[2], v[3]}};
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (at + e < total) p[at + e] = v[e];
-    }
-}
-
-__device__ __forceinline__ void store4(bf16_t* p, int at, int total, const float* v) {
-    struct __attribute__((packed, aligned(2))) U { uint32_t e[2]; };
-    if (at + 4 <= total) {
-        U u;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            u.e[e] = (uint32_t)f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16);
-        *reinterpret_cast<U*>(p + at) = u;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (at + e < total) store_f(p, at + e, v[e]);
-    }
 }
 
 template <int MT>
@@ -598,7 +870,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
                 }
             // one wave's LDS accesses are carried out in order; the fence keeps
             // the compiler from moving the reads up
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            wave_fence();
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc) {
                 halfx8 fh[MT], fl[MT];
@@ -614,9 +886,8 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
 #pragma unroll
                     for (int b = 0; b <= a; ++b, ++k) g[k] = mfma3(fh[a], fl[a], fh[b], fl[b], g[k]);
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            wave_fence();
         }
-        typedef float floatx4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) floatx4 lds_floatx4;
 #pragma unroll
         for (int k = 0; k < C::NT; ++k)
@@ -801,11 +1072,58 @@ SmallShape small_shape(int m, int n) {
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+int done(const char* what) {
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return set_error(DISCO_EHIP, "%s launch failed: %s", what, hipGetErrorString(e));
+    return DISCO_OK;
+}
+
+// Tile of a product: kinds 0 and 1 are 64 x 64 with a deep ring (one workgroup a
+// compute unit) and with a shallow one (two), 2 is 128 x 128, 3 is 192 x 192;
+// `splits` workgroups share a tile along K.
+struct TileChoice {
+    int kind = 0, splits = 1;
+};
+
+constexpr int kSides[4] = {64, 64, 128, 192};
+
+// The choice with the least estimated time.  Times in microseconds as measured
+// from 128 x 896 to 4096 x 4096: a 64-deep slice of one tile with single and
+// with three products, and a tile's start and end.  For instance 1024 x 4096 in
+// float32: X X^T on 136 tiles of 64 takes 29 us, on 36 of 128 71 us, on 64-tiles
+// shared by four 24 us and 2 us for their joining; P X on 512 tiles of 64 takes
+// 42 us, on 256 of 128 30 us.
+TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric, int np) {
+    static const double slice_us[4][2] = {{0.22, 0.39}, {0.30, 0.65}, {0.45, 1.1}, {1.0, 2.5}};
+    static const double ends_us[4] = {2.0, 2.0, 4.0, 8.0};
+    TileChoice best;
+    double best_us = 1e300;
+    for (int kind = 0; kind < 4; ++kind) {
+        const int64_t side = kSides[kind];
+        const int64_t ti = (ni + side - 1) / side, tj = (nj + side - 1) / side;
+        const int64_t tiles = batch * (symmetric ? ti * (ti + 1) / 2 : ti * tj);
+        const int64_t at_once = kind == 1 ? 512 : 256;
+        for (int splits : {1, 2, 4, 8, 16}) {
+            if (splits > 1 && (!can_split || kind == 3 || K / 64 < 4 * splits || tiles * splits > 2048)) break;
+            const int64_t rounds = (tiles * splits + at_once - 1) / at_once;
+            double us = rounds * (K / 64.0 / splits * slice_us[kind][np == 3] + ends_us[kind]);
+            if (splits > 1) us += 4.0 + 0.2 * splits * side / 64;
+            if (us < best_us) {
+                best_us = us;
+                best.kind = kind;
+                best.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 // Where everything of a call lies in its workspace.
 struct Layout {
     int m, n, mp, np, tall, nparts;
     size_t xplane, aplane;                 // elements of one plane
-    size_t partial, X, XT0, XT1, A, P;     // byte offsets
+    size_t partial, X, XT0, XT1, A, P, part;     // byte offsets
     size_t bytes;
 };
 
@@ -817,7 +1135,7 @@ Layout layout(int batch, int rows, int cols) {
     l.mp = (int)up(l.m, 64);
     l.np = (int)up(l.n, 64);
     const int64_t elems = (int64_t)rows * cols;
-    l.nparts = (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / 4096));
+    l.nparts = (int)std::max<int64_t>(1, std::min<int64_t>(256, elems / 16384));   // ns_load adds 256
     l.xplane = (size_t)l.mp * l.np;
     l.aplane = (size_t)l.mp * l.mp;
     size_t at = 0;
@@ -832,29 +1150,60 @@ Layout layout(int batch, int rows, int cols) {
     l.XT1 = take((size_t)batch * 2 * l.xplane * sizeof(half_t));
     l.A = take((size_t)batch * 2 * l.aplane * sizeof(half_t));
     l.P = take((size_t)batch * 2 * l.aplane * sizeof(half_t));
+    // the parts of X X^T where workgroups share its tiles
+    size_t part = 0;
+    for (int np : {1, 3}) {
+        const TileChoice t = choose_tile(batch, l.mp, l.mp, l.np, true, true, np);
+        const size_t side = kSides[t.kind], ti = (l.mp + side - 1) / side;
+        if (t.splits > 1)
+            part = std::max(part, (size_t)batch * (ti * (ti + 1) / 2) * t.splits * side * side * sizeof(float));
+    }
+    l.part = take(part);
     l.bytes = at;
     return l;
 }
 
-int done(const char* what) {
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return set_error(DISCO_EHIP, "%s launch failed: %s", what, hipGetErrorString(e));
+template <int SIDE, int WM, int WN, int NP, int BK, int NS, Epilogue E>
+int launch_tiles(Product p, int splits, int batch, hipStream_t st) {
+    constexpr const char* names[] = {"ns_gram", "ns_poly", "ns_step", "ns_last"};
+    const int64_t ti = (p.rows_u + SIDE - 1) / SIDE, tj = (p.rows_v + SIDE - 1) / SIDE;
+    const int64_t tiles = E == kGram || E == kPoly ? ti * (ti + 1) / 2 : ti * tj;
+    if (tiles * splits * batch > 0x7fffffff / 8) return set_error(DISCO_EUNSUPPORTED, "matrix too large");
+    p.tiles_i = (int)ti;
+    p.tiles_j = (int)tj;
+    p.splits = splits;
+    {
+        KernelTimer timer(names[E], st);
+        hipLaunchKernelGGL((ns_product<SIDE, SIDE, WM, WN, NP, BK, NS, E>), dim3((unsigned)(tiles * splits), batch),
+                           dim3(64 * WM * WN), 0, st, p);
+    }
+    if (int rc = done(names[E])) return rc;
+    if constexpr (E == kGram && SIDE < 192) {
+        if (splits > 1) {
+            KernelTimer timer("ns_join", st);
+            hipLaunchKernelGGL((ns_join<SIDE, SIDE, WM, WN, E>), dim3((unsigned)(tiles * WM * WN), batch),
+                               dim3(64), 0, st, p);
+            return done("ns_join");
+        }
+    }
     return DISCO_OK;
 }
 
 template <int NP, Epilogue E>
-int launch_product(const Product& p, int tiles, int batch, hipStream_t st) {
-    constexpr const char* names[] = {"ns_gram", "ns_poly", "ns_step", "ns_last"};
-    KernelTimer timer(names[E], st);
-    hipLaunchKernelGGL((ns_product<64, 64, 2, 2, NP, 2, E>), dim3((unsigned)tiles, batch), dim3(256),
-                       0, st, p);
-    return done(names[E]);
+int launch_product(const Product& p, int batch, hipStream_t st) {
+    const TileChoice t = choose_tile(batch, p.rows_u, p.rows_v, p.K, E == kGram, E == kGram || E == kPoly, NP);
+    // rings of 128, 64, 128 and 144 KB (96 KB for single products of 192)
+    switch (t.kind) {
+        case 0: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 4 : 8, E>(p, t.splits, batch, st);
+        case 1: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 2 : 4, E>(p, t.splits, batch, st);
+        case 2: return launch_tiles<128, 2, 2, NP, NP == 3 ? 32 : 64, 4, E>(p, t.splits, batch, st);
+        default: return launch_tiles<192, 2, 2, NP, NP == 3 ? 32 : 64, NP == 3 ? 3 : 2, E>(p, t.splits, batch, st);
+    }
 }
 
 template <Epilogue E>
-int launch_product(bool three, const Product& p, int tiles, int batch, hipStream_t st) {
-    return three ? launch_product<3, E>(p, tiles, batch, st) : launch_product<1, E>(p, tiles, batch, st);
+int launch_product(bool three, const Product& p, int batch, hipStream_t st) {
+    return three ? launch_product<3, E>(p, batch, st) : launch_product<1, E>(p, batch, st);
 }
 
 }  // namespace
@@ -931,10 +1280,10 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
         const dim3 grid(l.nparts, c.batch);
         const int64_t n = (int64_t)c.rows * c.cols;
         if (c.m_dtype == DISCO_F32)
-            hipLaunchKernelGGL(ns_norm<float>, grid, dim3(256), 0, st, src, c.momentum,
+            hipLaunchKernelGGL(ns_norm<float>, grid, dim3(1024), 0, st, src, c.momentum,
                                c.momentum_out, n, partial);
         else
-            hipLaunchKernelGGL(ns_norm<bf16_t>, grid, dim3(256), 0, st, src, c.momentum,
+            hipLaunchKernelGGL(ns_norm<bf16_t>, grid, dim3(1024), 0, st, src, c.momentum,
                                c.momentum_out, n, partial);
         if (int rc = done("ns_norm")) return rc;
     }
@@ -949,31 +1298,32 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
                                c.eps, l.m, l.n, l.mp, l.np, l.tall, X, XT[0], l.xplane);
         if (int rc = done("ns_load")) return rc;
     }
-    const int tm = l.mp / 64, tn = l.np / 64;
     // A bfloat16 result takes single float16 products in all but the last two
-    // steps: 2e-4 to 1e-3 off before its own rounding of 1.7e-3 (three products
-    // in the last two steps matter most: there A's entries are of order one and
-    // their rounding enters X unscaled).
+    // steps, and for X X^T throughout: 2e-4 to 1e-3 off before its own rounding
+    // of 1.7e-3.  In the last two steps A's entries are of order one and the
+    // rounding of P and X in the other products enters X unscaled.
     const int exact_from = sink.bf16 ? std::max(0, c.steps - 2) : 0;
     for (int t = 0; t < c.steps; ++t) {
-        const bool three = t >= exact_from, last = t + 1 == c.steps;
+        const bool three = t >= exact_from, last = t + 1 == c.steps, three_gram = !sink.bf16;
         half_t* xt = XT[t & 1];
         Product g{};
+        g.part = reinterpret_cast<float*>(ws + l.part);
+        Product q = g, s = g;
         g.u = g.v = X;
         g.u_plane = g.v_plane = l.xplane;
         g.K = l.np;
+        g.rows_u = g.rows_v = l.mp;
         g.out = g.out_t = A;
         g.o_plane = l.aplane;
-        g.add = X;   // not read
         g.ld_out = g.ld_t = l.mp;
         g.lo_out = g.lo_t = 1;
         g.cb = kSA / (kSX * kSX);
-        if (int rc = launch_product<kGram>(three, g, tm * (tm + 1) / 2, c.batch, st)) return rc;
+        if (int rc = launch_product<kGram>(three_gram, g, c.batch, st)) return rc;
 
-        Product q{};
         q.u = q.v = A;
         q.u_plane = q.v_plane = l.aplane;
         q.K = l.mp;
+        q.rows_u = q.rows_v = l.mp;
         q.out = q.out_t = P;
         q.add = A;
         q.o_plane = q.add_plane = l.aplane;
@@ -981,34 +1331,37 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
         q.lo_out = q.lo_t = three;
         q.ca = c.coeffs[1] * kSP / kSA;
         q.cb = c.coeffs[2] * kSP / (kSA * kSA);
-        if (int rc = launch_product<kPoly>(three, q, tm * (tm + 1) / 2, c.batch, st)) return rc;
+        // three products carry a I + P as well as P: no separate a X then
+        q.diagonal = three ? c.coeffs[0] * kSP : 0.0f;
+        if (int rc = launch_product<kPoly>(three, q, c.batch, st)) return rc;
 
-        Product s{};
         s.u = P;
         s.v = xt;
         s.u_plane = l.aplane;
         s.v_plane = s.add_plane = s.o_plane = l.xplane;
         s.K = l.mp;
-        s.tiles_j = tn;
+        s.rows_u = l.mp;
+        s.rows_v = l.np;
         s.out = X;
         s.out_t = XT[(t + 1) & 1];
-        s.add = xt;
+        s.add = three ? nullptr : xt;
         s.ld_out = l.np;
         s.ld_t = l.mp;
-        s.lo_out = t + 1 >= exact_from;   // the next X X^T reads it
+        s.lo_out = three_gram;   // X X^T reads it
         s.lo_t = 1;
         s.ca = c.coeffs[0];
         s.cb = 1.0f / kSP;
-        if (last) {
-            s.ca /= kSX;
+        int rc;
+        if (last) {   // three products
             s.cb /= kSX;
             s.m = l.m;
             s.n = l.n;
             s.tall = l.tall;
             s.sink = sink;
+            rc = launch_product<3, kLast>(s, c.batch, st);
+        } else {
+            rc = launch_product<kStep>(three, s, c.batch, st);
         }
-        const int rc = last ? launch_product<kLast>(three, s, tm * tn, c.batch, st)
-                            : launch_product<kStep>(three, s, tm * tn, c.batch, st);
         if (rc) return rc;
     }
     return DISCO_OK;
