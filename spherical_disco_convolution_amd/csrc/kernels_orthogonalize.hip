@@ -213,7 +213,7 @@ __device__ __forceinline__ double inv_norm(const double* partial, int nparts, fl
     return 1.0 / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)eps);
 }
 
-// X_0 in both orders, zero padded to mp x np: a 64 x 64 tile a workgroup,
+// X_0 in both orders, zero padded to multiples of 64: a 64 x 64 tile a workgroup,
 // through LDS.  tall: the source is [n][m].
 template <typename T>
 __global__ __launch_bounds__(256) void ns_load(Source src, const double* __restrict__ partial,
@@ -1061,13 +1061,296 @@ struct SmallShape {
 SmallShape small_shape(int m, int n) {
     SmallShape s;
     const int blocks = (n + 31) / 32, mt = (m + 31) / 32;
-    if (mt > 2 || blocks > (mt == 1 ? 32 : 16)) return s;
+    // 32 x 512 and 64 x 256; past that a step on one compute unit takes longer
+    // than a launch over several (64 x 448: 57 us here, 44 us by ns_panel)
+    if (mt > 2 || blocks > (mt == 1 ? 16 : 8)) return s;
     s.mt = mt;
     s.cb = 1;
     while (s.cb * 8 < blocks) s.cb *= 2;
     // at least a wave for each tile of A, also where there are fewer columns
     s.waves = std::max(mt * mt, (blocks + s.cb - 1) / s.cb);
     return s;
+}
+
+// ---------------------------------------------------------------------------
+// Flat matrices: one launch a step
+// ---------------------------------------------------------------------------
+// Up to 128 rows and 1024 columns.  A workgroup owns a panel of 128 columns and
+// does a whole step on it: it adds the panels' parts of X X^T, forms P (every
+// workgroup the same one: 128^3 products cost less than a launch), advances its
+// panel and leaves its part of the new X X^T.  At 128 x 896 the tiled products'
+// three launches a step, each 5 us long with next to no work in it, become one.
+//
+// LDS: the panel's X^T as rows of a column's M entries, hi then lo, whose
+// 16-byte chunk c lies in slot c ^ (column % chunks); A and then P as padded rows.
+template <int MT>
+struct PanelCfg {
+    static constexpr int M = 32 * MT, NT = MT * (MT + 1) / 2, CH = M / 8;
+    static constexpr int COLS = 128, WAVES = 8;
+    static constexpr int X_PLANE = COLS * 2 * M;            // bytes
+    static constexpr int ROW_A = 2 * M + 16, A_PLANE = M * ROW_A;
+    static constexpr int LDS = 2 * X_PLANE + 2 * A_PLANE;
+    static __device__ __forceinline__ uint32_t x_cell(int col, int row) {
+        return (uint32_t)(col * 2 * M + 16 * ((row >> 3) ^ (col & (CH - 1))) + 2 * (row & 7));
+    }
+};
+
+struct PanelArgs {
+    half_t* XT;                // [batch][hi, lo][np][M], advanced in place
+    size_t xplane;
+    const float* part_in;      // [batch][panel][tile][1024]
+    float* part_out;
+    int panels, np;
+    int m, n, tall;
+    float ca, cb, cc;
+    int first, last;           // only X X^T; only the result
+    Sink sink;
+};
+
+template <int MT>
+__global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
+    using C = PanelCfg<MT>;
+    constexpr int RT = MT / 2;   // row tiles of a wave
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_raw[C::LDS];
+    const uint32_t x_at = (uint32_t)(uintptr_t)(lds_u8*)&lds_raw[0];
+    const uint32_t a_at = x_at + 2 * C::X_PLANE;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int l32 = lane & 31, lg = lane >> 5;
+    const int panel = blockIdx.x, b = blockIdx.y, col0 = panel * C::COLS;
+    const int cols = min(C::COLS, p.np - col0);   // 64 or 128
+    half_t* xt = p.XT + (size_t)b * 2 * p.xplane + (size_t)col0 * C::M;
+
+    // the panel's X^T: 1 KB a load, 16 bytes a lane
+    constexpr int PER = C::X_PLANE / 1024 / C::WAVES;   // loads of a wave and plane
+#pragma unroll
+    for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+        for (int o = 0; o < PER; ++o) {
+            const int unit = o * C::WAVES + wave, chunk = unit * 64 + lane;
+            const int col = min(chunk / C::CH, cols - 1);   // past a half panel: its last column
+            const int slot = chunk % C::CH;
+            dma_lds16(xt + (size_t)pl * p.xplane + (size_t)col * C::M + 8 * (slot ^ ((chunk / C::CH) & (C::CH - 1))),
+                      x_at + (uint32_t)(pl * C::X_PLANE + unit * 1024));
+        }
+
+    typedef __attribute__((address_space(3))) half_t lds_half;
+    if (!p.first) {
+        // ---- A from the panels' parts, in order ----
+        const floatx4* in = reinterpret_cast<const floatx4*>(p.part_in) + (size_t)b * p.panels * C::NT * 256;
+        constexpr int POS = (C::NT * 256 + 511) / 512;
+        floatx4 v[POS];
+#pragma unroll
+        for (int k = 0; k < POS; ++k) v[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        // four panels' reads in flight; past the last panel it is read again and dropped
+        for (int q0 = 0; q0 < p.panels; q0 += 4) {
+            floatx4 f[4][POS];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < POS; ++k)
+                    f[u][k] = in[(size_t)min(q0 + u, p.panels - 1) * C::NT * 256 +
+                                 min(k * 512 + (int)threadIdx.x, C::NT * 256 - 1)];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (q0 + u < p.panels)
+#pragma unroll
+                    for (int k = 0; k < POS; ++k) v[k] += f[u][k];
+        }
+#pragma unroll
+        for (int k = 0; k < POS; ++k) {
+            const int group = uniform(8 * k + wave);   // of 64 places: a quarter of a tile
+            if (group >= C::NT * 4) break;
+            const int tile = group >> 2, q = group & 3, pl = lane;
+            int ta = 0;
+            while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
+            const int tb = tile - ta * (ta + 1) / 2;
+            const int i = 32 * ta + 8 * q + 4 * (pl >> 5), j = 32 * tb + (pl & 31);
+            halfx4 h, l;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const Pair s = split(v[k][r] * (kSA / (kSX * kSX)));
+                h[r] = s.h;
+                l[r] = s.l;
+            }
+            const uint32_t at = a_at + (uint32_t)(j * C::ROW_A + 2 * i);
+            *(lds_halfx4*)(uintptr_t)at = h;
+            *(lds_halfx4*)(uintptr_t)(at + C::A_PLANE) = l;
+            if (ta != tb) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t at2 = a_at + (uint32_t)((i + r) * C::ROW_A + 2 * j);
+                    *(lds_half*)(uintptr_t)at2 = h[r];
+                    *(lds_half*)(uintptr_t)(at2 + C::A_PLANE) = l[r];
+                }
+            }
+        }
+        __syncthreads();
+        // ---- P = a I + b A + c A^2: lower tiles wave, wave + 8 ----
+        constexpr int TILES = (C::NT + C::WAVES - 1) / C::WAVES;
+        floatx16 g[TILES];
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[k][e] = 0.0f;
+            const int tile = wave + C::WAVES * k;
+            if (tile >= C::NT) break;
+            int ta = 0;
+            while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
+            const int tb = tile - ta * (ta + 1) / 2;
+#pragma unroll
+            for (int kc = 0; kc < 2 * MT; ++kc) {
+                const uint32_t u = a_at + (uint32_t)((32 * ta + l32) * C::ROW_A + 32 * kc + 16 * lg);
+                const uint32_t w = a_at + (uint32_t)((32 * tb + l32) * C::ROW_A + 32 * kc + 16 * lg);
+                g[k] = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE),
+                             *(const lds_halfx8*)(uintptr_t)w, *(const lds_halfx8*)(uintptr_t)(w + C::A_PLANE), g[k]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 32 * ta + 8 * q + 4 * lg, j = 32 * tb + l32;
+                const uint32_t at = a_at + (uint32_t)(j * C::ROW_A + 2 * i);
+                const halfx4 h = *(const lds_halfx4*)(uintptr_t)at;
+                const halfx4 l = *(const lds_halfx4*)(uintptr_t)(at + C::A_PLANE);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    g[k][4 * q + r] = p.cb * (kSP / kSA) * ((float)h[r] + (float)l[r]) +
+                                      p.cc * (kSP / (kSA * kSA)) * g[k][4 * q + r] +
+                                      (i + r == j ? p.ca * kSP : 0.0f);
+            }
+        }
+        __syncthreads();   // A has been read: P takes its place
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            const int tile = wave + C::WAVES * k;
+            if (tile >= C::NT) break;
+            int ta = 0;
+            while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
+            const int tb = tile - ta * (ta + 1) / 2;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 32 * ta + 8 * q + 4 * lg, j = 32 * tb + l32;
+                halfx4 h, l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const Pair s = split(g[k][4 * q + r]);
+                    h[r] = s.h;
+                    l[r] = s.l;
+                }
+                const uint32_t at = a_at + (uint32_t)(j * C::ROW_A + 2 * i);
+                *(lds_halfx4*)(uintptr_t)at = h;
+                *(lds_halfx4*)(uintptr_t)(at + C::A_PLANE) = l;
+                if (ta != tb) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t at2 = a_at + (uint32_t)((i + r) * C::ROW_A + 2 * j);
+                        *(lds_half*)(uintptr_t)at2 = h[r];
+                        *(lds_half*)(uintptr_t)(at2 + C::A_PLANE) = l[r];
+                    }
+                }
+            }
+        }
+        wait_vmcnt<0>();   // the panel has landed
+        __syncthreads();
+        // ---- X <- (a I + P) X: RT row tiles of one block of 32 columns a wave ----
+        const int rt0 = (wave & 1) * RT, cb = wave >> 1;
+        floatx16 y[RT];
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[a][e] = 0.0f;
+#pragma unroll
+        for (int kc = 0; kc < 2 * MT; ++kc) {
+            const uint32_t v = x_at + C::x_cell(32 * cb + l32, 16 * kc + 8 * lg);
+            const halfx8 vh = *(const lds_halfx8*)(uintptr_t)v;
+            const halfx8 vl = *(const lds_halfx8*)(uintptr_t)(v + C::X_PLANE);
+#pragma unroll
+            for (int a = 0; a < RT; ++a) {
+                const uint32_t u = a_at + (uint32_t)((32 * (rt0 + a) + l32) * C::ROW_A + 32 * kc + 16 * lg);
+                y[a] = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE), vh, vl,
+                             y[a]);
+            }
+        }
+        if (p.last) {
+            const int64_t at0 = (int64_t)b * p.m * p.n;
+            const int j = col0 + 32 * cb + l32;
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = 32 * (rt0 + a) + 8 * (e >> 2) + 4 * lg + (e & 3);
+                    if (i < p.m && j < p.n)
+                        sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i : (int64_t)i * p.n + j),
+                                   y[a][e] * (1.0f / (kSP * kSX)));
+                }
+            return;
+        }
+        __syncthreads();   // the old panel has been read
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                halfx4 h, l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const Pair s = split(y[a][4 * q + r] * (1.0f / kSP));
+                    h[r] = s.h;
+                    l[r] = s.l;
+                }
+                const uint32_t at = x_at + C::x_cell(32 * cb + l32, 32 * (rt0 + a) + 8 * q + 4 * lg);
+                *(lds_halfx4*)(uintptr_t)at = h;
+                *(lds_halfx4*)(uintptr_t)(at + C::X_PLANE) = l;
+            }
+        __syncthreads();
+        // whole rows back to memory
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+            for (int o = 0; o < PER; ++o) {
+                const int chunk = (o * C::WAVES + wave) * 64 + lane, col = chunk / C::CH, c = chunk % C::CH;
+                if (col < cols)
+                    *reinterpret_cast<halfx8*>(xt + (size_t)pl * p.xplane + (size_t)col * C::M + 8 * c) =
+                        *(const lds_halfx8*)(uintptr_t)(x_at + pl * C::X_PLANE + C::x_cell(col, 8 * c));
+            }
+    } else {
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
+    // ---- this panel's part of X X^T: lower tiles wave, wave + 8 ----
+    float* out = p.part_out + ((size_t)b * p.panels + panel) * C::NT * 1024;
+    for (int tile = wave; tile < C::NT; tile += C::WAVES) {
+        int ta = 0;
+        while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
+        const int tb = tile - ta * (ta + 1) / 2;
+        floatx16 g;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) g[e] = 0.0f;
+        // this lane's cells of the first 16 columns, for the two halves of a read
+        const int s16 = lane & 15, q16 = lane >> 4;
+        const int col = 8 * (q16 >> 1) + (s16 >> 2), row = 16 * (q16 & 1) + 4 * (s16 & 3);
+        const uint32_t ca[2] = {x_at + C::x_cell(col, 32 * ta + row), x_at + C::x_cell(col + 4, 32 * ta + row)};
+        const uint32_t cb[2] = {x_at + C::x_cell(col, 32 * tb + row), x_at + C::x_cell(col + 4, 32 * tb + row)};
+#pragma unroll 4
+        for (int kc = 0; kc < cols / 16; ++kc) {
+            // 16 columns on, the slots are the same
+            auto turned = [&](const uint32_t (&cell)[2], int pl) {
+                const uint32_t at = (uint32_t)(pl * C::X_PLANE + kc * 32 * C::M);
+                const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[0] + at));
+                const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[1] + at));
+                return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            g = mfma3(turned(ca, 0), turned(ca, 1), turned(cb, 0), turned(cb, 1), g);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            reinterpret_cast<floatx4*>(out)[tile * 256 + q * 64 + lane] =
+                floatx4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]};
+    }
+}
+
+// Whether a matrix takes ns_panel, and its parts of X X^T.
+bool panel_shape(int m, int n) { return m <= 128 && n <= 1024; }
+size_t panel_part_bytes(int mp, int np) {
+    const int mt = mp / 32;
+    return (size_t)((np + 127) / 128) * (mt * (mt + 1) / 2) * 4096;
 }
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -1104,8 +1387,9 @@ TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool sy
         const int64_t ti = (ni + side - 1) / side, tj = (nj + side - 1) / side;
         const int64_t tiles = batch * (symmetric ? ti * (ti + 1) / 2 : ti * tj);
         const int64_t at_once = kind == 1 ? 512 : 256;
-        for (int splits : {1, 2, 4, 8, 16}) {
-            if (splits > 1 && (!can_split || kind == 3 || K / 64 < 4 * splits || tiles * splits > 2048)) break;
+        // also as many as fill the compute units once
+        for (int splits : {1, 2, 4, 8, 16, (int)std::min<int64_t>(16, std::max<int64_t>(1, at_once / tiles))}) {
+            if (splits > 1 && (!can_split || kind == 3 || K / 64 < 4 * splits || tiles * splits > 2048)) continue;
             const int64_t rounds = (tiles * splits + at_once - 1) / at_once;
             double us = rounds * (K / 64.0 / splits * slice_us[kind][np == 3] + ends_us[kind]);
             if (splits > 1) us += 4.0 + 0.2 * splits * side / 64;
@@ -1158,6 +1442,7 @@ Layout layout(int batch, int rows, int cols) {
         if (t.splits > 1)
             part = std::max(part, (size_t)batch * (ti * (ti + 1) / 2) * t.splits * side * side * sizeof(float));
     }
+    if (panel_shape(l.m, l.n)) part = 2 * batch * panel_part_bytes(l.mp, l.np);   // one read, one written
     l.part = take(part);
     l.bytes = at;
     return l;
@@ -1242,11 +1527,9 @@ template <typename T>
 int launch_small(const OrthoCall& c, const Sink& sink, const SmallShape& s, hipStream_t st) {
     if (s.mt == 1) {
         if (s.cb == 1) return launch_small<T, 1, 1>(c, sink, s.waves, st);
-        if (s.cb == 2) return launch_small<T, 1, 2>(c, sink, s.waves, st);
-        return launch_small<T, 1, 4>(c, sink, s.waves, st);
+        return launch_small<T, 1, 2>(c, sink, s.waves, st);
     }
-    if (s.cb == 1) return launch_small<T, 2, 1>(c, sink, s.waves, st);
-    return launch_small<T, 2, 2>(c, sink, s.waves, st);
+    return launch_small<T, 2, 1>(c, sink, s.waves, st);
 }
 
 }  // namespace
@@ -1298,6 +1581,35 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
                                c.eps, l.m, l.n, l.mp, l.np, l.tall, X, XT[0], l.xplane);
         if (int rc = done("ns_load")) return rc;
     }
+    if (panel_shape(l.m, l.n)) {
+        PanelArgs a{};
+        a.XT = XT[0];
+        a.xplane = l.xplane;
+        a.np = l.np;
+        a.panels = (l.np + 127) / 128;
+        a.m = l.m;
+        a.n = l.n;
+        a.tall = l.tall;
+        a.ca = c.coeffs[0];
+        a.cb = c.coeffs[1];
+        a.cc = c.coeffs[2];
+        a.sink = sink;
+        char* parts[2] = {ws + l.part, ws + l.part + c.batch * panel_part_bytes(l.mp, l.np)};
+        for (int t = 0; t <= c.steps; ++t) {
+            a.first = t == 0;
+            a.last = t == c.steps;
+            a.part_in = reinterpret_cast<const float*>(parts[(t + 1) & 1]);
+            a.part_out = reinterpret_cast<float*>(parts[t & 1]);
+            KernelTimer timer("ns_panel", st);
+            if (l.mp == 64)
+                hipLaunchKernelGGL(ns_panel<2>, dim3(a.panels, c.batch), dim3(512), 0, st, a);
+            else
+                hipLaunchKernelGGL(ns_panel<4>, dim3(a.panels, c.batch), dim3(512), 0, st, a);
+            if (int rc = done("ns_panel")) return rc;
+        }
+        return DISCO_OK;
+    }
+
     // A bfloat16 result takes single float16 products in all but the last two
     // steps, and for X X^T throughout: 2e-4 to 1e-3 off before its own rounding
     // of 1.7e-3.  In the last two steps A's entries are of order one and the
