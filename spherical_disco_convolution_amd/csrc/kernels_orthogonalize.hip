@@ -1328,17 +1328,18 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
         const int col = 8 * (q16 >> 1) + (s16 >> 2), row = 16 * (q16 & 1) + 4 * (s16 & 3);
         const uint32_t ca[2] = {x_at + C::x_cell(col, 32 * ta + row), x_at + C::x_cell(col + 4, 32 * ta + row)};
         const uint32_t cb[2] = {x_at + C::x_cell(col, 32 * tb + row), x_at + C::x_cell(col + 4, 32 * tb + row)};
-#pragma unroll 4
-        for (int kc = 0; kc < cols / 16; ++kc) {
-            // 16 columns on, the slots are the same
-            auto turned = [&](const uint32_t (&cell)[2], int pl) {
-                const uint32_t at = (uint32_t)(pl * C::X_PLANE + kc * 32 * C::M);
-                const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[0] + at));
-                const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[1] + at));
-                return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            };
-            g = mfma3(turned(ca, 0), turned(ca, 1), turned(cb, 0), turned(cb, 1), g);
-        }
+        for (int kc0 = 0; kc0 < cols / 16; kc0 += 4)   // 64 or 128 columns
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                // 16 columns on, the slots are the same
+                auto turned = [&](const uint32_t (&cell)[2], int pl) {
+                    const uint32_t at = (uint32_t)(pl * C::X_PLANE + (kc0 + u) * 32 * C::M);
+                    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[0] + at));
+                    const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[1] + at));
+                    return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                };
+                g = mfma3(turned(ca, 0), turned(ca, 1), turned(cb, 0), turned(cb, 1), g);
+            }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             reinterpret_cast<floatx4*>(out)[tile * 256 + q * 64 + lane] =
