@@ -761,7 +761,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), W = blockDim.x >> 6;
     const int l32 = lane & 31, lg = lane >> 5;
     const uint32_t piece = P_at + C::P_BYTES + (uint32_t)(wave * C::PIECE);
-    // 32-bit offsets from here on: at most 64 x 1024 elements
+    // 32-bit offsets from here on: at most 2^14 elements
     const int64_t base = (int64_t)blockIdx.x * m * n;
     const T* in = static_cast<const T*>(src.m) + base;
     const float* old = buf_out ? buf_in + base : nullptr;
@@ -779,7 +779,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
     const float rwidth = 1.0f / (float)width;
     // LDS place of element `at` and of the ones after it in its row
     auto place = [&](int at, int& q, int& r) {
-        q = (int)(((float)at + 0.5f) * rwidth);   // at < 2^16: exact
+        q = (int)(((float)at + 0.5f) * rwidth);   // at <= 2^14: exact
         r = at - q * width;
     };
     auto slot = [&](int q, int r) {
@@ -1075,7 +1075,7 @@ SmallShape small_shape(int m, int n) {
 // ---------------------------------------------------------------------------
 // Flat matrices: one launch a step
 // ---------------------------------------------------------------------------
-// Up to 128 rows and 1024 columns.  A workgroup owns a panel of 128 columns and
+// Up to 64 rows by 8192 columns, or 128 by 1536.  A workgroup owns a panel of 128 columns and
 // does a whole step on it: it adds the panels' parts of X X^T, forms P (every
 // workgroup the same one: 128^3 products cost less than a launch), advances its
 // panel and leaves its part of the new X X^T.  At 128 x 896 the tiled products'
@@ -1347,8 +1347,11 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
     }
 }
 
-// Whether a matrix takes ns_panel, and its parts of X X^T.
-bool panel_shape(int m, int n) { return m <= 128 && n <= 1024; }
+// Whether a matrix takes ns_panel, and its parts of X X^T.  Every panel reads
+// all parts: 0.1 us a part and step for 64 rows, 0.4 us for 128, which the tiled
+// products' two further launches a step are worth up to about here (in all 46 us
+// at 64 x 1000 and 91 us at 128 x 1024, against 105 and 117 us tiled).
+bool panel_shape(int m, int n) { return (m <= 64 && n <= 8192) || (m <= 128 && n <= 1536); }
 size_t panel_part_bytes(int mp, int np) {
     const int mt = mp / 32;
     return (size_t)((np + 127) / 128) * (mt * (mt + 1) / 2) * 4096;
