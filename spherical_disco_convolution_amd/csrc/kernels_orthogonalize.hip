@@ -1086,7 +1086,7 @@ SmallShape small_shape(int m, int n) {
 template <int MT>
 struct PanelCfg {
     static constexpr int M = 32 * MT, NT = MT * (MT + 1) / 2, CH = M / 8;
-    static constexpr int COLS = 128, WAVES = 8;
+    static constexpr int COLS = 128, WAVES = 4 * MT;        // a 32 x 32 block of the panel each
     static constexpr int X_PLANE = COLS * 2 * M;            // bytes
     static constexpr int ROW_A = 2 * M + 16, A_PLANE = M * ROW_A;
     static constexpr int LDS = 2 * X_PLANE + 2 * A_PLANE;
@@ -1108,9 +1108,9 @@ struct PanelArgs {
 };
 
 template <int MT>
-__global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
+__global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
     using C = PanelCfg<MT>;
-    constexpr int RT = MT / 2;   // row tiles of a wave
+    constexpr int THREADS = 64 * C::WAVES;
     __shared__ __attribute__((aligned(1024))) uint8_t lds_raw[C::LDS];
     const uint32_t x_at = (uint32_t)(uintptr_t)(lds_u8*)&lds_raw[0];
     const uint32_t a_at = x_at + 2 * C::X_PLANE;
@@ -1137,7 +1137,7 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
     if (!p.first) {
         // ---- A from the panels' parts, in order ----
         const floatx4* in = reinterpret_cast<const floatx4*>(p.part_in) + (size_t)b * p.panels * C::NT * 256;
-        constexpr int POS = (C::NT * 256 + 511) / 512;
+        constexpr int POS = (C::NT * 256 + THREADS - 1) / THREADS;
         floatx4 v[POS];
 #pragma unroll
         for (int k = 0; k < POS; ++k) v[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -1149,7 +1149,7 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
 #pragma unroll
                 for (int k = 0; k < POS; ++k)
                     f[u][k] = in[(size_t)min(q0 + u, p.panels - 1) * C::NT * 256 +
-                                 min(k * 512 + (int)threadIdx.x, C::NT * 256 - 1)];
+                                 min(k * THREADS + (int)threadIdx.x, C::NT * 256 - 1)];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (q0 + u < p.panels)
@@ -1158,7 +1158,7 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
         }
 #pragma unroll
         for (int k = 0; k < POS; ++k) {
-            const int group = uniform(8 * k + wave);   // of 64 places: a quarter of a tile
+            const int group = uniform(C::WAVES * k + wave);   // of 64 places: a quarter of a tile
             if (group >= C::NT * 4) break;
             const int tile = group >> 2, q = group & 3, pl = lane;
             int ta = 0;
@@ -1185,24 +1185,21 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
             }
         }
         __syncthreads();
-        // ---- P = a I + b A + c A^2: lower tiles wave, wave + 8 ----
-        constexpr int TILES = (C::NT + C::WAVES - 1) / C::WAVES;
-        floatx16 g[TILES];
+        // ---- P = a I + b A + c A^2: a lower tile a wave ----
+        static_assert(C::NT <= C::WAVES, "a wave for each tile");
+        int ta = 0;
+        while ((ta + 1) * (ta + 2) / 2 <= wave) ++ta;
+        const int tb = wave - ta * (ta + 1) / 2;
+        floatx16 g;
 #pragma unroll
-        for (int k = 0; k < TILES; ++k) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) g[k][e] = 0.0f;
-            const int tile = wave + C::WAVES * k;
-            if (tile >= C::NT) break;
-            int ta = 0;
-            while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
-            const int tb = tile - ta * (ta + 1) / 2;
+        for (int e = 0; e < 16; ++e) g[e] = 0.0f;
+        if (wave < C::NT) {
 #pragma unroll
             for (int kc = 0; kc < 2 * MT; ++kc) {
                 const uint32_t u = a_at + (uint32_t)((32 * ta + l32) * C::ROW_A + 32 * kc + 16 * lg);
                 const uint32_t w = a_at + (uint32_t)((32 * tb + l32) * C::ROW_A + 32 * kc + 16 * lg);
-                g[k] = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE),
-                             *(const lds_halfx8*)(uintptr_t)w, *(const lds_halfx8*)(uintptr_t)(w + C::A_PLANE), g[k]);
+                g = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE),
+                          *(const lds_halfx8*)(uintptr_t)w, *(const lds_halfx8*)(uintptr_t)(w + C::A_PLANE), g);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1212,26 +1209,19 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
                 const halfx4 l = *(const lds_halfx4*)(uintptr_t)(at + C::A_PLANE);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    g[k][4 * q + r] = p.cb * (kSP / kSA) * ((float)h[r] + (float)l[r]) +
-                                      p.cc * (kSP / (kSA * kSA)) * g[k][4 * q + r] +
-                                      (i + r == j ? p.ca * kSP : 0.0f);
+                    g[4 * q + r] = p.cb * (kSP / kSA) * ((float)h[r] + (float)l[r]) +
+                                   p.cc * (kSP / (kSA * kSA)) * g[4 * q + r] + (i + r == j ? p.ca * kSP : 0.0f);
             }
         }
         __syncthreads();   // A has been read: P takes its place
-#pragma unroll
-        for (int k = 0; k < TILES; ++k) {
-            const int tile = wave + C::WAVES * k;
-            if (tile >= C::NT) break;
-            int ta = 0;
-            while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
-            const int tb = tile - ta * (ta + 1) / 2;
+        if (wave < C::NT)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int i = 32 * ta + 8 * q + 4 * lg, j = 32 * tb + l32;
                 halfx4 h, l;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const Pair s = split(g[k][4 * q + r]);
+                    const Pair s = split(g[4 * q + r]);
                     h[r] = s.h;
                     l[r] = s.l;
                 }
@@ -1247,58 +1237,46 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
                     }
                 }
             }
-        }
         wait_vmcnt<0>();   // the panel has landed
         __syncthreads();
-        // ---- X <- (a I + P) X: RT row tiles of one block of 32 columns a wave ----
-        const int rt0 = (wave & 1) * RT, cb = wave >> 1;
-        floatx16 y[RT];
+        // ---- X <- (a I + P) X: a 32 x 32 block a wave ----
+        const int rt = wave % MT, cb = wave / MT;
+        floatx16 y;
 #pragma unroll
-        for (int a = 0; a < RT; ++a)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[a][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) y[e] = 0.0f;
 #pragma unroll
         for (int kc = 0; kc < 2 * MT; ++kc) {
             const uint32_t v = x_at + C::x_cell(32 * cb + l32, 16 * kc + 8 * lg);
-            const halfx8 vh = *(const lds_halfx8*)(uintptr_t)v;
-            const halfx8 vl = *(const lds_halfx8*)(uintptr_t)(v + C::X_PLANE);
-#pragma unroll
-            for (int a = 0; a < RT; ++a) {
-                const uint32_t u = a_at + (uint32_t)((32 * (rt0 + a) + l32) * C::ROW_A + 32 * kc + 16 * lg);
-                y[a] = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE), vh, vl,
-                             y[a]);
-            }
+            const uint32_t u = a_at + (uint32_t)((32 * rt + l32) * C::ROW_A + 32 * kc + 16 * lg);
+            y = mfma3(*(const lds_halfx8*)(uintptr_t)u, *(const lds_halfx8*)(uintptr_t)(u + C::A_PLANE),
+                      *(const lds_halfx8*)(uintptr_t)v, *(const lds_halfx8*)(uintptr_t)(v + C::X_PLANE), y);
         }
         if (p.last) {
             const int64_t at0 = (int64_t)b * p.m * p.n;
             const int j = col0 + 32 * cb + l32;
 #pragma unroll
-            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int i = 32 * (rt0 + a) + 8 * (e >> 2) + 4 * lg + (e & 3);
-                    if (i < p.m && j < p.n)
-                        sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i : (int64_t)i * p.n + j),
-                                   y[a][e] * (1.0f / (kSP * kSX)));
-                }
+            for (int e = 0; e < 16; ++e) {
+                const int i = 32 * rt + 8 * (e >> 2) + 4 * lg + (e & 3);
+                if (i < p.m && j < p.n)
+                    sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i : (int64_t)i * p.n + j),
+                               y[e] * (1.0f / (kSP * kSX)));
+            }
             return;
         }
         __syncthreads();   // the old panel has been read
 #pragma unroll
-        for (int a = 0; a < RT; ++a)
+        for (int q = 0; q < 4; ++q) {
+            halfx4 h, l;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                halfx4 h, l;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const Pair s = split(y[a][4 * q + r] * (1.0f / kSP));
-                    h[r] = s.h;
-                    l[r] = s.l;
-                }
-                const uint32_t at = x_at + C::x_cell(32 * cb + l32, 32 * (rt0 + a) + 8 * q + 4 * lg);
-                *(lds_halfx4*)(uintptr_t)at = h;
-                *(lds_halfx4*)(uintptr_t)(at + C::X_PLANE) = l;
+            for (int r = 0; r < 4; ++r) {
+                const Pair s = split(y[4 * q + r] * (1.0f / kSP));
+                h[r] = s.h;
+                l[r] = s.l;
             }
+            const uint32_t at = x_at + C::x_cell(32 * cb + l32, 32 * rt + 8 * q + 4 * lg);
+            *(lds_halfx4*)(uintptr_t)at = h;
+            *(lds_halfx4*)(uintptr_t)(at + C::X_PLANE) = l;
+        }
         __syncthreads();
         // whole rows back to memory
 #pragma unroll
@@ -1314,12 +1292,12 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
         wait_vmcnt<0>();
         __syncthreads();
     }
-    // ---- this panel's part of X X^T: lower tiles wave, wave + 8 ----
+    // ---- this panel's part of X X^T: a lower tile a wave ----
     float* out = p.part_out + ((size_t)b * p.panels + panel) * C::NT * 1024;
-    for (int tile = wave; tile < C::NT; tile += C::WAVES) {
+    if (wave < C::NT) {
         int ta = 0;
-        while ((ta + 1) * (ta + 2) / 2 <= tile) ++ta;
-        const int tb = tile - ta * (ta + 1) / 2;
+        while ((ta + 1) * (ta + 2) / 2 <= wave) ++ta;
+        const int tb = wave - ta * (ta + 1) / 2;
         floatx16 g;
 #pragma unroll
         for (int e = 0; e < 16; ++e) g[e] = 0.0f;
@@ -1342,7 +1320,7 @@ __global__ __launch_bounds__(512) void ns_panel(PanelArgs p) {
             }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            reinterpret_cast<floatx4*>(out)[tile * 256 + q * 64 + lane] =
+            reinterpret_cast<floatx4*>(out)[wave * 256 + q * 64 + lane] =
                 floatx4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]};
     }
 }
@@ -1608,7 +1586,7 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
             if (l.mp == 64)
                 hipLaunchKernelGGL(ns_panel<2>, dim3(a.panels, c.batch), dim3(512), 0, st, a);
             else
-                hipLaunchKernelGGL(ns_panel<4>, dim3(a.panels, c.batch), dim3(512), 0, st, a);
+                hipLaunchKernelGGL(ns_panel<4>, dim3(a.panels, c.batch), dim3(1024), 0, st, a);
             if (int rc = done("ns_panel")) return rc;
         }
         return DISCO_OK;
