@@ -45,8 +45,13 @@ struct Pair {
     half_t h, l;
 };
 
+// v as hi + lo.  The empty asm pins v to its float32 value: without it the
+// compiler may round hi from the unrounded product that v comes from and lo
+// from v, and near a tie the two then belong to different neighbours (single
+// entries 2^-11 off).
 __device__ __forceinline__ Pair split(float v) {
     Pair p;
+    asm volatile("" : "+v"(v));
     p.h = (half_t)v;
     p.l = (half_t)(v - (float)p.h);
     return p;
@@ -1100,18 +1105,156 @@ struct PanelArgs {
     size_t xplane;
     const float* part_in;      // [batch][panel][tile][1024]
     float* part_out;
+    int* exponents;            // [batch][panel]: X as loaded is the matrix times 2^-exponent
     int panels, np;
     int m, n, tall;
-    float ca, cb, cc;
-    int first, last;           // only X X^T; only the result
+    float ca, cb, cc, eps;
+    int raw, last;             // the step on X as loaded; only the result
     Sink sink;
 };
+
+// A panel's part of X X^T: a lower tile a wave.
+template <int MT>
+__device__ __forceinline__ void panel_gram(uint32_t x_at, int cols, float* out, int wave, int lane) {
+    using C = PanelCfg<MT>;
+    if (wave >= C::NT) return;
+    int ta = 0;
+    while ((ta + 1) * (ta + 2) / 2 <= wave) ++ta;
+    const int tb = wave - ta * (ta + 1) / 2;
+    floatx16 g;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) g[e] = 0.0f;
+    // this lane's cells of the first 16 columns, for the two halves of a read
+    const int s16 = lane & 15, q16 = lane >> 4;
+    const int col = 8 * (q16 >> 1) + (s16 >> 2), row = 16 * (q16 & 1) + 4 * (s16 & 3);
+    const uint32_t ca[2] = {x_at + C::x_cell(col, 32 * ta + row), x_at + C::x_cell(col + 4, 32 * ta + row)};
+    const uint32_t cb[2] = {x_at + C::x_cell(col, 32 * tb + row), x_at + C::x_cell(col + 4, 32 * tb + row)};
+    for (int kc0 = 0; kc0 < cols / 16; kc0 += 4)   // 64 or 128 columns
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // 16 columns on, the slots are the same
+            auto turned = [&](const uint32_t (&cell)[2], int pl) {
+                const uint32_t at = (uint32_t)(pl * C::X_PLANE + (kc0 + u) * 32 * C::M);
+                const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[0] + at));
+                const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[1] + at));
+                return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            g = mfma3(turned(ca, 0), turned(ca, 1), turned(cb, 0), turned(cb, 1), g);
+        }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        reinterpret_cast<floatx4*>(out)[wave * 256 + q * 64 + lane] =
+            floatx4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]};
+}
+
+// Loads a panel (advancing the momentum where there is one), as the matrix times
+// the power of two that brings the panel's largest entry into [1, 2), and leaves
+// its part of X X^T.  The Frobenius norm is that product's trace: the first
+// ns_panel divides by it, which saves the two launches that a norm of its own
+// and the division take.
+template <typename T, int MT>
+__global__ __launch_bounds__(256 * MT) void ns_panel_load(Source src, const float* buf_in, float* buf_out,
+                                                          PanelArgs p) {
+    using C = PanelCfg<MT>;
+    constexpr int THREADS = 64 * C::WAVES;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_raw[2 * C::X_PLANE];
+    __shared__ float stage[C::COLS * (C::M + 1) > C::M * (C::COLS + 1) ? C::COLS * (C::M + 1) : C::M * (C::COLS + 1)];
+    __shared__ float red[C::WAVES];
+    const uint32_t x_at = (uint32_t)(uintptr_t)(lds_u8*)&lds_raw[0];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int panel = blockIdx.x, b = blockIdx.y, col0 = panel * C::COLS;
+    const int cols = min(C::COLS, p.np - col0);
+    const int64_t base = (int64_t)b * p.m * p.n;
+    const T* in = static_cast<const T*>(src.m) + base;
+    const float* old = buf_out ? buf_in + base : nullptr;
+    float* fresh = buf_out ? buf_out + base : nullptr;
+
+    // rows of memory that cross the panel, four elements a thread and pass
+    const int real = min(C::COLS, p.n - col0);                     // columns of the matrix, at least 1
+    const int rows = p.tall ? real : p.m, width = p.tall ? p.m : real;
+    const int ld = (p.tall ? C::M : C::COLS) + 1;
+    constexpr int ROWS_MOST = C::COLS > C::M ? C::COLS : C::M, QUADS = ROWS_MOST / 4;
+    constexpr int PASSES = ROWS_MOST * QUADS / THREADS;
+    float v[PASSES][4], o[PASSES][4];
+    auto where = [&](int k, int& r, int& c, int64_t& at) {
+        const int idx = k * THREADS + threadIdx.x;
+        r = idx / QUADS;
+        c = idx % QUADS * 4;
+        at = p.tall ? (int64_t)(col0 + r) * p.m : (int64_t)r * p.n + col0;
+        return r < rows && c < width;
+    };
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        int r, c;
+        int64_t at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = o[k][e] = 0.0f;
+        if (where(k, r, c, at)) {
+            load4(in + at, c, width, v[k]);
+            if (fresh != nullptr) load4(old + at, c, width, o[k]);
+        }
+    }
+    float most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        int r, c;
+        int64_t at;
+        if (!where(k, r, c, at)) continue;
+        if (fresh != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[k][e] = src.beta * o[k][e] + v[k][e];
+                v[k][e] = src.nesterov ? v[k][e] + src.beta * o[k][e] : o[k][e];
+            }
+            store4(fresh + at, c, width, o[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < width) {
+                most = fmaxf(most, fabsf(v[k][e]));   // passes over a NaN, which poisons the sums later
+                stage[r * ld + c + e] = v[k][e];
+            }
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor(most, k));
+    if (lane == 0) red[wave] = most;
+    __syncthreads();
+    for (int w = 0; w < C::WAVES; ++w) most = fmaxf(most, red[w]);
+    // -200: a panel of zeros counts for nothing beside any other
+    const int exponent = most > 0.0f ? (most < INFINITY ? ilogbf(most) : 127) : -200;
+    if (threadIdx.x == 0) p.exponents[b * p.panels + panel] = exponent;
+
+    half_t* xt = p.XT + (size_t)b * 2 * p.xplane + (size_t)col0 * C::M;
+#pragma unroll
+    for (int k = 0; k < C::X_PLANE / 16 / THREADS; ++k) {
+        const int chunk = k * THREADS + threadIdx.x, col = chunk / C::CH, c = chunk % C::CH;
+        halfx8 h, l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = 8 * c + e;
+            const float f = col < real && i < p.m ? stage[p.tall ? col * ld + i : i * ld + col] : 0.0f;
+            const Pair q = split(ldexpf(f, -exponent) * kSX);
+            h[e] = q.h;
+            l[e] = q.l;
+        }
+        const uint32_t at = x_at + C::x_cell(col, 8 * c);
+        *(lds_halfx8*)(uintptr_t)at = h;
+        *(lds_halfx8*)(uintptr_t)(at + C::X_PLANE) = l;
+        if (col < cols) {
+            *reinterpret_cast<halfx8*>(xt + (size_t)col * C::M + 8 * c) = h;
+            *reinterpret_cast<halfx8*>(xt + p.xplane + (size_t)col * C::M + 8 * c) = l;
+        }
+    }
+    __syncthreads();
+    panel_gram<MT>(x_at, cols, p.part_out + ((size_t)b * p.panels + panel) * C::NT * 1024, wave, lane);
+}
 
 template <int MT>
 __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
     using C = PanelCfg<MT>;
     constexpr int THREADS = 64 * C::WAVES;
     __shared__ __attribute__((aligned(1024))) uint8_t lds_raw[C::LDS];
+    __shared__ float red[C::WAVES];
     const uint32_t x_at = (uint32_t)(uintptr_t)(lds_u8*)&lds_raw[0];
     const uint32_t a_at = x_at + 2 * C::X_PLANE;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -1134,13 +1277,17 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
         }
 
     typedef __attribute__((address_space(3))) half_t lds_half;
-    if (!p.first) {
+    float x_scale = 1.0f;   // of the panel: the matrix's norm, once
+    {
         // ---- A from the panels' parts, in order ----
         const floatx4* in = reinterpret_cast<const floatx4*>(p.part_in) + (size_t)b * p.panels * C::NT * 256;
         constexpr int POS = (C::NT * 256 + THREADS - 1) / THREADS;
         floatx4 v[POS];
 #pragma unroll
         for (int k = 0; k < POS; ++k) v[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        int top = -200;   // the panels' largest exponent
+        if (p.raw)
+            for (int q = 0; q < p.panels; ++q) top = max(top, p.exponents[b * p.panels + q]);
         // four panels' reads in flight; past the last panel it is read again and dropped
         for (int q0 = 0; q0 < p.panels; q0 += 4) {
             floatx4 f[4][POS];
@@ -1152,9 +1299,38 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
                                  min(k * THREADS + (int)threadIdx.x, C::NT * 256 - 1)];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (q0 + u < p.panels)
+                if (q0 + u < p.panels) {
+                    const float weight =
+                        p.raw ? ldexpf(1.0f, 2 * (p.exponents[b * p.panels + q0 + u] - top)) : 1.0f;
 #pragma unroll
-                    for (int k = 0; k < POS; ++k) v[k] += f[u][k];
+                    for (int k = 0; k < POS; ++k) v[k] += weight * f[u][k];
+                }
+        }
+        float a_scale = kSA / (kSX * kSX);
+        if (p.raw) {
+            // |M|_F^2 = trace(M M^T), in units of 2^(2 top) / kSX^2
+            float trace = 0.0f;
+#pragma unroll
+            for (int k = 0; k < POS; ++k) {
+                const int group = uniform(C::WAVES * k + wave);
+                if (group >= C::NT * 4) break;
+                int ta = 0;
+                while ((ta + 1) * (ta + 2) / 2 <= group >> 2) ++ta;
+                if ((group >> 2) != ta * (ta + 3) / 2) continue;   // not a diagonal tile
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (8 * (group & 3) + 4 * lg + r == l32) trace += v[k][r];
+            }
+#pragma unroll
+            for (int k = 32; k > 0; k >>= 1) trace += __shfl_xor(trace, k);
+            if (lane == 0) red[wave] = trace;
+            __syncthreads();
+            double sum = 0.0;
+            for (int w = 0; w < C::WAVES; ++w) sum += (double)red[w];
+            const double unit = ldexp(1.0, top);
+            const double r = unit / (sqrt(sum) * (1.0 / kSX) * unit + (double)p.eps);
+            a_scale *= (float)(r * r);
+            x_scale = (float)(r * ldexp(1.0, p.exponents[b * p.panels + panel] - top));
         }
 #pragma unroll
         for (int k = 0; k < POS; ++k) {
@@ -1168,7 +1344,7 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
             halfx4 h, l;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const Pair s = split(v[k][r] * (kSA / (kSX * kSX)));
+                const Pair s = split(v[k][r] * a_scale);
                 h[r] = s.h;
                 l[r] = s.l;
             }
@@ -1259,7 +1435,7 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
                 const int i = 32 * rt + 8 * (e >> 2) + 4 * lg + (e & 3);
                 if (i < p.m && j < p.n)
                     sink_store(p.sink, at0 + (p.tall ? (int64_t)j * p.m + i : (int64_t)i * p.n + j),
-                               y[e] * (1.0f / (kSP * kSX)));
+                               y[e] * (x_scale / (kSP * kSX)));
             }
             return;
         }
@@ -1269,7 +1445,7 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
             halfx4 h, l;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const Pair s = split(y[4 * q + r] * (1.0f / kSP));
+                const Pair s = split(y[4 * q + r] * (x_scale / kSP));
                 h[r] = s.h;
                 l[r] = s.l;
             }
@@ -1288,41 +1464,8 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
                     *reinterpret_cast<halfx8*>(xt + (size_t)pl * p.xplane + (size_t)col * C::M + 8 * c) =
                         *(const lds_halfx8*)(uintptr_t)(x_at + pl * C::X_PLANE + C::x_cell(col, 8 * c));
             }
-    } else {
-        wait_vmcnt<0>();
-        __syncthreads();
     }
-    // ---- this panel's part of X X^T: a lower tile a wave ----
-    float* out = p.part_out + ((size_t)b * p.panels + panel) * C::NT * 1024;
-    if (wave < C::NT) {
-        int ta = 0;
-        while ((ta + 1) * (ta + 2) / 2 <= wave) ++ta;
-        const int tb = wave - ta * (ta + 1) / 2;
-        floatx16 g;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = 0.0f;
-        // this lane's cells of the first 16 columns, for the two halves of a read
-        const int s16 = lane & 15, q16 = lane >> 4;
-        const int col = 8 * (q16 >> 1) + (s16 >> 2), row = 16 * (q16 & 1) + 4 * (s16 & 3);
-        const uint32_t ca[2] = {x_at + C::x_cell(col, 32 * ta + row), x_at + C::x_cell(col + 4, 32 * ta + row)};
-        const uint32_t cb[2] = {x_at + C::x_cell(col, 32 * tb + row), x_at + C::x_cell(col + 4, 32 * tb + row)};
-        for (int kc0 = 0; kc0 < cols / 16; kc0 += 4)   // 64 or 128 columns
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                // 16 columns on, the slots are the same
-                auto turned = [&](const uint32_t (&cell)[2], int pl) {
-                    const uint32_t at = (uint32_t)(pl * C::X_PLANE + (kc0 + u) * 32 * C::M);
-                    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[0] + at));
-                    const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(cell[1] + at));
-                    return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                };
-                g = mfma3(turned(ca, 0), turned(ca, 1), turned(cb, 0), turned(cb, 1), g);
-            }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            reinterpret_cast<floatx4*>(out)[wave * 256 + q * 64 + lane] =
-                floatx4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]};
-    }
+    panel_gram<MT>(x_at, cols, p.part_out + ((size_t)b * p.panels + panel) * C::NT * 1024, wave, lane);
 }
 
 // Whether a matrix takes ns_panel, and its parts of X X^T.  Every panel reads
@@ -1330,9 +1473,10 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
 // products' two further launches a step are worth up to about here (in all 46 us
 // at 64 x 1000 and 91 us at 128 x 1024, against 105 and 117 us tiled).
 bool panel_shape(int m, int n) { return (m <= 64 && n <= 8192) || (m <= 128 && n <= 1536); }
+int panels_of(int np) { return (np + 127) / 128; }
 size_t panel_part_bytes(int mp, int np) {
     const int mt = mp / 32;
-    return (size_t)((np + 127) / 128) * (mt * (mt + 1) / 2) * 4096;
+    return (size_t)panels_of(np) * (mt * (mt + 1) / 2) * 4096;
 }
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -1410,6 +1554,13 @@ Layout layout(int batch, int rows, int cols) {
         at = up(at + bytes, 1024);
         return here;
     };
+    if (panel_shape(l.m, l.n)) {   // two sets of parts: one read, one written
+        l.partial = take((size_t)batch * panels_of(l.np) * sizeof(int));
+        l.XT0 = take((size_t)batch * 2 * l.xplane * sizeof(half_t));
+        l.part = take(2 * batch * panel_part_bytes(l.mp, l.np));
+        l.bytes = at;
+        return l;
+    }
     l.partial = take((size_t)batch * l.nparts * sizeof(double));
     l.X = take((size_t)batch * 2 * l.xplane * sizeof(half_t));
     l.XT0 = take((size_t)batch * 2 * l.xplane * sizeof(half_t));
@@ -1424,7 +1575,6 @@ Layout layout(int batch, int rows, int cols) {
         if (t.splits > 1)
             part = std::max(part, (size_t)batch * (ti * (ti + 1) / 2) * t.splits * side * side * sizeof(float));
     }
-    if (panel_shape(l.m, l.n)) part = 2 * batch * panel_part_bytes(l.mp, l.np);   // one read, one written
     l.part = take(part);
     l.bytes = at;
     return l;
@@ -1533,6 +1683,53 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
 
     const Layout l = layout(c.batch, c.rows, c.cols);
     char* ws = static_cast<char*>(c.workspace);
+    if (panel_shape(l.m, l.n)) {
+        PanelArgs a{};
+        a.XT = reinterpret_cast<half_t*>(ws + l.XT0);
+        a.xplane = l.xplane;
+        a.exponents = reinterpret_cast<int*>(ws + l.partial);
+        a.np = l.np;
+        a.panels = panels_of(l.np);
+        a.m = l.m;
+        a.n = l.n;
+        a.tall = l.tall;
+        a.ca = c.coeffs[0];
+        a.cb = c.coeffs[1];
+        a.cc = c.coeffs[2];
+        a.eps = c.eps;
+        a.sink = sink;
+        char* parts[2] = {ws + l.part, ws + l.part + c.batch * panel_part_bytes(l.mp, l.np)};
+        const dim3 grid(a.panels, c.batch), block(l.mp == 64 ? 512 : 1024);
+        const Source from{c.m, c.momentum_out, c.beta, c.nesterov};
+        a.part_out = reinterpret_cast<float*>(parts[0]);
+        {
+            KernelTimer timer("ns_panel_load", st);
+            const bool f32 = c.m_dtype == DISCO_F32;
+#define DISCO_NS(T, MT) \
+    hipLaunchKernelGGL((ns_panel_load<T, MT>), grid, block, 0, st, from, c.momentum, c.momentum_out, a)
+            if (l.mp == 64) {
+                if (f32) DISCO_NS(float, 2);
+                else DISCO_NS(bf16_t, 2);
+            } else {
+                if (f32) DISCO_NS(float, 4);
+                else DISCO_NS(bf16_t, 4);
+            }
+#undef DISCO_NS
+        }
+        if (int rc = done("ns_panel_load")) return rc;
+        for (int t = 0; t < c.steps; ++t) {
+            a.raw = t == 0;
+            a.last = t + 1 == c.steps;
+            a.part_in = reinterpret_cast<const float*>(parts[t & 1]);
+            a.part_out = reinterpret_cast<float*>(parts[(t + 1) & 1]);
+            KernelTimer timer("ns_panel", st);
+            if (l.mp == 64) hipLaunchKernelGGL(ns_panel<2>, grid, block, 0, st, a);
+            else hipLaunchKernelGGL(ns_panel<4>, grid, block, 0, st, a);
+            if (int rc = done("ns_panel")) return rc;
+        }
+        return DISCO_OK;
+    }
+
     double* partial = reinterpret_cast<double*>(ws + l.partial);
     half_t* X = reinterpret_cast<half_t*>(ws + l.X);
     half_t* XT[2] = {reinterpret_cast<half_t*>(ws + l.XT0), reinterpret_cast<half_t*>(ws + l.XT1)};
@@ -1563,35 +1760,6 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
                                c.eps, l.m, l.n, l.mp, l.np, l.tall, X, XT[0], l.xplane);
         if (int rc = done("ns_load")) return rc;
     }
-    if (panel_shape(l.m, l.n)) {
-        PanelArgs a{};
-        a.XT = XT[0];
-        a.xplane = l.xplane;
-        a.np = l.np;
-        a.panels = (l.np + 127) / 128;
-        a.m = l.m;
-        a.n = l.n;
-        a.tall = l.tall;
-        a.ca = c.coeffs[0];
-        a.cb = c.coeffs[1];
-        a.cc = c.coeffs[2];
-        a.sink = sink;
-        char* parts[2] = {ws + l.part, ws + l.part + c.batch * panel_part_bytes(l.mp, l.np)};
-        for (int t = 0; t <= c.steps; ++t) {
-            a.first = t == 0;
-            a.last = t == c.steps;
-            a.part_in = reinterpret_cast<const float*>(parts[(t + 1) & 1]);
-            a.part_out = reinterpret_cast<float*>(parts[t & 1]);
-            KernelTimer timer("ns_panel", st);
-            if (l.mp == 64)
-                hipLaunchKernelGGL(ns_panel<2>, dim3(a.panels, c.batch), dim3(512), 0, st, a);
-            else
-                hipLaunchKernelGGL(ns_panel<4>, dim3(a.panels, c.batch), dim3(1024), 0, st, a);
-            if (int rc = done("ns_panel")) return rc;
-        }
-        return DISCO_OK;
-    }
-
     // A bfloat16 result takes single float16 products in all but the last two
     // steps, and for X X^T throughout: 2e-4 to 1e-3 off before its own rounding
     // of 1.7e-3.  In the last two steps A's entries are of order one and the

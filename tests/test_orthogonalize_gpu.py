@@ -129,6 +129,17 @@ def test_rows_of_very_different_size(sdc):
     assert float((o.double() - ref).abs().max()) <= 485 * 2.0 ** -23
 
 
+@pytest.mark.parametrize("rows,cols", [(60, 200), (64, 448), (128, 896), (128, 128), (300, 500), (1024, 600)])
+def test_no_single_entry_is_off(sdc, rows, cols):
+    # Two steps amplify by at most a^2 = 12; an operand is off by 2^-22 of its
+    # entry at most, the largest entry is some five times the root mean square:
+    # 12 * 2^-22 * 5 = 1.4e-5 of that.  A hi and a lo part that do not belong
+    # together would put single entries 1e-4 to 1e-3 off, unseen in the norm.
+    m = update(7, 1, rows, cols)
+    d = (sdc.orthogonalize(m, steps=2).double() - ns64(m, 2)).abs()
+    assert float(d.max() / ns64(m, 2).square().mean().sqrt()) <= 2e-5
+
+
 def test_zero_nan_infinity(sdc):
     for rows, cols in ((5, 9), (64, 448), (130, 200), (300, 40)):
         m = update(1, 4, rows, cols)
