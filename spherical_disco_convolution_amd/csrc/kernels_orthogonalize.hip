@@ -1498,14 +1498,15 @@ struct TileChoice {
 constexpr int kSides[4] = {64, 64, 128, 192};
 
 // The choice with the least estimated time.  Times in microseconds as measured
-// from 128 x 896 to 4096 x 4096: a 64-deep slice of one tile with single and
+// from 256 x 256 to 4096 x 4096: a 64-deep slice of one tile with single and
 // with three products, and a tile's start and end.  For instance 1024 x 4096 in
-// float32: X X^T on 136 tiles of 64 takes 29 us, on 36 of 128 71 us, on 64-tiles
-// shared by four 24 us and 2 us for their joining; P X on 512 tiles of 64 takes
-// 42 us, on 256 of 128 30 us.
+// float32: X X^T on 136 tiles of 64 takes 28 us, on 36 of 128 68 us, on 128-tiles
+// shared by seven 17 us and 9 us for their joining; P X on 512 tiles of 64 35 us,
+// on 256 of 128 29 us.  4096 x 4096 in float32: X X^T on 253 tiles of 192 takes
+// 208 us, on 528 of 128 269 us.
 TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric, int np) {
-    static const double slice_us[4][2] = {{0.22, 0.39}, {0.30, 0.65}, {0.45, 1.1}, {1.0, 2.5}};
-    static const double ends_us[4] = {2.0, 2.0, 4.0, 8.0};
+    static const double slice_us[4][2] = {{0.22, 0.39}, {0.30, 0.65}, {0.35, 1.0}, {1.0, 2.5}};
+    static const double ends_us[4] = {2.0, 2.0, 3.5, 8.0};
     TileChoice best;
     double best_us = 1e300;
     for (int kind = 0; kind < 4; ++kind) {
@@ -1613,7 +1614,7 @@ int launch_product(const Product& p, int batch, hipStream_t st) {
     switch (t.kind) {
         case 0: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 4 : 8, E>(p, t.splits, batch, st);
         case 1: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 2 : 4, E>(p, t.splits, batch, st);
-        case 2: return launch_tiles<128, 2, 2, NP, NP == 3 ? 32 : 64, 4, E>(p, t.splits, batch, st);
+        case 2: return launch_tiles<128, 2, 4, NP, NP == 3 ? 32 : 64, 4, E>(p, t.splits, batch, st);
         default: return launch_tiles<192, 2, 2, NP, NP == 3 ? 32 : 64, NP == 3 ? 3 : 2, E>(p, t.splits, batch, st);
     }
 }
