@@ -10,7 +10,9 @@
 //
 // Both directions move each element once and do about ten operations on it,
 // so HBM bounds them; the kernels hold a point's channels in registers
-// between the statistics and the output so that nothing is read twice.
+// between the statistics and the output so that nothing is read twice.  Forward,
+// 721 x 1440 x 128 bf16 with a residual (1.07 GB): 225 us, 4.8 TB/s, where a
+// large copy reaches 4.9 to 5.2.
 // inner > 1 ("field" kernels): a lane owns V neighbouring points, the waves of
 // a workgroup split the channels, and the partial statistics meet in LDS.
 // inner == 1 ("row" kernels): a row's channels are spread over 1 to 1024 lanes.
@@ -671,7 +673,10 @@ __global__ __launch_bounds__(1024) void ln_fwd_row_walk(
 // Backward of rows.  Persistent workgroups of blockDim / tpr row slots; each
 // thread keeps the parameter sums of its channels in registers over all its
 // rows, and the slots are added in LDS, in slot order, at the end, so that a
-// workgroup leaves one row of partial sums.  gamma waits in LDS.
+// workgroup leaves one row of partial sums.  gamma waits in LDS.  16384 rows of
+// 2048 bf16 (201 MB): 58 us, 3.5 TB/s; the 64 sums, the row and gy take 221
+// registers a lane, so eight waves share a compute unit, and keeping the next
+// row in flight as well spills (72 us).
 template <typename TX, typename TG, typename TO, int V, int NV>
 __global__ __launch_bounds__(V * NV > 16 ? 512 : 1024) void ln_bwd_row(
     const TX* __restrict__ x, const TG* __restrict__ gy, const float* __restrict__ mean_in,
@@ -922,7 +927,8 @@ RowShape row_shape(int C, int64_t rows, int v) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch may have at most 2^32 - 1 threads.
+bool fits(int64_t grid, int threads) { return grid <= 0xffffffffLL / threads && grid <= 0x7fffffff; }
 
 int done(const char* what) {
     hipError_t e = hipGetLastError();
@@ -939,14 +945,14 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
     if (inner == 1) {
         const RowShape r = row_shape(C, outer, V16);
         if (r.nv == 0) {
-            if (outer > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many rows");
+            if (!fits(outer, 1024)) return set_error(DISCO_EUNSUPPORTED, "too many rows");
             KernelTimer timer("ln_fwd_row_walk", st);
             hipLaunchKernelGGL((ln_fwd_row_walk<TX, TY, RES>), dim3((unsigned)outer), dim3(1024), 0,
                                st, x, res, gamma, beta, y, s, mean, rstd, C, eps);
             return done("ln_fwd_row_walk");
         }
         const int64_t grid = cdiv(outer, r.threads / r.tpr);
-        if (grid > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many rows");
+        if (!fits(grid, r.threads)) return set_error(DISCO_EUNSUPPORTED, "too many rows");
         KernelTimer timer("ln_fwd_row", st);
 #define DISCO_LN(NV)                                                                             \
     hipLaunchKernelGGL((ln_fwd_row<TX, TY, V16, NV, RES>), dim3((unsigned)grid), dim3(r.threads), 0, \
@@ -960,7 +966,7 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
     const FieldShape f = field_shape(C, kFwdMaxCpw);
     if (f.cpw == 0) {
         const int64_t total = outer * inner, grid = cdiv(total, 64);
-        if (grid > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many points");
+        if (!fits(grid, 1024)) return set_error(DISCO_EUNSUPPORTED, "too many points");
         KernelTimer timer("ln_fwd_field_walk", st);
         hipLaunchKernelGGL((ln_fwd_field_walk<TX, TY, RES>), dim3((unsigned)grid), dim3(64, 16), 0,
                            st, x, res, gamma, beta, y, s, mean, rstd, C, inner, total, eps);
@@ -972,7 +978,7 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
     const bool wide = inner >= vw && outer * cdiv(inner, vw) >= (int64_t)512 * 64 * f.wp;
     const int V = wide ? vw : 1;
     const int64_t groups = cdiv(inner, V), total = outer * groups, grid = cdiv(total, 64 * f.wp);
-    if (grid > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many points");
+    if (!fits(grid, 64 * f.wc * f.wp)) return set_error(DISCO_EUNSUPPORTED, "too many points");
     const size_t lds = f.wc > 1 ? (size_t)f.wc * f.wp * 128 * V * sizeof(float) : 0;
     KernelTimer timer("ln_fwd_field", st);
 #define DISCO_LN(VV, CPW)                                                                        \
@@ -1053,7 +1059,7 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
     if (inner == 1) {
         const BwdRowShape r = bwd_row_shape(C, outer, VR);
         if (r.nv == 0) {
-            if (outer > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many rows");
+            if (!fits(outer, 1024)) return set_error(DISCO_EUNSUPPORTED, "too many rows");
             if (gx != nullptr) {
                 KernelTimer timer("ln_bwd_row_walk", st);
                 hipLaunchKernelGGL((ln_bwd_row_walk<TX, TG, TO>), dim3((unsigned)outer), dim3(1024),
@@ -1087,7 +1093,7 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
         const FieldShape f = field_shape(C, kBwdMaxCpw);
         if (f.cpw == 0) {
             const int64_t total = outer * inner, grid = cdiv(total, 64);
-            if (grid > kMaxGrid) return set_error(DISCO_EUNSUPPORTED, "too many points");
+            if (!fits(grid, 1024)) return set_error(DISCO_EUNSUPPORTED, "too many points");
             if (gx != nullptr) {
                 KernelTimer timer("ln_bwd_field_walk", st);
                 hipLaunchKernelGGL((ln_bwd_field_walk<TX, TG, TO>), dim3((unsigned)grid),

@@ -68,7 +68,7 @@ FIELDS = [(1, 4, 33, 64), (1, 1, 5, 7), (2, 3, 9, 16), (3, 8, 1, 2), (1, 17, 12,
           (1, 512, 45, 91), (2, 600, 7, 9), (300, 6, 3, 1), (1, 128, 361, 720), (1, 16, 721, 1439),
           (5, 24, 181, 359)]
 ROWS = [(1, 1), (3, 5), (1, 7), (300, 8), (2, 16), (70, 63), (5, 64), (129, 129), (1, 1000), (9, 2048),
-        (5000, 96), (2500, 2049), (4100, 31), (2, 4099), (3000, 4100), (1, 16384), (3, 16385), (2, 40001), (1, 1)]
+        (5000, 96), (2500, 2049), (4100, 31), (2, 4099), (3000, 4100), (600, 8192), (520, 8200), (1, 16384), (3, 16385), (2, 40001), (1, 1)]
 CASES = [(s, 1) for s in FIELDS] + [(s, -1) for s in ROWS]
 TYPES = [(F32, F32, False), (F32, BF16, True), (BF16, BF16, True), (BF16, F32, False), (BF16, BF16, False)]
 
