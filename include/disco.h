@@ -328,13 +328,15 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
  * bfloat16 rounding of it (single float16 products in all but the last two
  * steps).  steps lies in 1..64.  coeffs: three floats in HOST memory, or NULL
  * for 3.4445, -4.7750, 2.0315; EUNSUPPORTED where they would carry the
- * singular values out of the operands' range (above about 3.5).  A NaN or an
+ * singular values (above about 3.5) or the polynomial a + b s^2 + c s^4 (above
+ * 24) out of the operands' range.  A NaN or an
  * infinity anywhere in a matrix makes its whole result NaN; a zero matrix
  * stays zero (eps > 0).  Results do not depend on the other matrices of the
  * batch and are reproducible. */
 
-/* Bytes of device workspace that the two calls below need, or a negative
- * status (EUNSUPPORTED for more than 65535 matrices). */
+/* Bytes of device workspace that the two calls below need (none for matrices
+ * that one workgroup holds: up to 32 x 512 or 64 x 256, either way up), or a
+ * negative status (EUNSUPPORTED for more than 65535 matrices). */
 int64_t disco_orthogonalize_workspace(int32_t batch, int32_t rows, int32_t cols);
 
 /* o = the orthogonalised m; m [batch, rows, cols] of m_dtype, o of o_dtype. */

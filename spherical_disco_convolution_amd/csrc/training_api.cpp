@@ -68,19 +68,21 @@ int check_ortho(int32_t batch, int32_t rows, int32_t cols, int32_t steps, const 
         out_coeffs[k] = c[k];
     }
     // The singular values start in [0, 1] and go through s (a + b s^2 + c s^4)
-    // step by step; X X^T and the polynomial have to stay in the range of the
-    // scaled float16 operands (16 and 32; a quarter is left to sampling).
+    // step by step; X X^T, the polynomial's part in s and a + that part have to
+    // stay in the range of the scaled float16 operands (16, 32 and 32; a quarter
+    // is left to sampling).
     double hi = 1.0;
     for (int k = 0; k < steps; ++k) {
         double next = 0.0, poly = 0.0;
         for (int q = 0; q <= 64; ++q) {
             const double s = hi * q / 64.0, s2 = s * s, p = s2 * (c[1] + c[2] * s2);
-            poly = std::max(poly, std::fabs(p));
+            poly = std::max(poly, std::max(std::fabs(p), std::fabs(c[0] + p)));
             next = std::max(next, std::fabs(s * (c[0] + p)));
         }
         if (hi * hi > 12.0 || poly > 24.0)
-            return set_error(DISCO_EUNSUPPORTED, "with these coefficients the singular values grow "
-                             "to %.3g at step %d: out of the operands' range", hi, k + 1);
+            return set_error(DISCO_EUNSUPPORTED, "with these coefficients the singular values reach "
+                             "%.3g and the polynomial %.3g at step %d: out of the operands' range",
+                             hi, poly, k + 1);
         hi = next;
     }
     return DISCO_OK;

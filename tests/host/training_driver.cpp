@@ -144,6 +144,7 @@ int main() {
     expect(ortho(T(0), T(1), 2, 30, 40, 5, nullptr, 1e-7f, T(1), 4096), EI, "workspace on the result");
     const float wild[3] = {50.0f, 0.0f, 0.0f}, nan[3] = {NAN, 0.0f, 0.0f}, mild[3] = {2.0f, -1.5f, 0.5f};
     expect(ortho(T(0), T(1), 2, 30, 40, 5, wild, 1e-7f, T(2), 4096), EU, "growing coefficients");
+    expect(ortho(T(0), T(1), 2, 30, 40, 1, wild, 1e-7f, T(2), 4096), EU, "one step of large coefficients");
     expect(ortho(T(0), T(1), 2, 30, 40, 5, nan, 1e-7f, T(2), 4096), EI, "NaN coefficient");
     expect(ortho(T(0), T(1), 2, 30, 40, 64, mild, 1e-7f, T(2), 4096), OK, "other coefficients");
     expect(ortho(nullptr, nullptr, 0, 30, 40, 5, nullptr, 1e-7f, nullptr, 0), OK, "empty");

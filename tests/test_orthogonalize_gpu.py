@@ -264,6 +264,8 @@ def test_refusals(sdc):
         sdc.orthogonalize(m, coeffs=(float("nan"), 0.0, 0.0))
     with pytest.raises(NotImplementedError):
         sdc.orthogonalize(m, coeffs=(50.0, 0.0, 0.0))
+    with pytest.raises(NotImplementedError):
+        sdc.orthogonalize(m, steps=1, coeffs=(50.0, 0.0, 0.0))
     with pytest.raises(ValueError):
         sdc.orthogonalize(m.cpu())
     w = randn(1, (8, 12))
