@@ -11,7 +11,7 @@
 // Both directions move each element once and do about ten operations on it,
 // so HBM bounds them; the kernels hold a point's channels in registers
 // between the statistics and the output so that nothing is read twice.  Forward,
-// 721 x 1440 x 128 bf16 with a residual (1.07 GB): 225 us, 4.8 TB/s, where a
+// 721 x 1440 x 128 bf16 with a residual (1.07 GB): 228 us, 4.7 TB/s, where a
 // large copy reaches 4.9 to 5.2.
 // inner > 1 ("field" kernels): a lane owns V neighbouring points, the waves of
 // a workgroup split the channels, and the partial statistics meet in LDS.
@@ -562,6 +562,28 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
     return t;
 }
 
+// Two sums at once in a loop over rows: one barrier, the caller alternating
+// between two places of 32 floats from one row to the next.
+__device__ __forceinline__ void row_sums(float& a, float& b, int tpr, float* red) {
+    for (int m = min(tpr, 64) >> 1; m > 0; m >>= 1) {
+        a += __shfl_xor(a, m);
+        b += __shfl_xor(b, m);
+    }
+    if (tpr <= 64) return;
+    const int wave = threadIdx.x >> 6, n = tpr >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        red[2 * wave] = a;
+        red[2 * wave + 1] = b;
+    }
+    __syncthreads();
+    const float* mine = red + 2 * (wave / n * n);
+    a = b = 0.0f;
+    for (int k = 0; k < n; ++k) {
+        a += mine[2 * k];
+        b += mine[2 * k + 1];
+    }
+}
+
 // A row's C channels over tpr threads, thread t holding vectors t, t + tpr, ...
 template <typename TX, typename TY, int V, int NV, bool RES>
 __global__ __launch_bounds__(1024) void ln_fwd_row(
@@ -673,19 +695,20 @@ __global__ __launch_bounds__(1024) void ln_fwd_row_walk(
 // Backward of rows.  Persistent workgroups of blockDim / tpr row slots; each
 // thread keeps the parameter sums of its channels in registers over all its
 // rows, and the slots are added in LDS, in slot order, at the end, so that a
-// workgroup leaves one row of partial sums.  gamma waits in LDS.  16384 rows of
-// 2048 bf16 (201 MB): 58 us, 3.5 TB/s; the 64 sums, the row and gy take 221
-// registers a lane, so eight waves share a compute unit, and keeping the next
-// row in flight as well spills (72 us).
+// workgroup leaves one row of partial sums.  gamma waits in LDS.  HBM bounds it:
+// 16384 rows of 2048 bf16 (201 MB) take 51 us, 3.9 TB/s, the second launch 4 us
+// of them (46 us repeated on the same tensors, whose 201 MB the last cache partly
+// keeps); the same in float32 85 us, 4.7 TB/s.
 template <typename TX, typename TG, typename TO, int V, int NV>
-__global__ __launch_bounds__(V * NV > 16 ? 512 : 1024) void ln_bwd_row(
+__global__ __launch_bounds__(1024) void ln_bwd_row(
     const TX* __restrict__ x, const TG* __restrict__ gy, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const float* __restrict__ gamma,
     const TG* __restrict__ gsum, TO* __restrict__ gx, float* __restrict__ partial, int C,
     int64_t rows, int tpr) {
-    extern __shared__ __attribute__((aligned(16))) float lds[];   // 16 floats, then gamma or the sums
+    extern __shared__ __attribute__((aligned(16))) float lds[];   // 64 floats, then gamma or the sums
     float* red = lds;
-    float* vec = lds + 16;
+    float* vec = lds + 64;
+    int odd = 0;
     const int t = threadIdx.x & (tpr - 1);
     const int slots = blockDim.x / tpr, slot = threadIdx.x / tpr;
     float dg[NV][V], db[NV][V];
@@ -738,8 +761,10 @@ __global__ __launch_bounds__(V * NV > 16 ? 512 : 1024) void ln_bwd_row(
             vx[j].keep_packed();
             vg[j].keep_packed();
         }
-        s1 = row_sum(s1, tpr, red) * rc;
-        s2 = row_sum(s2, tpr, red) * rc;
+        row_sums(s1, s2, tpr, red + odd);
+        odd ^= 32;
+        s1 *= rc;
+        s2 *= rc;
         if (gx != nullptr && active) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
@@ -853,25 +878,25 @@ __global__ __launch_bounds__(256) void ln_bwd_row_params_walk(
     partial[(size_t)blockIdx.y * 2 * C + C + c] = q;
 }
 
-// ggamma and gbeta from partial[n][2][C]: 8 columns a workgroup, the rows in 32
+// ggamma and gbeta from partial[n][2][C]: 16 columns a workgroup, the rows in 64
 // interleaved slices, added in a fixed order.
-__global__ __launch_bounds__(256) void ln_reduce_params(const float* __restrict__ partial, int n,
-                                                        int C, float* __restrict__ ggamma,
-                                                        float* __restrict__ gbeta) {
-    __shared__ float red[32][9];
-    const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
-    const int64_t i = (int64_t)blockIdx.x * 8 + col;
+__global__ __launch_bounds__(1024) void ln_reduce_params(const float* __restrict__ partial, int n,
+                                                         int C, float* __restrict__ ggamma,
+                                                         float* __restrict__ gbeta) {
+    __shared__ float red[64][17];
+    const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const int64_t i = (int64_t)blockIdx.x * 16 + col;
     float a = 0.0f;
     if (i < 2 * (int64_t)C) {
 #pragma unroll 8
-        for (int k = slice; k < n; k += 32) a += partial[(size_t)k * 2 * C + i];
+        for (int k = slice; k < n; k += 64) a += partial[(size_t)k * 2 * C + i];
     }
     red[slice][col] = a;
     __syncthreads();
     if (slice == 0 && i < 2 * (int64_t)C) {
         a = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) a += red[k][col];
+        for (int k = 0; k < 64; ++k) a += red[k][col];
         if (i < C) {
             if (ggamma) ggamma[i] = a;
         } else if (gbeta) {
@@ -935,6 +960,17 @@ int done(const char* what) {
     if (e != hipSuccess)
         return set_error(DISCO_EHIP, "%s launch failed: %s", what, hipGetErrorString(e));
     return DISCO_OK;
+}
+
+template <typename K>
+int allow_lds(K* kernel, size_t bytes) {
+    if (bytes <= 65536) return DISCO_OK;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) return DISCO_OK;
+    (void)hipGetLastError();
+    return set_error(DISCO_EHIP, "layer norm: %zu bytes of LDS refused: %s", bytes,
+                     hipGetErrorString(e));
 }
 
 template <typename TX, typename TY, bool RES>
@@ -1001,8 +1037,13 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
     return done("ln_fwd_field");
 }
 
-// The backward kernel's: rows share a workgroup as long as that leaves one for
-// each of 256 compute units, since each workgroup leaves a row of partial sums.
+// The backward kernel's.  One vector a thread and 512 threads a workgroup, two of
+// them a compute unit: 16384 rows of 2048 bf16 take 46 us, with four vectors (64
+// sums a thread, one workgroup a unit) 62 us, repeated on the same tensors.  Fewer than
+// 8192 rows over 512 threads and more get workgroups of 1024, one a unit: half as
+// many rows of partial sums (1024 rows of 4096 bf16: 21 us against 29; 16384 of
+// 2048 float32: 103 us against 85), and up to 16 channels a thread to leave room
+// for two rows (4096 rows of 8192 bf16: 52 us against 62).
 struct BwdRowShape : RowShape {
     int slots = 0;
     int grid = 0;
@@ -1010,22 +1051,18 @@ struct BwdRowShape : RowShape {
 
 BwdRowShape bwd_row_shape(int C, int64_t rows, int v) {
     BwdRowShape r;
-    static_cast<RowShape&>(r) = row_shape(C, rows, v);
-    if (r.nv == 0 || C > 16384) {   // past 16 channels a lane of 1024
-        r.nv = 0;
-        return r;
-    }
-    if (C > 8192 && r.tpr < 1024) {   // the slots' sums would need more than 64 KB of LDS
-        r.tpr = 1024;
-        r.nv = 1;
-        while ((int64_t)r.tpr * r.nv * v < C) r.nv *= 2;
-    }
+    const int vecs = (int)(((int64_t)C + v - 1) / v);
+    if (C > 16384) return r;   // walk kernels
+    r.tpr = 1;
+    while (r.tpr < vecs && r.tpr < 512) r.tpr *= 2;
+    if (16 * r.tpr < C) r.tpr = 1024;
+    r.nv = 1;
+    while (r.tpr * r.nv < vecs) r.nv *= 2;
+    const int most = r.tpr >= 512 && rows < 8192 ? 1024 : 512;
     r.slots = std::max(1, 256 / r.tpr);
-    // 32 channels a lane and their sums take more than 128 registers
-    const int most = v * r.nv > 16 ? 512 : 1024;
     while (r.slots * 2 * r.tpr <= most && rows >= (int64_t)256 * 2 * r.slots) r.slots *= 2;
     r.threads = r.slots * r.tpr;
-    r.grid = (int)std::min<int64_t>(r.threads >= 512 ? 256 : 512, cdiv(rows, r.slots));
+    r.grid = (int)std::min<int64_t>(r.threads > 512 ? 256 : 512, cdiv(rows, r.slots));
     return r;
 }
 
@@ -1077,15 +1114,18 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
         } else {
             n = r.grid;
             const size_t lds =
-                (16 + std::max<size_t>((size_t)r.nv * r.tpr * VR, r.slots > 1 ? 2 * (size_t)C : 0)) *
-                sizeof(float);
+                (64 + std::max<size_t>((size_t)r.nv * r.tpr * VR, r.slots > 1 ? 2 * (size_t)C : 0)) *
+                sizeof(float);   // up to 64.25 KB
             KernelTimer timer("ln_bwd_row", st);
 #define DISCO_LN(NV)                                                                               \
-    hipLaunchKernelGGL((ln_bwd_row<TX, TG, TO, VR, NV>), dim3(n), dim3(r.threads), lds, st, x, gy, \
-                       mean, rstd, gamma, gsum, gx, part, C, outer, r.tpr)
+    do {                                                                                           \
+        if (int rc = allow_lds(&ln_bwd_row<TX, TG, TO, VR, NV>, lds)) return rc;                   \
+        hipLaunchKernelGGL((ln_bwd_row<TX, TG, TO, VR, NV>), dim3(n), dim3(r.threads), lds, st, x, \
+                           gy, mean, rstd, gamma, gsum, gx, part, C, outer, r.tpr);                \
+    } while (0)
             if (r.nv == 1) DISCO_LN(1);
             else if (r.nv == 2) DISCO_LN(2);
-            else DISCO_LN(4);
+            else if constexpr (VR == 4) DISCO_LN(4);   // 16 channels at most
 #undef DISCO_LN
             if (int rc = done("ln_bwd_row")) return rc;
         }
@@ -1138,8 +1178,8 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
     }
     if (!params) return DISCO_OK;
     KernelTimer timer("ln_reduce_params", st);
-    hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(2 * (int64_t)C, 8)), dim3(256), 0, st,
-                       partial, n, C, ggamma, gbeta);
+    hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(2 * (int64_t)C, 16)), dim3(1024), 0,
+                       st, partial, n, C, ggamma, gbeta);
     return done("ln_reduce_params");
 }
 

@@ -467,10 +467,10 @@ __device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t total) {
 }
 
 // Tile number -> tile row and column, by bands of kBand tile rows, column by
-// column within a band, so that neighbouring numbers form squares: with
-// die_order the products of 4096 x 4096 fetch a quarter less time (a die's 64
-// tiles of 128 read 16 row panels instead of up to 34).  Symmetric results have
-// the lower triangle only.
+// column within a band, so that neighbouring numbers form squares and a die's
+// tiles share operands in its L2: in all 2643 us at 4096 x 4096
+// bf16 and 419 us at 1024 x 4096 float32, without die_order 2772 and 447 us, with
+// neither it nor bands 2666 and 449 us.  Symmetric results have the lower triangle only.
 constexpr int kBand = 8;
 
 template <Epilogue E>
@@ -1075,7 +1075,7 @@ SmallShape small_shape(int m, int n) {
     SmallShape s;
     const int blocks = (n + 31) / 32, mt = (m + 31) / 32;
     // 32 x 512 and 64 x 256; past that a step on one compute unit takes longer
-    // than a launch over several (64 x 448: 57 us here, 44 us by ns_panel)
+    // than a launch over several (64 x 448: 42 us here, 38 us by ns_panel)
     if (mt > 2 || blocks > (mt == 1 ? 16 : 8)) return s;
     s.mt = mt;
     s.cb = 1;
@@ -1478,8 +1478,8 @@ __global__ __launch_bounds__(256 * MT) void ns_panel(PanelArgs p) {
 
 // Whether a matrix takes ns_panel, and its parts of X X^T.  Every panel reads
 // all parts: 0.1 us a part and step for 64 rows, 0.4 us for 128, which the tiled
-// products' two further launches a step are worth up to about here (in all 46 us
-// at 64 x 1000 and 91 us at 128 x 1024, against 105 and 117 us tiled).
+// products' two further launches a step are worth up to about here (in all 38 us
+// at 64 x 448 and 84 us at 128 x 896, against 80 and 119 us tiled).
 bool panel_shape(int m, int n) { return (m <= 64 && n <= 8192) || (m <= 128 && n <= 1536); }
 int panels_of(int np) { return (np + 127) / 128; }
 size_t panel_part_bytes(int mp, int np) {
@@ -1508,10 +1508,12 @@ constexpr int kSides[4] = {64, 64, 128, 192};
 // The choice with the least estimated time.  Times in microseconds as measured
 // from 256 x 256 to 4096 x 4096: a 64-deep slice of one tile with single and
 // with three products, and a tile's start and end.  For instance 1024 x 4096 in
-// float32: X X^T on 136 tiles of 64 takes 28 us, on 36 of 128 68 us, on 128-tiles
-// shared by seven 17 us and 9 us for their joining; P X on 512 tiles of 64 35 us,
-// on 256 of 128 29 us.  4096 x 4096 in float32: X X^T on 253 tiles of 192 takes
-// 208 us, on 528 of 128 269 us.
+// float32: X X^T on 136 tiles of 64 takes 32 us, on 36 of 128 73 us, on 128-tiles
+// shared by seven 23 us and 7 us more for their joining; P X on 1024 tiles of 64
+// 41 to 45 us, on 256 of 128 35 us, on 132 of 192 57 us.  4096 x 4096 in bfloat16: X X^T
+// on 253 tiles of 192 takes 92 us, on 528 of 128 114 us; P X with three products
+// on 1024 of 128 417 us, on 484 of 192 411 us, over a call's first four
+// steps 236 and 253 us each on average.
 TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric, int np) {
     static const double slice_us[4][2] = {{0.22, 0.39}, {0.30, 0.65}, {0.35, 1.0}, {1.0, 2.5}};
     static const double ends_us[4] = {2.0, 2.0, 3.5, 8.0};

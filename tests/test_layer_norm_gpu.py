@@ -131,6 +131,13 @@ def test_backward(sdc, shape, axis):
         assert par[0] is None and torch.equal(par[1], gg) and torch.equal(par[2], gb)
 
 
+# one, two, four and more rows a workgroup, one and several rounds, a last round that is not full
+@pytest.mark.parametrize("rows,C", [(1031, 4096), (511, 4097), (1025, 8192), (1300, 2400), (2600, 777), (2049, 513),
+                                    (9000, 129), (260, 12345)])
+def test_backward_rows_of_a_workgroup(sdc, rows, C):
+    test_backward(sdc, (rows, C), -1)
+
+
 @pytest.mark.parametrize("shape,axis", [((2, 12, 9, 14), 1), ((40, 24), -1)])
 def test_gradient_against_differences(sdc, shape, axis):
     # central differences of L = sum(gy y + gs s) along random directions; step
