@@ -325,13 +325,42 @@ __global__ __launch_bounds__(1024) void ln_fwd_field_walk(
     }
 }
 
+__device__ __forceinline__ float lane_of(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Sums of N values over a wave's lanes.  Each step a lane passes on the half of
+// its values that the lane across keeps, N - 1 exchanges and then one a step for
+// the last value instead of 6 N: at the end of a workgroup of 16 waves those
+// take longer than a tile (four fields of 256 channels and 65 x 128 points, bf16:
+// 29 us in all against 43).  Both halves are read before the choice, which keeps
+// them in registers (chosen first: 80 us).  Returns which value's sum v[0] is; lanes that differ in
+// the last 6 - log2(N) bits hold the same.
+template <int N>
+__device__ __forceinline__ int spread_sums(float* v, int lane) {
+    int which = 0, m = 32;
+#pragma unroll
+    for (int half = N / 2; half > 0; half /= 2, m /= 2) {
+        const bool upper = (lane & m) != 0;
+        which += upper ? half : 0;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const float low = v[k], high = v[k + half];
+            v[k] = (upper ? high : low) + __shfl_xor(upper ? low : high, m);
+        }
+    }
+#pragma unroll
+    for (m = 32 / N; m > 0; m /= 2) v[0] += __shfl_xor(v[0], m);
+    return which;
+}
+
 // Backward of a field.  Persistent workgroups walk tiles of 64 V points; each
 // lane keeps its channels' ggamma and gbeta in registers over all its tiles,
 // and a workgroup's sums go to partial[block * WP + wp][2][C] at the end.
 //
 // At C = 128 bf16 with gsum (721 x 1440, 1.07 GB) the tile is two points a lane:
 // 110 registers, so that two workgroups of 8 waves share a compute unit and one
-// loads while the other waits for its sums: 242 us, 4.4 TB/s.  Four points a
+// loads while the other waits for its sums: 236 us, 4.5 TB/s.  Four points a
 // lane spill (367 us), and loading the next tile ahead with 244 registers and
 // one workgroup a unit comes to 281 us.
 template <typename TX, typename TG, typename TO, int V, int CPW, int WAVES>
@@ -344,6 +373,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ln_bwd_field(
     const int lane = threadIdx.x, WC = blockDim.y, WP = blockDim.z;
     const int wc = uniform(threadIdx.y), wp = uniform(threadIdx.z);
     const int c0 = wc * CPW, nc = min(CPW, C - c0);
+    // read once and kept by a lane each: loads among the products would wait one by one
+    const float mine_of_gamma = gamma ? gamma[c0 + min(lane, nc - 1)] : 1.0f;
     float dg[CPW], db[CPW];
 #pragma unroll
     for (int i = 0; i < CPW; ++i) dg[i] = db[i] = 0.0f;
@@ -380,7 +411,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ln_bwd_field(
 #pragma unroll
         for (int i = 0; i < CPW; ++i)
             if (i < nc) {
-                const float ga = gamma ? gamma[c0 + i] : 1.0f;
+                const float ga = lane_of(mine_of_gamma, i);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float gr = vg[i].get(e);
@@ -429,7 +460,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ln_bwd_field(
 #pragma unroll
             for (int i = 0; i < CPW; ++i)
                 if (i < nc) {
-                    const float ga = gamma ? gamma[c0 + i] : 1.0f;
+                    const float ga = lane_of(mine_of_gamma, i);
                     float f[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
@@ -445,20 +476,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ln_bwd_field(
     }
     if (partial != nullptr) {
         float* row = partial + ((size_t)blockIdx.x * WP + wp) * 2 * C;
+        float v[2 * CPW];
 #pragma unroll
-        for (int i = 0; i < CPW; ++i)
-            if (i < nc) {
-                float a = dg[i], q = db[i];
-#pragma unroll
-                for (int m = 32; m > 0; m >>= 1) {
-                    a += __shfl_xor(a, m);
-                    q += __shfl_xor(q, m);
-                }
-                if (lane == 0) {
-                    row[c0 + i] = a;
-                    row[C + c0 + i] = q;
-                }
-            }
+        for (int i = 0; i < CPW; ++i) {
+            v[i] = dg[i];
+            v[CPW + i] = db[i];
+        }
+        const int i = spread_sums<2 * CPW>(v, lane), c = i % CPW;
+        if ((lane & (32 / CPW - 1)) == 0 && c < nc) row[(i / CPW) * C + c0 + c] = v[0];
     }
 }
 
