@@ -322,11 +322,12 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
  * values are all near one:
  *   X = M / (|M|_F + eps)
  *   steps times: A = X X^T, X <- a X + (b A + c A^2) X      (coeffs = a, b, c)
- * (X^T in X's place where rows > cols: the same map).  Accuracy goes by the
- * result's type: a float32 result has float32 accuracy (operands as pairs of
- * float16, three matrix-core products for one); a bfloat16 result is within a
- * bfloat16 rounding of it (single float16 products in all but the last two
- * steps).  steps lies in 1..64.  coeffs: three floats in HOST memory, or NULL
+ * (X^T in X's place where rows > cols: the same map).  Operands are pairs of
+ * float16 (22 bits) and sums float32, whatever the types; the result is rounded
+ * once to its own, so that a bfloat16 result is the float32 one rounded.  Before
+ * that it is within 1e-5 (relative, of the whole matrix) for five default steps; a
+ * further step can amplify its error by up to a, as in any float32 arithmetic.
+ * steps lies in 1..64.  coeffs: three floats in HOST memory, or NULL
  * for 3.4445, -4.7750, 2.0315; EUNSUPPORTED where they would carry the
  * singular values (above about 3.5) or the polynomial a + b s^2 + c s^4 (above
  * 24) out of the operands' range.  A NaN or an

@@ -636,8 +636,8 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
                   stream=None):
     """Newton-Schulz orthogonalisation of a matrix [rows, cols] or of each
     matrix of a batch [batch, rows, cols]: singular values near one, singular
-    vectors kept.  The result has out_dtype, or m's dtype, and that type's
-    accuracy.  coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
+    vectors kept.  The result is computed to float32 accuracy and rounded to
+    out_dtype, or m's dtype.  coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
     torch = _torch()
     if m.dim() not in (2, 3):
         raise ValueError("m must be [rows, cols] or [batch, rows, cols]")

@@ -10,7 +10,11 @@
 // a third of the float16 rate, five times that of the float32 matrix
 // instructions.  bfloat16 operands would lose too much: the map f(s) = a s +
 // b s^3 + c s^5 amplifies small singular values by up to a^steps, and 8-bit
-// operands leave results 1 to 10 percent off.  The caller has checked that
+// operands leave results 1 to 10 percent off.  Single float16 products in the
+// first steps of a bfloat16 result were no way either: 2e-3 off after five steps
+// with one strong direction over equal ones a fifth as large, 1e-1 after sixteen,
+// where the result's own rounding is 1.7e-3.  So every result is computed the
+// same way and rounded once, to its type.  The caller has checked that
 // singular values stay below 3.5 and the polynomial below 24, so the scales
 // below keep every entry inside float16's range, and the lo parts' granularity
 // is 2^-36.
@@ -306,10 +310,9 @@ struct Product {
     float* part;              // [batch][tile][split][BM * BN] where splits > 1
     // results and other operands
     half_t *out, *out_t;      // [i][j] and [j][i] (hi, lo); kGram / kPoly: one symmetric matrix
-    const half_t* add;        // kPoly: A; kStep: X^T as [j][i], or NULL
+    const half_t* add;        // kPoly: A
     size_t o_plane, add_plane;
     int ld_out, ld_t;         // row strides of out and out_t (and add)
-    int lo_out, lo_t;         // whether the lo planes of out, out_t are wanted
     float ca, cb;             // factors of `add` and of the accumulated product
     float diagonal;           // added where i == j (kPoly)
     int m, n, tall;           // kLast: true sizes and orientation
@@ -363,38 +366,33 @@ __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN]
         for (int c = 0; c < TN; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[a][c][e] *= p.cb;
-    if constexpr (E == kPoly || E == kStep) {
-        if (p.add != nullptr) {
-            half_t* add = const_cast<half_t*>(p.add) + (size_t)b * 2 * p.add_plane + (size_t)jb * p.ld_t + ib;
-#pragma unroll
-            for (int pl = 0; pl < 2; ++pl) {
-                IO::template move<TN * 32, TM * 4, true>(add + (size_t)pl * p.add_plane, p.ld_t, rows_j,
-                                                         rows_i, piece, IO::ROW_T, lane);
-                wave_fence();
-#pragma unroll
-                for (int a = 0; a < TM; ++a)
-#pragma unroll
-                    for (int c = 0; c < TN; ++c)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const halfx4 x = *(const lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[a][c][4 * q + e] += p.ca * (float)x[e];
-                        }
-                wave_fence();
-            }
-        }
-    }
     if constexpr (E == kPoly) {
-        if (p.diagonal != 0.0f)
+        half_t* add = const_cast<half_t*>(p.add) + (size_t)b * 2 * p.add_plane + (size_t)jb * p.ld_t + ib;
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl) {
+            IO::template move<TN * 32, TM * 4, true>(add + (size_t)pl * p.add_plane, p.ld_t, rows_j,
+                                                     rows_i, piece, IO::ROW_T, lane);
+            wave_fence();
 #pragma unroll
             for (int a = 0; a < TM; ++a)
 #pragma unroll
                 for (int c = 0; c < TN; ++c)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (ib + 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3) == jb + 32 * c + l32)
-                            acc[a][c][e] += p.diagonal;
+                    for (int q = 0; q < 4; ++q) {
+                        const halfx4 x = *(const lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[a][c][4 * q + e] += p.ca * (float)x[e];
+                    }
+            wave_fence();
+        }
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int c = 0; c < TN; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (ib + 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3) == jb + 32 * c + l32)
+                        acc[a][c][e] += p.diagonal;
     }
     if constexpr (E == kLast) {
         const int64_t at0 = (int64_t)b * p.m * p.n;
@@ -416,28 +414,25 @@ __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN]
         const bool both = E == kStep || off_diagonal;
 #pragma unroll
         for (int pl = 0; pl < 2; ++pl) {
-            if (pl == 1 && !p.lo_t && !p.lo_out) break;
-            if (pl == 0 || p.lo_t) {
 #pragma unroll
-                for (int a = 0; a < TM; ++a)
+            for (int a = 0; a < TM; ++a)
 #pragma unroll
-                    for (int c = 0; c < TN; ++c)
+                for (int c = 0; c < TN; ++c)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            halfx4 h;
+                    for (int q = 0; q < 4; ++q) {
+                        halfx4 h;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const Pair s = split(acc[a][c][4 * q + e]);
-                                h[e] = pl ? s.l : s.h;
-                            }
-                            *(lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane) = h;
+                        for (int e = 0; e < 4; ++e) {
+                            const Pair s = split(acc[a][c][4 * q + e]);
+                            h[e] = pl ? s.l : s.h;
                         }
-                wave_fence();
-                IO::template move<TN * 32, TM * 4, false>(out_t + (size_t)pl * p.o_plane, p.ld_t, rows_j,
-                                                          rows_i, piece, IO::ROW_T, lane);
-                wave_fence();
-            }
-            if (both && (pl == 0 || p.lo_out)) {
+                        *(lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane) = h;
+                    }
+            wave_fence();
+            IO::template move<TN * 32, TM * 4, false>(out_t + (size_t)pl * p.o_plane, p.ld_t, rows_j,
+                                                      rows_i, piece, IO::ROW_T, lane);
+            wave_fence();
+            if (both) {
                 typedef __attribute__((address_space(3))) half_t lds_half;
 #pragma unroll
                 for (int a = 0; a < TM; ++a)
@@ -515,11 +510,11 @@ __device__ __forceinline__ void tile_of(int tile, int tiles_i, int tiles_j, int&
 // ns_join.  (The last of them could add the parts itself, but the fence that
 // makes them visible writes back a die's whole L2: 65 us against 24 with the
 // second launch at 1024 x 4096.)
-template <int BM, int BN, int WM, int WN, int NP, int BK, int NS, Epilogue E>
-__global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * (NP == 3 ? 2 : 1) * 2 * BK > 81920 ? 1 : 2) void ns_product(
+template <int BM, int BN, int WM, int WN, int BK, int NS, Epilogue E>
+__global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * 4 * BK > 81920 ? 1 : 2) void ns_product(
     Product p) {
     constexpr int W = WM * WN;
-    constexpr int PL = NP == 3 ? 2 : 1;                      // planes of an operand
+    constexpr int PL = 2;                                    // planes of an operand
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     constexpr int CH = BK / 8, RPU = 64 / CH;                // chunks a row, rows a load
     constexpr int ROWB = 2 * BK, KS = BK / 16;
@@ -607,20 +602,19 @@ __global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * (NP == 3 ? 2 : 1) * 
     // One 16-deep step's products.  The next slice's loads go out between them,
     // evenly over the slice: issued in a row they hold up the wave, and with it
     // the matrix core, for as long as the products take.
-    constexpr int PRODUCTS = TM * TN * NP;   // of one step
+    constexpr int PRODUCTS = TM * TN * 3;   // of one step
     // two stages: before the last step, which waits for them
     constexpr int SPREAD = PRODUCTS * (NS == 2 ? KS - 1 : KS);
     auto multiply = [&](int set, int ks, int load_k, bool load) {
         int n = ks * PRODUCTS;   // products of the slice so far
 #pragma unroll
-        for (int part = NP == 3 ? 0 : 2; part < 3; ++part)   // lo hi, hi lo, hi hi
+        for (int part = 0; part < 3; ++part)   // lo hi, hi lo, hi hi
 #pragma unroll
             for (int a = 0; a < TM; ++a)
 #pragma unroll
                 for (int c = 0; c < TN; ++c) {
                     acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        fu[set][a][part == 0 ? PL - 1 : 0], fv[set][c][part == 1 ? PL - 1 : 0], acc[a][c],
-                        0, 0, 0);
+                        fu[set][a][part == 0], fv[set][c][part == 1], acc[a][c], 0, 0, 0);
                     const int o0 = min(n * OPS / SPREAD, OPS), o1 = min((n + 1) * OPS / SPREAD, OPS);
                     ++n;
                     if (load && o1 > o0) {
@@ -723,8 +717,7 @@ __global__ __launch_bounds__(64) void ns_join(Product p) {
 // rows, so the products chain without moving X.  X X^T sums over columns, which
 // lie across lanes: each wave turns its block over in its own piece of LDS
 // (transposing reads), the waves' partial sums meet in LDS, and A and P live
-// there too.  Always three products: a step is a few hundred matrix
-// instructions and the barriers and LDS round trips around them cost as much.
+// there too.
 typedef int16_t v4i16_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16_t lds_v4i16;
 
@@ -1506,16 +1499,13 @@ struct TileChoice {
 constexpr int kSides[4] = {64, 64, 128, 192};
 
 // The choice with the least estimated time.  Times in microseconds as measured
-// from 256 x 256 to 4096 x 4096: a 64-deep slice of one tile with single and
-// with three products, and a tile's start and end.  For instance 1024 x 4096 in
-// float32: X X^T on 136 tiles of 64 takes 32 us, on 36 of 128 73 us, on 128-tiles
-// shared by seven 23 us and 7 us more for their joining; P X on 1024 tiles of 64
-// 41 to 45 us, on 256 of 128 35 us, on 132 of 192 57 us.  4096 x 4096 in bfloat16: X X^T
-// on 253 tiles of 192 takes 92 us, on 528 of 128 114 us; P X with three products
-// on 1024 of 128 417 us, on 484 of 192 411 us, over a call's first four
-// steps 236 and 253 us each on average.
-TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric, int np) {
-    static const double slice_us[4][2] = {{0.22, 0.39}, {0.30, 0.65}, {0.35, 1.0}, {1.0, 2.5}};
+// from 256 x 256 to 4096 x 4096: a 64-deep slice of one tile, and a tile's start
+// and end.  For instance 1024 x 4096: X X^T on 136 tiles of 64 takes 32 us, on 36 of
+// 128 73 us, on 128-tiles shared by seven 23 us and 7 us more for their joining; P X
+// on 1024 tiles of 64 41 to 45 us, on 256 of 128 35 us, on 132 of 192 57 us.  4096 x
+// 4096: P X on 1024 tiles of 128 417 us, on 484 of 192 411 us.
+TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric) {
+    static const double slice_us[4] = {0.39, 0.65, 1.0, 2.5};
     static const double ends_us[4] = {2.0, 2.0, 3.5, 8.0};
     TileChoice best;
     double best_us = 1e300;
@@ -1528,7 +1518,7 @@ TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool sy
         for (int splits : {1, 2, 4, 8, 16, (int)std::min<int64_t>(16, std::max<int64_t>(1, at_once / tiles))}) {
             if (splits > 1 && (!can_split || kind == 3 || K / 64 < 4 * splits || tiles * splits > 2048)) continue;
             const int64_t rounds = (tiles * splits + at_once - 1) / at_once;
-            double us = rounds * (K / 64.0 / splits * slice_us[kind][np == 3] + ends_us[kind]);
+            double us = rounds * (K / 64.0 / splits * slice_us[kind] + ends_us[kind]);
             if (splits > 1) us += 4.0 + 0.2 * splits * side / 64;
             if (us < best_us) {
                 best_us = us;
@@ -1579,19 +1569,14 @@ Layout layout(int batch, int rows, int cols) {
     l.A = take((size_t)batch * 2 * l.aplane * sizeof(half_t));
     l.P = take((size_t)batch * 2 * l.aplane * sizeof(half_t));
     // the parts of X X^T where workgroups share its tiles
-    size_t part = 0;
-    for (int np : {1, 3}) {
-        const TileChoice t = choose_tile(batch, l.mp, l.mp, l.np, true, true, np);
-        const size_t side = kSides[t.kind], ti = (l.mp + side - 1) / side;
-        if (t.splits > 1)
-            part = std::max(part, (size_t)batch * (ti * (ti + 1) / 2) * t.splits * side * side * sizeof(float));
-    }
-    l.part = take(part);
+    const TileChoice t = choose_tile(batch, l.mp, l.mp, l.np, true, true);
+    const size_t side = kSides[t.kind], ti = (l.mp + side - 1) / side;
+    l.part = take(t.splits > 1 ? (size_t)batch * (ti * (ti + 1) / 2) * t.splits * side * side * sizeof(float) : 0);
     l.bytes = at;
     return l;
 }
 
-template <int SIDE, int WM, int WN, int NP, int BK, int NS, Epilogue E>
+template <int SIDE, int WM, int WN, int BK, int NS, Epilogue E>
 int launch_tiles(Product p, int splits, int batch, hipStream_t st) {
     constexpr const char* names[] = {"ns_gram", "ns_poly", "ns_step", "ns_last"};
     const int64_t ti = (p.rows_u + SIDE - 1) / SIDE, tj = (p.rows_v + SIDE - 1) / SIDE;
@@ -1602,7 +1587,7 @@ int launch_tiles(Product p, int splits, int batch, hipStream_t st) {
     p.splits = splits;
     {
         KernelTimer timer(names[E], st);
-        hipLaunchKernelGGL((ns_product<SIDE, SIDE, WM, WN, NP, BK, NS, E>), dim3((unsigned)(tiles * splits), batch),
+        hipLaunchKernelGGL((ns_product<SIDE, SIDE, WM, WN, BK, NS, E>), dim3((unsigned)(tiles * splits), batch),
                            dim3(64 * WM * WN), 0, st, p);
     }
     if (int rc = done(names[E])) return rc;
@@ -1617,21 +1602,16 @@ int launch_tiles(Product p, int splits, int batch, hipStream_t st) {
     return DISCO_OK;
 }
 
-template <int NP, Epilogue E>
-int launch_product(const Product& p, int batch, hipStream_t st) {
-    const TileChoice t = choose_tile(batch, p.rows_u, p.rows_v, p.K, E == kGram, E == kGram || E == kPoly, NP);
-    // rings of 128, 64, 128 and 144 KB (96 KB for single products of 192)
-    switch (t.kind) {
-        case 0: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 4 : 8, E>(p, t.splits, batch, st);
-        case 1: return launch_tiles<64, 2, 2, NP, 64, NP == 3 ? 2 : 4, E>(p, t.splits, batch, st);
-        case 2: return launch_tiles<128, 2, 4, NP, NP == 3 ? 32 : 64, 4, E>(p, t.splits, batch, st);
-        default: return launch_tiles<192, 2, 2, NP, NP == 3 ? 32 : 64, NP == 3 ? 3 : 2, E>(p, t.splits, batch, st);
-    }
-}
-
 template <Epilogue E>
-int launch_product(bool three, const Product& p, int batch, hipStream_t st) {
-    return three ? launch_product<3, E>(p, batch, st) : launch_product<1, E>(p, batch, st);
+int launch_product(const Product& p, int batch, hipStream_t st) {
+    const TileChoice t = choose_tile(batch, p.rows_u, p.rows_v, p.K, E == kGram, E == kGram || E == kPoly);
+    // rings of 128, 64, 128 and 144 KB
+    switch (t.kind) {
+        case 0: return launch_tiles<64, 2, 2, 64, 4, E>(p, t.splits, batch, st);
+        case 1: return launch_tiles<64, 2, 2, 64, 2, E>(p, t.splits, batch, st);
+        case 2: return launch_tiles<128, 2, 4, 32, 4, E>(p, t.splits, batch, st);
+        default: return launch_tiles<192, 2, 2, 32, 3, E>(p, t.splits, batch, st);
+    }
 }
 
 }  // namespace
@@ -1771,13 +1751,8 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
                                c.eps, l.m, l.n, l.mp, l.np, l.tall, X, XT[0], l.xplane);
         if (int rc = done("ns_load")) return rc;
     }
-    // A bfloat16 result takes single float16 products in all but the last two
-    // steps, and for X X^T throughout: 2e-4 to 1e-3 off before its own rounding
-    // of 1.7e-3.  In the last two steps A's entries are of order one and the
-    // rounding of P and X in the other products enters X unscaled.
-    const int exact_from = sink.bf16 ? std::max(0, c.steps - 2) : 0;
     for (int t = 0; t < c.steps; ++t) {
-        const bool three = t >= exact_from, last = t + 1 == c.steps, three_gram = !sink.bf16;
+        const bool last = t + 1 == c.steps;
         half_t* xt = XT[t & 1];
         Product g{};
         g.part = reinterpret_cast<float*>(ws + l.part);
@@ -1789,9 +1764,8 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
         g.out = g.out_t = A;
         g.o_plane = l.aplane;
         g.ld_out = g.ld_t = l.mp;
-        g.lo_out = g.lo_t = 1;
         g.cb = kSA / (kSX * kSX);
-        if (int rc = launch_product<kGram>(three_gram, g, c.batch, st)) return rc;
+        if (int rc = launch_product<kGram>(g, c.batch, st)) return rc;
 
         q.u = q.v = A;
         q.u_plane = q.v_plane = l.aplane;
@@ -1801,39 +1775,33 @@ int launch_orthogonalize(const OrthoCall& c, void* stream) {
         q.add = A;
         q.o_plane = q.add_plane = l.aplane;
         q.ld_out = q.ld_t = l.mp;
-        q.lo_out = q.lo_t = three;
         q.ca = c.coeffs[1] * kSP / kSA;
         q.cb = c.coeffs[2] * kSP / (kSA * kSA);
-        // three products carry a I + P as well as P: no separate a X then
-        q.diagonal = three ? c.coeffs[0] * kSP : 0.0f;
-        if (int rc = launch_product<kPoly>(three, q, c.batch, st)) return rc;
+        q.diagonal = c.coeffs[0] * kSP;   // a I + P: no separate a X
+        if (int rc = launch_product<kPoly>(q, c.batch, st)) return rc;
 
         s.u = P;
         s.v = xt;
         s.u_plane = l.aplane;
-        s.v_plane = s.add_plane = s.o_plane = l.xplane;
+        s.v_plane = s.o_plane = l.xplane;
         s.K = l.mp;
         s.rows_u = l.mp;
         s.rows_v = l.np;
         s.out = X;
         s.out_t = XT[(t + 1) & 1];
-        s.add = three ? nullptr : xt;
         s.ld_out = l.np;
         s.ld_t = l.mp;
-        s.lo_out = three_gram;   // X X^T reads it
-        s.lo_t = 1;
-        s.ca = c.coeffs[0];
         s.cb = 1.0f / kSP;
         int rc;
-        if (last) {   // three products
+        if (last) {
             s.cb /= kSX;
             s.m = l.m;
             s.n = l.n;
             s.tall = l.tall;
             s.sink = sink;
-            rc = launch_product<3, kLast>(s, c.batch, st);
+            rc = launch_product<kLast>(s, c.batch, st);
         } else {
-            rc = launch_product<kStep>(three, s, c.batch, st);
+            rc = launch_product<kStep>(s, c.batch, st);
         }
         if (rc) return rc;
     }
