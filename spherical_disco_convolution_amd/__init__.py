@@ -21,6 +21,11 @@ Entry points (same names as the C ABI, without the ``disco_`` prefix):
     layer_norm_bwd(x, gy, mean, rstd, gamma, gsum=...) -> (gx, ggamma, gbeta)
     orthogonalize(m, ...) -> o                  Newton-Schulz products
     muon_step(w, grad, momentum, lr, ...) -> (w, momentum, w16)   one optimiser step
+
+With stream=s a call's kernels run on s, and its results are there once s has
+come to them.  Inputs have to be ready on s (s.wait_stream where another stream
+makes them); they may be let go of as soon as the call returns, and so may the
+results by the stream that was current at the call.
 """
 from __future__ import annotations
 
@@ -268,8 +273,26 @@ def _raw_current_stream():
     return raw(torch.cuda.current_device())
 
 
-def _stream(stream):
-    return ctypes.c_void_p(_raw_current_stream() if stream is None else stream.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(_raw_current_stream())
+
+
+def _on(stream, f, *args):
+    """f(*args) on `stream`.  A block of the allocator's is free as far as the stream
+    goes that it was taken under, so the call takes its results and its scratch under
+    `stream`.  What it was given is kept, should the caller let go of it, until
+    `stream` is through with it, and the results until the current stream is."""
+    torch = _torch()
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    given = [t for t in args if isinstance(t, torch.Tensor)]
+    for t in given:
+        t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(current)
+    return out
 
 
 def _need(t, name, shape):
@@ -281,6 +304,8 @@ def _need(t, name, shape):
 
 def contract(psi: Psi, x, xk=None, xk_dtype=None, stream=None):
     """xk[b,c,k,j,q] = sum_(i,p) Psi[k,j,(i,p)] x[b,c,i,(q*s+p) mod nlon_in]."""
+    if stream is not None:
+        return _on(stream, contract, psi, x, xk, xk_dtype)
     torch = _torch()
     if x.dim() != 4:
         raise ValueError("x must be [B, C, nlat_in, nlon_in]")
@@ -291,12 +316,14 @@ def contract(psi: Psi, x, xk=None, xk_dtype=None, stream=None):
         xk = torch.empty((B, C, psi.K, psi.nlat_out, psi.nlon_out), dtype=dt, device=x.device)
     _need(xk, "xk", (B, C, psi.K, psi.nlat_out, psi.nlon_out))
     _check(_lib.disco_contract(psi.handle, x.data_ptr(), _dtype_code(x), xk.data_ptr(),
-                               _dtype_code(xk), B, C, _stream(stream)), "contract")
+                               _dtype_code(xk), B, C, _stream()), "contract")
     return xk
 
 
 def einsum(xk, w, groups: int = 1, bias=None, y=None, out_dtype=None, stream=None):
     """y[b,co,j,q] = bias[co] + sum_(ci',k) w[co,ci',k] xk[b, G(co)*Ci/G+ci', k, j, q]."""
+    if stream is not None:
+        return _on(stream, einsum, xk, w, groups, bias, y, out_dtype)
     torch = _torch()
     if xk.dim() != 5 or w.dim() != 3:
         raise ValueError("xk must be [B, Ci, K, nlat_out, nlon_out] and w [Co, Ci/groups, K]")
@@ -318,7 +345,7 @@ def einsum(xk, w, groups: int = 1, bias=None, y=None, out_dtype=None, stream=Non
         bptr = bias.data_ptr()
     _check(_lib.disco_einsum(xk.data_ptr(), _dtype_code(xk), w.data_ptr(), _dtype_code(w), bptr,
                              y.data_ptr(), _dtype_code(y), B, Ci, Co, groups, K, H, W,
-                             _stream(stream)), "einsum")
+                             _stream()), "einsum")
     return y
 
 
@@ -359,6 +386,8 @@ def kernel_timing_read(max_kernels: int = 64) -> dict:
 
 def fused_fwd(psi: Psi, x, w, groups: int = 1, bias=None, y=None, out_dtype=None, stream=None):
     """The forward DISCO convolution without storing the K-expanded tensor."""
+    if stream is not None:
+        return _on(stream, fused_fwd, psi, x, w, groups, bias, y, out_dtype)
     torch = _torch()
     if x.dim() != 4 or w.dim() != 3:
         raise ValueError("x must be [B, Ci, nlat_in, nlon_in] and w [Co, Ci/groups, K]")
@@ -380,7 +409,7 @@ def fused_fwd(psi: Psi, x, w, groups: int = 1, bias=None, y=None, out_dtype=None
         bptr = bias.data_ptr()
     _check(_lib.disco_fused_fwd(psi.handle, x.data_ptr(), _dtype_code(x), w.data_ptr(),
                                 _dtype_code(w), bptr, y.data_ptr(), _dtype_code(y), B, Ci, Co,
-                                groups, _stream(stream)), "fused_fwd")
+                                groups, _stream()), "fused_fwd")
     return y
 
 
@@ -388,6 +417,8 @@ def fused_fwd(psi: Psi, x, w, groups: int = 1, bias=None, y=None, out_dtype=None
 def fused_fwd_noalloc(psi: Psi, x, w, y, groups: int = 1, bias=None, stream=None):
     """fused_fwd for callers that cannot allocate device memory: the direct
     algorithms with the library's fixed scratch; y must be given."""
+    if stream is not None:
+        return _on(stream, fused_fwd_noalloc, psi, x, w, y, groups, bias)
     if x.dim() != 4 or w.dim() != 3:
         raise ValueError("x must be [B, Ci, nlat_in, nlon_in] and w [Co, Ci/groups, K]")
     B, Ci = x.shape[:2]
@@ -403,7 +434,7 @@ def fused_fwd_noalloc(psi: Psi, x, w, y, groups: int = 1, bias=None, stream=None
         bptr = bias.data_ptr()
     _check(_lib.disco_fused_fwd_noalloc(psi.handle, x.data_ptr(), _dtype_code(x), w.data_ptr(),
                                         _dtype_code(w), bptr, y.data_ptr(), _dtype_code(y), B, Ci,
-                                        Co, groups, _stream(stream)), "fused_fwd_noalloc")
+                                        Co, groups, _stream()), "fused_fwd_noalloc")
     return y
 
 
@@ -413,6 +444,8 @@ def fused_fwd_noalloc(psi: Psi, x, w, y, groups: int = 1, bias=None, stream=None
 def contract_transpose(psi: Psi, gxk, gx=None, gx_dtype=None, stream=None):
     """gx[b,c,i,(q*s+p) mod nlon_in] = sum over windows of Psi[k,j,(i,p)] gxk[b,c,k,j,q]
     (the adjoint of contract)."""
+    if stream is not None:
+        return _on(stream, contract_transpose, psi, gxk, gx, gx_dtype)
     torch = _torch()
     if gxk.dim() != 5:
         raise ValueError("gxk must be [B, C, K, nlat_out, nlon_out]")
@@ -423,13 +456,15 @@ def contract_transpose(psi: Psi, gxk, gx=None, gx_dtype=None, stream=None):
         gx = torch.empty((B, C, psi.nlat_in, psi.nlon_in), dtype=dt, device=gxk.device)
     _need(gx, "gx", (B, C, psi.nlat_in, psi.nlon_in))
     _check(_lib.disco_contract_transpose(psi.handle, gxk.data_ptr(), _dtype_code(gxk),
-                                         gx.data_ptr(), _dtype_code(gx), B, C, _stream(stream)),
+                                         gx.data_ptr(), _dtype_code(gx), B, C, _stream()),
            "contract_transpose")
     return gx
 
 
 def einsum_grad_xk(gy, w, groups: int = 1, gxk=None, out_dtype=None, stream=None):
     """gxk[b, G*Ci/G+ci', k, j, q] = sum_{co in G} w[co,ci',k] gy[b,co,j,q]."""
+    if stream is not None:
+        return _on(stream, einsum_grad_xk, gy, w, groups, gxk, out_dtype)
     torch = _torch()
     if gy.dim() != 4 or w.dim() != 3:
         raise ValueError("gy must be [B, Co, nlat_out, nlon_out] and w [Co, Ci/groups, K]")
@@ -445,12 +480,14 @@ def einsum_grad_xk(gy, w, groups: int = 1, gxk=None, out_dtype=None, stream=None
     _need(gxk, "gxk", (B, Ci, K, H, W))
     _check(_lib.disco_einsum_grad_xk(gy.data_ptr(), _dtype_code(gy), w.data_ptr(), _dtype_code(w),
                                      gxk.data_ptr(), _dtype_code(gxk), B, Ci, Co, groups, K, H, W,
-                                     _stream(stream)), "einsum_grad_xk")
+                                     _stream()), "einsum_grad_xk")
     return gxk
 
 
 def einsum_grad_w(xk, gy, groups: int = 1, gw=None, stream=None):
     """gw[co,ci',k] = sum_{b,j,q} gy[b,co,j,q] xk[b, G(co)*Ci/G+ci', k, j, q] (float32)."""
+    if stream is not None:
+        return _on(stream, einsum_grad_w, xk, gy, groups, gw)
     torch = _torch()
     if xk.dim() != 5 or gy.dim() != 4:
         raise ValueError("xk must be [B, Ci, K, nlat_out, nlon_out] and gy [B, Co, nlat_out, nlon_out]")
@@ -466,7 +503,7 @@ def einsum_grad_w(xk, gy, groups: int = 1, gw=None, stream=None):
     if gw.dtype != torch.float32:
         raise ValueError("gw must be float32")
     _check(_lib.disco_einsum_grad_w(xk.data_ptr(), _dtype_code(xk), gy.data_ptr(), _dtype_code(gy),
-                                    gw.data_ptr(), B, Ci, Co, groups, K, H, W, _stream(stream)),
+                                    gw.data_ptr(), B, Ci, Co, groups, K, H, W, _stream()),
            "einsum_grad_w")
     return gw
 
@@ -475,6 +512,8 @@ def fused_bwd(psi: Psi, x, w, gy, groups: int = 1, need_gx: bool = True, need_gw
               need_gbias: bool = False, gx_dtype=None, stream=None):
     """Gradients (gx, gw, gbias) of sum(gy * fused_fwd(psi, x, w)) with X_K
     recomputed slab by slab; entries not asked for are None."""
+    if stream is not None:
+        return _on(stream, fused_bwd, psi, x, w, gy, groups, need_gx, need_gw, need_gbias, gx_dtype)
     torch = _torch()
     if x.dim() != 4 or w.dim() != 3 or gy.dim() != 4:
         raise ValueError("x must be [B, Ci, nlat_in, nlon_in], w [Co, Ci/groups, K] and gy "
@@ -500,7 +539,7 @@ def fused_bwd(psi: Psi, x, w, gy, groups: int = 1, need_gx: bool = True, need_gw
                                 _dtype_code(gx) if gx is not None else F32,
                                 gw.data_ptr() if gw is not None else None,
                                 gb.data_ptr() if gb is not None else None,
-                                B, Ci, Co, groups, _stream(stream)), "fused_bwd")
+                                B, Ci, Co, groups, _stream()), "fused_bwd")
     return gx, gw, gb
 
 
@@ -529,15 +568,10 @@ def _f32_ptr(t, name, shape):
     return t.data_ptr()
 
 
-def _workspace(nbytes, like, stream):
-    """Scratch for one call on like's device (None for no bytes): the allocator
-    keeps it until the call's stream is done with it."""
-    if nbytes == 0:
-        return None
-    ws = like.new_empty(nbytes, dtype=_torch().uint8)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+def _workspace(nbytes, like):
+    """Scratch for one call on like's device (None for no bytes).  Let go of when the
+    call returns, it goes to later work on the current stream only."""
+    return like.new_empty(nbytes, dtype=_torch().uint8) if nbytes else None
 
 
 def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, axis: int = 1,
@@ -549,6 +583,8 @@ def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, a
     Returns (y, s, mean, rstd): s is None without a residual, the statistics
     (float32, x's shape without the axis) None with need_stats=False.  y has
     out_dtype, or x's dtype."""
+    if stream is not None:
+        return _on(stream, layer_norm_fwd, x, gamma, beta, residual, eps, axis, y, out_dtype, need_stats)
     torch = _torch()
     outer, C, inner, points = _norm_view(x, axis)
     _need(x, "x", x.shape)
@@ -570,7 +606,7 @@ def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, a
         x.data_ptr(), _dtype_code(x), residual.data_ptr() if s is not None else None, gptr, bptr,
         y.data_ptr(), _dtype_code(y), s.data_ptr() if s is not None else None,
         mean.data_ptr() if need_stats else None, rstd.data_ptr() if need_stats else None,
-        outer, C, inner, eps, _stream(stream)), "layer_norm_fwd")
+        outer, C, inner, eps, _stream()), "layer_norm_fwd")
     return y, s, mean, rstd
 
 
@@ -580,6 +616,9 @@ def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need
     asked for are None.  x is what was normalised (the forward's s where it had
     a residual).  gsum (gy's dtype): the gradient that reaches x past the norm,
     added to gx.  gx has gx_dtype, or float32."""
+    if stream is not None:
+        return _on(stream, layer_norm_bwd, x, gy, mean, rstd, gamma, gsum, axis, need_gx, need_gparams,
+                   gx_dtype)
     torch = _torch()
     outer, C, inner, points = _norm_view(x, axis)
     _need(x, "x", x.shape)
@@ -602,13 +641,13 @@ def layer_norm_bwd(x, gy, mean, rstd, gamma=None, gsum=None, axis: int = 1, need
         nws = _lib.disco_layer_norm_bwd_workspace(outer, C, inner)
         if nws < 0:
             _check(nws, "layer_norm_bwd")
-        ws = _workspace(nws, x, stream)
+        ws = _workspace(nws, x)
     _check(_lib.disco_layer_norm_bwd(
         x.data_ptr(), _dtype_code(x), gy.data_ptr(), _dtype_code(gy), mptr, rptr, gptr,
         gsum.data_ptr() if gsum is not None else None,
         gx.data_ptr() if need_gx else None, _dtype_code(gx) if need_gx else F32,
         gg.data_ptr() if need_gparams else None, gb.data_ptr() if need_gparams else None,
-        ws.data_ptr() if ws is not None else None, nws, outer, C, inner, _stream(stream)),
+        ws.data_ptr() if ws is not None else None, nws, outer, C, inner, _stream()),
         "layer_norm_bwd")
     return gx, gg, gb
 
@@ -625,11 +664,11 @@ def _coeffs(coeffs):
     return (ctypes.c_float * 3)(*coeffs)
 
 
-def _ortho_workspace(batch, rows, cols, like, stream, what):
+def _ortho_workspace(batch, rows, cols, like, what):
     n = _lib.disco_orthogonalize_workspace(batch, rows, cols)
     if n < 0:
         _check(n, what)
-    return _workspace(n, like, stream), n
+    return _workspace(n, like), n
 
 
 def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps: float = 1e-7,
@@ -638,6 +677,8 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
     matrix of a batch [batch, rows, cols]: singular values near one, singular
     vectors kept.  The result is computed to float32 accuracy and rounded to
     out_dtype, or m's dtype.  coeffs: (a, b, c) of the step X <- a X + (b A + c A^2) X."""
+    if stream is not None:
+        return _on(stream, orthogonalize, m, out, out_dtype, steps, coeffs, eps)
     torch = _torch()
     if m.dim() not in (2, 3):
         raise ValueError("m must be [rows, cols] or [batch, rows, cols]")
@@ -648,11 +689,11 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
         out = torch.empty_like(m, dtype=m.dtype if out_dtype is None else out_dtype)
     else:
         _need(out, "out", m.shape)
-    ws, nws = _ortho_workspace(batch, rows, cols, m, stream, "orthogonalize")
+    ws, nws = _ortho_workspace(batch, rows, cols, m, "orthogonalize")
     _check(_lib.disco_orthogonalize(m.data_ptr(), _dtype_code(m), out.data_ptr(), _dtype_code(out),
                                     batch, rows, cols, steps, _coeffs(coeffs), eps,
                                     ws.data_ptr() if ws is not None else None, nws,
-                                    _stream(stream)), "orthogonalize")
+                                    _stream()), "orthogonalize")
     return out
 
 
@@ -672,6 +713,9 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
     updated in place unless w_out / momentum_out are given.  need_bf16_copy:
     also return (in w16, if given) the bfloat16 copy of a float32 w.
     Returns (w, momentum, w16)."""
+    if stream is not None:
+        return _on(stream, muon_step, w, grad, momentum, lr, beta, nesterov, weight_decay, scale, steps, coeffs,
+                   eps, groups, w_out, momentum_out, need_bf16_copy, w16)
     torch = _torch()
     if w.dim() < 2:
         raise ValueError("w must have at least two dimensions")
@@ -696,10 +740,10 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
         _need(w16, "w16", w.shape)
         if w16.dtype != torch.bfloat16:
             raise ValueError("w16 must be bfloat16")
-    ws, nws = _ortho_workspace(groups, rows, cols, w, stream, "muon_step")
+    ws, nws = _ortho_workspace(groups, rows, cols, w, "muon_step")
     _check(_lib.disco_muon_step(
         grad.data_ptr(), _dtype_code(grad), mptr, _f32_ptr(momentum_out, "momentum_out", w.shape),
         w.data_ptr(), _dtype_code(w), w_out.data_ptr(), w16.data_ptr() if w16 is not None else None,
         lr, beta, int(nesterov), weight_decay, scale, groups, rows, cols, steps, _coeffs(coeffs), eps,
-        ws.data_ptr() if ws is not None else None, nws, _stream(stream)), "muon_step")
+        ws.data_ptr() if ws is not None else None, nws, _stream()), "muon_step")
     return w_out, momentum_out, w16
