@@ -15,9 +15,9 @@
 // with one strong direction over equal ones a fifth as large, 1e-1 after sixteen,
 // where the result's own rounding is 1.7e-3.  So every result is computed the
 // same way and rounded once, to its type.  The caller has checked that
-// singular values stay below 3.5 and the polynomial below 24, so the scales
-// below keep every entry inside float16's range, and the lo parts' granularity
-// is 2^-36.
+// singular values stay below 3.5 in what goes into a step, and the polynomial below
+// 24, so the scales below keep every operand inside float16's range, and the lo
+// parts' granularity is 2^-36.  The last step's result goes out in float32.
 //
 // X is kept in both orders, [m][n] for X X^T and [n][m] for P X, so that both
 // operands of every product are contiguous along the summed index; the matrix
@@ -850,6 +850,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
             }
     __syncthreads();   // the pieces lie where X_0 lay
 
+    floatx16 y[CB][MT];
     for (int t = 0; t < steps; ++t) {
         // ---- this wave's part of X X^T, lower tiles ----
         floatx16 g[C::NT];
@@ -971,7 +972,6 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
         }
         __syncthreads();
         // ---- X <- a X + P X ----
-        floatx16 y[CB][MT];
 #pragma unroll
         for (int c = 0; c < CB; ++c)
 #pragma unroll
@@ -1000,14 +1000,16 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const Pair p = split(
-                        ca * ((float)xh[c][a][e >> 3][e & 7] + (float)xl[c][a][e >> 3][e & 7]) +
-                        y[c][a][e] * (1.0f / kSP));
+                    y[c][a][e] = ca * ((float)xh[c][a][e >> 3][e & 7] + (float)xl[c][a][e >> 3][e & 7]) +
+                                 y[c][a][e] * (1.0f / kSP);
+                    const Pair p = split(y[c][a][e]);
                     xh[c][a][e >> 3][e & 7] = p.h;
                     xl[c][a][e >> 3][e & 7] = p.l;
                 }
     }
-    // ---- result: back through LDS, written as it lies in memory ----
+    // ---- result: the last step's float32 values, back through LDS and written as
+    // they lie in memory.  No step reads them: they may exceed float16's range (16
+    // times kSX), as the caller's check allows them to ----
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < CB; ++c)
@@ -1018,8 +1020,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
                 const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
                 const int j = 32 * (wave + W * c) + l32;
                 if (i < m && j < n)
-                    *(lds_float*)(uintptr_t)(x_at + 4u * (uint32_t)(i * ld + j)) =
-                        ((float)xh[c][a][e >> 3][e & 7] + (float)xl[c][a][e >> 3][e & 7]) * (1.0f / kSX);
+                    *(lds_float*)(uintptr_t)(x_at + 4u * (uint32_t)(i * ld + j)) = y[c][a][e] * (1.0f / kSX);
             }
     __syncthreads();
     for (int at0 = 4 * threadIdx.x; at0 < total; at0 += 4 * K * blockDim.x) {
