@@ -332,8 +332,8 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
  * singular values (above about 3.5) or the polynomial a + b s^2 + c s^4 (above
  * 24) out of the operands' range.  A NaN or an
  * infinity anywhere in a matrix makes its whole result NaN; a zero matrix
- * stays zero (eps > 0).  Results do not depend on the other matrices of the
- * batch and are reproducible. */
+ * stays zero (eps > 0).  A matrix has the same bits by itself as in a
+ * batch of any size, and they are reproducible. */
 
 /* Bytes of device workspace that the two calls below need (none for matrices
  * that one workgroup holds: up to 32 x 512 or 64 x 256, either way up), or a

@@ -101,6 +101,13 @@ __device__ __forceinline__ Sink sink_from(Sink s, int64_t base) {
     return s;
 }
 
+// The new weight.  The fused multiply-add is written out, here and where P is
+// formed: left to the compiler, which of the two products is the rounded one could
+// change from one kernel to the next.
+__device__ __forceinline__ float new_weight(const Sink& s, float w, float o) {
+    return fmaf(-s.rate, o, s.keep * w);
+}
+
 template <typename I>
 __device__ __forceinline__ void sink_store(const Sink& s, I i, float o) {
     if (s.o != nullptr) {
@@ -110,9 +117,9 @@ __device__ __forceinline__ void sink_store(const Sink& s, I i, float o) {
     }
     if (s.bf16) {
         const float w = load_f(static_cast<const bf16_t*>(s.w), i);
-        store_f(static_cast<bf16_t*>(s.w_out), i, s.keep * w - s.rate * o);
+        store_f(static_cast<bf16_t*>(s.w_out), i, new_weight(s, w, o));
     } else {
-        const float v = s.keep * static_cast<const float*>(s.w)[i] - s.rate * o;
+        const float v = new_weight(s, static_cast<const float*>(s.w)[i], o);
         static_cast<float*>(s.w_out)[i] = v;
         if (s.w16 != nullptr) store_f(s.w16, i, v);
     }
@@ -323,18 +330,25 @@ struct Product {
 // layout and rows in memory, through the wave's own piece of LDS at `at`.  One
 // wave's LDS accesses are carried out in order; the fences keep the compiler
 // from reordering them.
+enum Keep { kAll, kFromDiagonal, kLeft };
+
 template <int TM, int TN>
 struct BlockIO {
     static constexpr int ROW_T = TM * 64 + 16, ROW = TN * 64 + 16;   // bytes of a padded row
     static constexpr int BYTES = TN * 32 * ROW_T > TM * 32 * ROW ? TN * 32 * ROW_T : TM * 32 * ROW;
 
-    // 16-byte pieces of R rows of 8 C elements, row r at g + r * ld
-    template <int R, int C, bool LOAD>
+    // 16-byte pieces of R rows of 8 C elements, row r at g + r * ld.  K: only those
+    // whose 32 x 32 tile, `right` tiles right of the diagonal at the first row and
+    // column, lies on the diagonal or right of it, or left of it.
+    template <int R, int C, bool LOAD, Keep K = kAll>
     static __device__ __forceinline__ void move(half_t* g, size_t ld, int rows, int cols,
-                                                uint32_t at, int row_bytes, int lane) {
+                                                uint32_t at, int row_bytes, int lane, int right = 0) {
 #pragma unroll 4
         for (int it = 0; it < (R * C + 63) / 64; ++it) {
             const int idx = it * 64 + lane, r = idx / C, c = idx % C;
+            const int over = right + (c >> 2) - (r >> 5);
+            if (K == kFromDiagonal && over < 0) continue;
+            if (K == kLeft && over >= 0) continue;
             if ((R * C % 64 == 0 || idx < R * C) && r < rows && 8 * c < cols) {
                 half_t* q = g + (size_t)r * ld + 8 * c;
                 lds_halfx8* l = (lds_halfx8*)(uintptr_t)(at + (uint32_t)(r * row_bytes + 16 * c));
@@ -355,7 +369,7 @@ __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_A
 // What becomes of a wave's block of sums whose first row and column are ib and jb.
 template <int TM, int TN, Epilogue E>
 __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN], int b, int ib, int jb,
-                                       bool off_diagonal, uint32_t piece, int lane) {
+                                       uint32_t piece, int lane) {
     using IO = BlockIO<TM, TN>;
     const int l32 = lane & 31, lg = lane >> 5;
     // lane: column j = lane % 32, rows i = 8 (e / 4) + 4 (lane / 32) + e % 4
@@ -381,7 +395,8 @@ __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN]
                     for (int q = 0; q < 4; ++q) {
                         const halfx4 x = *(const lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[a][c][4 * q + e] += p.ca * (float)x[e];
+                        for (int e = 0; e < 4; ++e)
+                            acc[a][c][4 * q + e] = fmaf(p.ca, (float)x[e], acc[a][c][4 * q + e]);
                     }
             wave_fence();
         }
@@ -410,8 +425,12 @@ __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN]
     } else {
         half_t* out = p.out + (size_t)b * 2 * p.o_plane + (size_t)ib * p.ld_out + jb;
         half_t* out_t = p.out_t + (size_t)b * 2 * p.o_plane + (size_t)jb * p.ld_t + ib;
-        // a symmetric result's diagonal tiles are whole already
-        const bool both = E == kStep || off_diagonal;
+        // Of a symmetric result what is right of the diagonal (in 32 x 32 tiles) is the
+        // mirror image of what is left of it, also inside a workgroup's tile: the two
+        // sums add lo hi and hi lo in another order, and which of them counts must
+        // not depend on the tile's size.
+        constexpr bool kMirrored = E != kStep;
+        const int right = (ib - jb) / 32;
 #pragma unroll
         for (int pl = 0; pl < 2; ++pl) {
 #pragma unroll
@@ -429,27 +448,25 @@ __device__ __forceinline__ void finish(const Product& p, floatx16 (&acc)[TM][TN]
                         *(lds_halfx4*)(uintptr_t)IO::cell_t(piece, a, c, q, lane) = h;
                     }
             wave_fence();
-            IO::template move<TN * 32, TM * 4, false>(out_t + (size_t)pl * p.o_plane, p.ld_t, rows_j,
-                                                      rows_i, piece, IO::ROW_T, lane);
+            IO::template move<TN * 32, TM * 4, false, kMirrored ? kFromDiagonal : kAll>(
+                out_t + (size_t)pl * p.o_plane, p.ld_t, rows_j, rows_i, piece, IO::ROW_T, lane, right);
             wave_fence();
-            if (both) {
-                typedef __attribute__((address_space(3))) half_t lds_half;
+            typedef __attribute__((address_space(3))) half_t lds_half;
 #pragma unroll
-                for (int a = 0; a < TM; ++a)
+            for (int a = 0; a < TM; ++a)
 #pragma unroll
-                    for (int c = 0; c < TN; ++c)
+                for (int c = 0; c < TN; ++c)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const Pair s = split(acc[a][c][e]);
-                            const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
-                            *(lds_half*)(uintptr_t)(piece + (uint32_t)(i * IO::ROW + 2 * (32 * c + l32))) =
-                                pl ? s.l : s.h;
-                        }
-                wave_fence();
-                IO::template move<TM * 32, TN * 4, false>(out + (size_t)pl * p.o_plane, p.ld_out, rows_i,
-                                                          rows_j, piece, IO::ROW, lane);
-                wave_fence();
-            }
+                    for (int e = 0; e < 16; ++e) {
+                        const Pair s = split(acc[a][c][e]);
+                        const int i = 32 * a + 8 * (e >> 2) + 4 * lg + (e & 3);
+                        *(lds_half*)(uintptr_t)(piece + (uint32_t)(i * IO::ROW + 2 * (32 * c + l32))) =
+                            pl ? s.l : s.h;
+                    }
+            wave_fence();
+            IO::template move<TM * 32, TN * 4, false, kMirrored ? kLeft : kAll>(
+                out + (size_t)pl * p.o_plane, p.ld_out, rows_i, rows_j, piece, IO::ROW, lane, -right);
+            wave_fence();
         }
     }
 }
@@ -537,10 +554,10 @@ __global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * 4 * BK > 81920 ? 1 :
     const half_t* u = p.u + (size_t)b * 2 * p.u_plane;
     const half_t* v = p.v + (size_t)b * 2 * p.v_plane;
 
-    // this workgroup's slices
-    const int nk_all = p.K / BK;
-    const int k_lo = (int)((int64_t)nk_all * part / p.splits);
-    const int nk = (int)((int64_t)nk_all * (part + 1) / p.splits) - k_lo;
+    // this workgroup's slices: shares are whole 64-deep slices for every tile
+    const int nk_all = p.K / 64;
+    const int k_lo = (int)((int64_t)nk_all * part / p.splits) * (64 / BK);
+    const int nk = (int)((int64_t)nk_all * (part + 1) / p.splits) * (64 / BK) - k_lo;
 
     const half_t* src[OPS];
 #pragma unroll
@@ -667,7 +684,7 @@ __global__ __launch_bounds__(64 * WM * WN, NS * (BM + BN) * 4 * BK > 81920 ? 1 :
         return;
     }
     __syncthreads();   // the ring is free
-    finish<TM, TN, E>(p, acc, b, i0 + wm * TM * 32, j0 + wn * TN * 32, ti != tj,
+    finish<TM, TN, E>(p, acc, b, i0 + wm * TM * 32, j0 + wn * TN * 32,
                       ring_at + (uint32_t)(wave * PIECE), lane);
 }
 
@@ -703,7 +720,7 @@ __global__ __launch_bounds__(64) void ns_join(Product p) {
                 }
     }
     const int wm = wave / WN, wn = wave % WN;
-    finish<TM, TN, E>(p, acc, b, ti * BM + wm * TM * 32, tj * BN + wn * TN * 32, ti != tj,
+    finish<TM, TN, E>(p, acc, b, ti * BM + wm * TM * 32, tj * BN + wn * TN * 32,
                       (uint32_t)(uintptr_t)(lds_u8*)&lds[0], lane);
 }
 
@@ -1050,7 +1067,7 @@ __global__ __launch_bounds__(512) void ns_small(Source src, const float* buf_in,
             }
             if (to.o == nullptr) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = to.keep * w[k][e] - to.rate * f[e];
+                for (int e = 0; e < 4; ++e) f[e] = new_weight(to, w[k][e], f[e]);
             }
             void* out = to.o ? to.o : to.w_out;
             if (to.bf16) store4(static_cast<bf16_t*>(out), at, total, f);
@@ -1505,28 +1522,46 @@ constexpr int kSides[4] = {64, 64, 128, 192};
 // 128 73 us, on 128-tiles shared by seven 23 us and 7 us more for their joining; P X
 // on 1024 tiles of 64 41 to 45 us, on 256 of 128 35 us, on 132 of 192 57 us.  4096 x
 // 4096: P X on 1024 tiles of 128 417 us, on 484 of 192 411 us.
+// The shares decide the order of the float32 sums and are those of one matrix, so
+// that its bits do not depend on how many others share the call; the tile does not
+// change them, and goes by the whole batch.  (Shares by the batch as well would be
+// worth up to an eighth: four matrices of 640 x 4096 take 679 us, and took 605; two of
+// 1024 x 4096 750 and 689.)
 TileChoice choose_tile(int batch, int ni, int nj, int K, bool can_split, bool symmetric) {
     static const double slice_us[4] = {0.39, 0.65, 1.0, 2.5};
     static const double ends_us[4] = {2.0, 2.0, 3.5, 8.0};
+    constexpr double kNever = 1e300;
+    auto tiles_of = [&](int kind) {
+        const int64_t side = kSides[kind], ti = (ni + side - 1) / side, tj = (nj + side - 1) / side;
+        return symmetric ? ti * (ti + 1) / 2 : ti * tj;
+    };
+    auto at_once = [](int kind) { return kind == 1 ? 512 : 256; };
+    auto estimate = [&](int kind, int splits, int matrices) {
+        if (splits > 1 && kind == 3) return kNever;
+        const int64_t rounds = (matrices * tiles_of(kind) * splits + at_once(kind) - 1) / at_once(kind);
+        const double us = rounds * (K / 64.0 / splits * slice_us[kind] + ends_us[kind]);
+        return splits > 1 ? us + 4.0 + 0.2 * splits * kSides[kind] / 64 : us;
+    };
     TileChoice best;
-    double best_us = 1e300;
-    for (int kind = 0; kind < 4; ++kind) {
-        const int64_t side = kSides[kind];
-        const int64_t ti = (ni + side - 1) / side, tj = (nj + side - 1) / side;
-        const int64_t tiles = batch * (symmetric ? ti * (ti + 1) / 2 : ti * tj);
-        const int64_t at_once = kind == 1 ? 512 : 256;
-        // also as many as fill the compute units once
-        for (int splits : {1, 2, 4, 8, 16, (int)std::min<int64_t>(16, std::max<int64_t>(1, at_once / tiles))}) {
-            if (splits > 1 && (!can_split || kind == 3 || K / 64 < 4 * splits || tiles * splits > 2048)) continue;
-            const int64_t rounds = (tiles * splits + at_once - 1) / at_once;
-            double us = rounds * (K / 64.0 / splits * slice_us[kind] + ends_us[kind]);
-            if (splits > 1) us += 4.0 + 0.2 * splits * side / 64;
-            if (us < best_us) {
-                best_us = us;
-                best.kind = kind;
-                best.splits = splits;
-            }
+    double best_us = kNever;
+    auto consider = [&](int kind, int splits, int matrices) {
+        const double us = estimate(kind, splits, matrices);
+        if (us < best_us) {
+            best_us = us;
+            best.kind = kind;
+            best.splits = splits;
         }
+    };
+    for (int kind = 0; kind < 4; ++kind) {
+        const int64_t tiles = tiles_of(kind);
+        // also as many as fill the compute units once
+        for (int splits : {1, 2, 4, 8, 16, (int)std::min<int64_t>(16, std::max<int64_t>(1, at_once(kind) / tiles))})
+            if (splits == 1 || (can_split && K / 64 >= 4 * splits && tiles * splits <= 2048))
+                consider(kind, splits, 1);
+    }
+    if (batch > 1) {
+        best_us = kNever;
+        for (int kind = 0; kind < 4; ++kind) consider(kind, best.splits, batch);
     }
     return best;
 }
