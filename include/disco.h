@@ -278,8 +278,9 @@ int disco_fused_bwd(const disco_psi* psi, const void* x, int x_dtype, const void
  * convolution in a pre-norm residual block.  Tensors are dense and seen as
  * [outer, C, inner]: a field [B, C, nlat, nlon] is outer = B, inner =
  * nlat*nlon; channel-last rows [n, C] are outer = n, inner = 1.  Pointers
- * need the alignment of their element only.  Statistics are float32, the
- * mean first and then the centred squares.  Outputs may not overlap inputs. */
+ * need the alignment of their element only.  C is at most 2^30 (EUNSUPPORTED
+ * past it).  Statistics are float32, the mean first and then the centred
+ * squares.  Outputs may not overlap inputs. */
 
 /* Forward:
  *   s = x, or x + residual rounded to x_dtype and stored in `sum`
@@ -337,7 +338,8 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
 
 /* Bytes of device workspace that the two calls below need (none for matrices
  * that one workgroup holds: up to 32 x 512 or 64 x 256, either way up), or a
- * negative status (EUNSUPPORTED for more than 65535 matrices). */
+ * negative status (EUNSUPPORTED for more than 65535 matrices or sides past
+ * 2^31 - 64). */
 int64_t disco_orthogonalize_workspace(int32_t batch, int32_t rows, int32_t cols);
 
 /* o = the orthogonalised m; m [batch, rows, cols] of m_dtype, o of o_dtype. */

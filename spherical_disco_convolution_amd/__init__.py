@@ -546,6 +546,13 @@ def fused_bwd(psi: Psi, x, w, gy, groups: int = 1, need_gx: bool = True, need_gw
 # ----------------------------------------------------------------------------
 # layer norm
 # ----------------------------------------------------------------------------
+def _int32(*sizes):
+    """The library takes these as 32-bit integers; ctypes would cut them off."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise NotImplementedError(f"a size or count of {n} does not fit 32 bits")
+
+
 def _norm_view(x, axis):
     """(outer, C, inner, shape without the channel axis) of x's channel axis."""
     if x.dim() < 2:
@@ -555,6 +562,7 @@ def _norm_view(x, axis):
     axis %= x.dim()
     shape = x.shape
     before, after = shape[:axis], shape[axis + 1:]
+    _int32(shape[axis])
     return math.prod(before), shape[axis], math.prod(after), before + after
 
 
@@ -685,6 +693,7 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
     _need(m, "m", m.shape)
     batch = m.shape[0] if m.dim() == 3 else 1
     rows, cols = m.shape[-2:]
+    _int32(batch, rows, cols, steps)
     if out is None:
         out = torch.empty_like(m, dtype=m.dtype if out_dtype is None else out_dtype)
     else:
@@ -732,6 +741,7 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
     if w_out.dtype != w.dtype:
         raise ValueError(f"w_out must have w's dtype ({w.dtype})")
     rows, cols = w.shape[0] // groups, math.prod(w.shape[1:])
+    _int32(groups, rows, cols, steps)
     if scale is None:
         scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
     if w16 is None and need_bf16_copy:

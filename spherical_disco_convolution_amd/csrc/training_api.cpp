@@ -56,6 +56,9 @@ int check_ortho(int32_t batch, int32_t rows, int32_t cols, int32_t steps, const 
     int64_t t = (int64_t)rows * cols;
     if (__builtin_mul_overflow(t, (int64_t)batch, &t) || t > (INT64_MAX >> 8))
         return set_error(DISCO_EINVAL, "batch * rows * cols is too large");
+    constexpr int32_t kMostSide = INT32_MAX - 63;   // rounded up to 64 in 32 bits
+    if (rows > kMostSide || cols > kMostSide)
+        return set_error(DISCO_EUNSUPPORTED, "at most %d rows or columns (got %d x %d)", kMostSide, rows, cols);
     *n = t;
     if (steps < 1 || steps > 64)
         return set_error(DISCO_EINVAL, "steps must lie in 1..64 (got %d)", steps);
@@ -93,6 +96,9 @@ int check_norm_sizes(int64_t outer, int32_t C, int64_t inner, int64_t* n) {
     if (outer < 0 || inner < 0 || C < 1)
         return set_error(DISCO_EINVAL, "sizes must be outer >= 0, C >= 1, inner >= 0 (got %lld, %d, "
                          "%lld)", (long long)outer, C, (long long)inner);
+    constexpr int32_t kMostChannels = 1 << 30;   // kernels add up to 2^24 to a channel in 32 bits
+    if (C > kMostChannels)
+        return set_error(DISCO_EUNSUPPORTED, "at most %d channels (got %d)", kMostChannels, C);
     int64_t t = 0;
     if (__builtin_mul_overflow(outer, inner, &t) || __builtin_mul_overflow(t, (int64_t)C, &t) ||
         t > (INT64_MAX >> 4))
