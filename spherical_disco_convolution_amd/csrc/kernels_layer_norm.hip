@@ -16,7 +16,7 @@
 // inner > 1 ("field" kernels): a lane owns V neighbouring points, the waves of
 // a workgroup split the channels, and the partial statistics meet in LDS.
 // inner == 1 ("row" kernels): a row's channels are spread over 1 to 1024 lanes.
-// Statistics are float32: the mean first, then the centred squares (no
+// Statistics are float32 at least: the mean first, then the centred squares (no
 // E[x^2] - mu^2), merged across waves as (mean, sum of squares) pairs.
 #include <hip/hip_runtime.h>
 
@@ -271,7 +271,11 @@ __global__ __launch_bounds__(CPW > 16 ? 1024 : 512, 4) void ln_fwd_field(
 
 // More channels than the registers of a workgroup hold: the waves walk the
 // channels three times (mean, centred squares, output), a point per lane; the
-// second and third walk find the tile in the caches.
+// second and third walk find the tile in the caches.  Runs of kRun terms of the walk
+// kernels' sums are added in float64: in float32 chains of C / 16 (rows: C / 1024)
+// terms rstd is 1e-4 off at 2^24 channels.
+constexpr int kRun = 64;
+
 template <typename TX, typename TY, bool RES>
 __global__ __launch_bounds__(1024) void ln_fwd_field_walk(
     const TX* __restrict__ x, const TX* __restrict__ res, const float* __restrict__ gamma,
@@ -285,30 +289,40 @@ __global__ __launch_bounds__(1024) void ln_fwd_field_walk(
     const bool active = g < total;
     const int64_t b = active ? split_index(g, inner, total) : 0;
     const int64_t o = b * C * inner + (active ? g - b * inner : 0);
-    float acc = 0.0f;
-    for (int c = wc; c < C; c += 16) {
-        const int64_t at = o + (int64_t)c * inner;
-        float f = active ? load_f(x, at) : 0.0f;
-        if constexpr (RES) {
-            if (active) {
-                store_f(s, at, f + load_f(res, at));
-                f = load_f(s, at);
+    double acc = 0.0;
+    for (int first = wc; first < C; first += 16 * kRun) {
+        const int end = min(C, first + 16 * kRun);
+        float run = 0.0f;
+        for (int c = first; c < end; c += 16) {
+            const int64_t at = o + (int64_t)c * inner;
+            float f = active ? load_f(x, at) : 0.0f;
+            if constexpr (RES) {
+                if (active) {
+                    store_f(s, at, f + load_f(res, at));
+                    f = load_f(s, at);
+                }
             }
+            run += f;
         }
-        acc += f;
+        acc += run;
     }
-    red[0][wc][lane] = acc;
+    red[0][wc][lane] = (float)acc;
     __syncthreads();
     float mu = 0.0f;
     for (int k = 0; k < 16; ++k) mu += red[0][k][lane];
     mu /= (float)C;
     const TX* src = RES ? s : x;
-    acc = 0.0f;
-    for (int c = wc; c < C; c += 16) {
-        const float d = active ? load_f(src, o + (int64_t)c * inner) - mu : 0.0f;
-        acc += d * d;
+    acc = 0.0;
+    for (int first = wc; first < C; first += 16 * kRun) {
+        const int end = min(C, first + 16 * kRun);
+        float run = 0.0f;
+        for (int c = first; c < end; c += 16) {
+            const float d = active ? load_f(src, o + (int64_t)c * inner) - mu : 0.0f;
+            run += d * d;
+        }
+        acc += run;
     }
-    red[1][wc][lane] = acc;
+    red[1][wc][lane] = (float)acc;
     __syncthreads();
     float m2 = 0.0f;
     for (int k = 0; k < 16; ++k) m2 += red[1][k][lane];
@@ -501,18 +515,24 @@ __global__ __launch_bounds__(1024) void ln_bwd_field_walk(
     const int64_t b = active ? split_index(g, inner, total) : 0;
     const int64_t o = b * C * inner + (active ? g - b * inner : 0);
     const float mu = active ? mean_in[g] : 0.0f, r = active ? rstd_in[g] : 0.0f;
-    float s1 = 0.0f, s2 = 0.0f;
+    double a1 = 0.0, a2 = 0.0;
     if (active)
-        for (int c = wc; c < C; c += 16) {
-            const int64_t at = o + (int64_t)c * inner;
-            const float t = load_f(gy, at) * (gamma ? gamma[c] : 1.0f);
-            s1 += t;
-            s2 += t * ((load_f(x, at) - mu) * r);
+        for (int first = wc; first < C; first += 16 * kRun) {
+            const int end = min(C, first + 16 * kRun);
+            float run1 = 0.0f, run2 = 0.0f;
+            for (int c = first; c < end; c += 16) {
+                const int64_t at = o + (int64_t)c * inner;
+                const float t = load_f(gy, at) * (gamma ? gamma[c] : 1.0f);
+                run1 += t;
+                run2 += t * ((load_f(x, at) - mu) * r);
+            }
+            a1 += run1;
+            a2 += run2;
         }
-    red[0][wc][lane] = s1;
-    red[1][wc][lane] = s2;
+    red[0][wc][lane] = (float)a1;
+    red[1][wc][lane] = (float)a2;
     __syncthreads();
-    s1 = s2 = 0.0f;
+    float s1 = 0.0f, s2 = 0.0f;
     for (int k = 0; k < 16; ++k) {
         s1 += red[0][k][lane];
         s2 += red[1][k][lane];
@@ -691,23 +711,33 @@ __global__ __launch_bounds__(1024) void ln_fwd_row_walk(
     float* __restrict__ mean_out, float* __restrict__ rstd_out, int C, float eps) {
     __shared__ float red[16];
     const int64_t row = blockIdx.x, o = row * C;
-    float a = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 1024) {
-        float f = load_f(x, o + c);
-        if constexpr (RES) {
-            store_f(s, o + c, f + load_f(res, o + c));
-            f = load_f(s, o + c);
+    double a = 0.0;
+    for (int first = threadIdx.x; first < C; first += 1024 * kRun) {
+        const int end = min(C, first + 1024 * kRun);
+        float run = 0.0f;
+        for (int c = first; c < end; c += 1024) {
+            float f = load_f(x, o + c);
+            if constexpr (RES) {
+                store_f(s, o + c, f + load_f(res, o + c));
+                f = load_f(s, o + c);
+            }
+            run += f;
         }
-        a += f;
+        a += run;
     }
-    const float mu = row_sum(a, 1024, red) / (float)C;
+    const float mu = row_sum((float)a, 1024, red) / (float)C;
     const TX* src = RES ? s : x;
-    a = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 1024) {
-        const float d = load_f(src, o + c) - mu;
-        a += d * d;
+    a = 0.0;
+    for (int first = threadIdx.x; first < C; first += 1024 * kRun) {
+        const int end = min(C, first + 1024 * kRun);
+        float run = 0.0f;
+        for (int c = first; c < end; c += 1024) {
+            const float d = load_f(src, o + c) - mu;
+            run += d * d;
+        }
+        a += run;
     }
-    const float r = rsqrtf(row_sum(a, 1024, red) / (float)C + eps);
+    const float r = rsqrtf(row_sum((float)a, 1024, red) / (float)C + eps);
     if (threadIdx.x == 0 && mean_out != nullptr) {
         mean_out[row] = mu;
         rstd_out[row] = r;
@@ -869,14 +899,20 @@ __global__ __launch_bounds__(1024) void ln_bwd_row_walk(
     __shared__ float red[16];
     const int64_t row = blockIdx.x, o = row * C;
     const float mu = mean_in[row], r = rstd_in[row];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 1024) {
-        const float q = load_f(gy, o + c) * (gamma ? gamma[c] : 1.0f);
-        s1 += q;
-        s2 += q * ((load_f(x, o + c) - mu) * r);
+    double a1 = 0.0, a2 = 0.0;
+    for (int first = threadIdx.x; first < C; first += 1024 * kRun) {
+        const int end = min(C, first + 1024 * kRun);
+        float run1 = 0.0f, run2 = 0.0f;
+        for (int c = first; c < end; c += 1024) {
+            const float q = load_f(gy, o + c) * (gamma ? gamma[c] : 1.0f);
+            run1 += q;
+            run2 += q * ((load_f(x, o + c) - mu) * r);
+        }
+        a1 += run1;
+        a2 += run2;
     }
-    s1 = row_sum(s1, 1024, red) / (float)C;
-    s2 = row_sum(s2, 1024, red) / (float)C;
+    const float s1 = row_sum((float)a1, 1024, red) / (float)C;
+    const float s2 = row_sum((float)a2, 1024, red) / (float)C;
     for (int c = threadIdx.x; c < C; c += 1024) {
         const float h = (load_f(x, o + c) - mu) * r;
         float f = r * (load_f(gy, o + c) * (gamma ? gamma[c] : 1.0f) - s1 - h * s2);
