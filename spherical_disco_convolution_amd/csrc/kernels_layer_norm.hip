@@ -550,15 +550,15 @@ __global__ __launch_bounds__(1024) void ln_bwd_field_walk(
 }
 
 // ggamma and gbeta partial sums of one channel over one slice of the points:
-// grid (C, slices); partial[slice][2][C].  For shapes the other kernels do not
-// hold in registers.
+// grid (C, slices), its first channel `first`; partial[slice][2][C].  For shapes the
+// other kernels do not hold in registers.
 template <typename TX, typename TG>
 __global__ __launch_bounds__(256) void ln_bwd_params_walk(
     const TX* __restrict__ x, const TG* __restrict__ gy, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, float* __restrict__ partial, int C, int64_t inner,
-    int64_t points) {
+    int64_t points, int first) {
     __shared__ float red[2][4];
-    const int c = blockIdx.x;
+    const int c = first + (int)blockIdx.x;
     float a = 0.0f, q = 0.0f;
     for (int64_t p = (int64_t)blockIdx.y * 256 + threadIdx.x; p < points;
          p += (int64_t)gridDim.y * 256) {
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(256) void ln_bwd_params_walk(
     if (threadIdx.x == 0) {
         float* row = partial + (size_t)blockIdx.y * 2 * C;
         row[c] = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-        row[C + c] = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+        row[(int64_t)C + c] = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     }
 }
 
@@ -940,13 +940,14 @@ __global__ __launch_bounds__(256) void ln_bwd_row_params_walk(
 }
 
 // ggamma and gbeta from partial[n][2][C]: 16 columns a workgroup, the rows in 64
-// interleaved slices, added in a fixed order.
+// interleaved slices, added in a fixed order; a launch starts at column `first`.
 __global__ __launch_bounds__(1024) void ln_reduce_params(const float* __restrict__ partial, int n,
-                                                         int C, float* __restrict__ ggamma,
+                                                         int C, int64_t first,
+                                                         float* __restrict__ ggamma,
                                                          float* __restrict__ gbeta) {
     __shared__ float red[64][17];
     const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    const int64_t i = (int64_t)blockIdx.x * 16 + col;
+    const int64_t i = first + (int64_t)blockIdx.x * 16 + col;
     float a = 0.0f;
     if (i < 2 * (int64_t)C) {
 #pragma unroll 8
@@ -1013,7 +1014,9 @@ RowShape row_shape(int C, int64_t rows, int v) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A launch may have at most 2^32 - 1 threads.
+// A launch may have at most 2^32 - 1 threads (more are cut off without an error): the
+// sums of more channels than that take several launches of up to 2^31.
+constexpr int64_t kLaunchThreads = (int64_t)1 << 31;
 bool fits(int64_t grid, int threads) { return grid <= 0xffffffffLL / threads && grid <= 0x7fffffff; }
 
 int done(const char* what) {
@@ -1204,10 +1207,14 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
             }
             if (params) {
                 n = (int)std::min<int64_t>(64, cdiv(total, 256));
-                KernelTimer timer("ln_bwd_params_walk", st);
-                hipLaunchKernelGGL((ln_bwd_params_walk<TX, TG>), dim3(C, n), dim3(256), 0, st, x, gy,
-                                   mean, rstd, part, C, inner, total);
-                if (int rc = done("ln_bwd_params_walk")) return rc;
+                constexpr int64_t kChannels = kLaunchThreads / 256;
+                for (int64_t c = 0; c < C; c += kChannels) {
+                    KernelTimer timer("ln_bwd_params_walk", st);
+                    hipLaunchKernelGGL((ln_bwd_params_walk<TX, TG>),
+                                       dim3((unsigned)std::min(C - c, kChannels), n), dim3(256), 0, st, x,
+                                       gy, mean, rstd, part, C, inner, total, (int)c);
+                    if (int rc = done("ln_bwd_params_walk")) return rc;
+                }
             }
         } else {
             const int vw = f.cpw == 16 ? V / 2 : V;
@@ -1238,10 +1245,14 @@ int bwd_typed(const TX* x, const TG* gy, const float* mean, const float* rstd, c
         }
     }
     if (!params) return DISCO_OK;
-    KernelTimer timer("ln_reduce_params", st);
-    hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(2 * (int64_t)C, 16)), dim3(1024), 0,
-                       st, partial, n, C, ggamma, gbeta);
-    return done("ln_reduce_params");
+    constexpr int64_t kColumns = kLaunchThreads / 1024 * 16;
+    for (int64_t i = 0; i < 2 * (int64_t)C; i += kColumns) {
+        KernelTimer timer("ln_reduce_params", st);
+        hipLaunchKernelGGL(ln_reduce_params, dim3((unsigned)cdiv(std::min(2 * (int64_t)C - i, kColumns), 16)),
+                           dim3(1024), 0, st, partial, n, C, i, ggamma, gbeta);
+        if (int rc = done("ln_reduce_params")) return rc;
+    }
+    return DISCO_OK;
 }
 
 }  // namespace

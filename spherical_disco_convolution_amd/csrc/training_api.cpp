@@ -96,7 +96,7 @@ int check_norm_sizes(int64_t outer, int32_t C, int64_t inner, int64_t* n) {
     if (outer < 0 || inner < 0 || C < 1)
         return set_error(DISCO_EINVAL, "sizes must be outer >= 0, C >= 1, inner >= 0 (got %lld, %d, "
                          "%lld)", (long long)outer, C, (long long)inner);
-    constexpr int32_t kMostChannels = 1 << 30;   // kernels add up to 2^24 to a channel in 32 bits
+    constexpr int32_t kMostChannels = 1 << 30;   // kernels add up to 2^16 to a channel in 32 bits
     if (C > kMostChannels)
         return set_error(DISCO_EUNSUPPORTED, "at most %d channels (got %d)", kMostChannels, C);
     int64_t t = 0;

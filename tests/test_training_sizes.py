@@ -29,7 +29,7 @@ def test_orthogonalize_takes_the_largest_side():
 @pytest.mark.parametrize("C", [TOP, TOP - 1023, 2 ** 30 + 1])
 @pytest.mark.parametrize("inner", [1, 2])
 def test_layer_norm_refuses_channel_counts_that_leave_no_room_to_stride(C, inner):
-    # a lane's next channel is up to 2^24 further on, in 32 bits
+    # a lane's next channel is up to 2^16 further on, in 32 bits
     lib, fake = sdc._lib, ctypes.c_void_p(0x1000)
     assert lib.disco_layer_norm_bwd_workspace(1, C, inner) == sdc.DISCO_EUNSUPPORTED
     assert "1073741824" in lib.disco_last_error().decode()
