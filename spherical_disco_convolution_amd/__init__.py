@@ -566,6 +566,11 @@ def _norm_view(x, axis):
     return math.prod(before), shape[axis], math.prod(after), before + after
 
 
+def _same_dtype(t, name, out_dtype):
+    if out_dtype is not None and t.dtype != out_dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, out_dtype is {out_dtype}")
+
+
 def _f32_ptr(t, name, shape):
     """Pointer of an optional float32 tensor."""
     if t is None:
@@ -607,6 +612,7 @@ def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, a
         y = torch.empty_like(x, dtype=x.dtype if out_dtype is None else out_dtype)
     else:
         _need(y, "y", x.shape)
+        _same_dtype(y, "y", out_dtype)
     if need_stats:
         mean = x.new_empty(points, dtype=torch.float32)
         rstd = torch.empty_like(mean)
@@ -698,6 +704,7 @@ def orthogonalize(m, out=None, out_dtype=None, steps: int = 5, coeffs=None, eps:
         out = torch.empty_like(m, dtype=m.dtype if out_dtype is None else out_dtype)
     else:
         _need(out, "out", m.shape)
+        _same_dtype(out, "out", out_dtype)
     ws, nws = _ortho_workspace(batch, rows, cols, m, "orthogonalize")
     _check(_lib.disco_orthogonalize(m.data_ptr(), _dtype_code(m), out.data_ptr(), _dtype_code(out),
                                     batch, rows, cols, steps, _coeffs(coeffs), eps,
