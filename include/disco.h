@@ -328,6 +328,8 @@ int disco_layer_norm_bwd(const void* x, int x_dtype, const void* gy, int gy_dtyp
  * once to its own, so that a bfloat16 result is the float32 one rounded.  Before
  * that it is within 1e-5 (relative, of the whole matrix) for five default steps; a
  * further step can amplify its error by up to a, as in any float32 arithmetic.
+ * Entries of X are held to 2^-36 at least, so a matrix whose norm is far below eps
+ * loses digits.
  * steps lies in 1..64.  coeffs: three floats in HOST memory, or NULL
  * for 3.4445, -4.7750, 2.0315; EUNSUPPORTED where they would carry the
  * singular values (above about 3.5) or the polynomial a + b s^2 + c s^4 (above

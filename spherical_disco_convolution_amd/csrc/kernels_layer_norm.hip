@@ -8,9 +8,12 @@
 //   gx = r (t - 1/C sum_c t - h 1/C sum_c t h) (+ gsum)
 //   ggamma_c = sum_points gy h,   gbeta_c = sum_points gy.
 //
-// Both directions move each element once and do about ten operations on it,
-// so HBM bounds them; the kernels hold a point's channels in registers
-// between the statistics and the output so that nothing is read twice.  Forward,
+// Both directions do about ten operations on an element, so HBM bounds them; the
+// kernels hold a point's channels in registers between the statistics and the
+// output so that nothing is read twice.  Only the walk kernels, for what registers
+// do not hold, read everything two or three times (backward of 181 x 360 points
+// float32: 256 channels in registers 56 us, 300 by walks 104 us, 512 186 us; the
+// bytes take 40, 47 and 80 us at 5 TB/s).  Forward,
 // 721 x 1440 x 128 bf16 with a residual (1.07 GB): 228 us, 4.7 TB/s, where a
 // large copy reaches 4.9 to 5.2.
 // inner > 1 ("field" kernels): a lane owns V neighbouring points, the waves of
@@ -1073,7 +1076,8 @@ int fwd_typed(const TX* x, const TX* res, const float* gamma, const float* beta,
         return done("ln_fwd_field_walk");
     }
     // 16 bytes a lane (8 where a wave holds 32 channels: 64 registers of data
-    // either way) where that leaves 512 workgroups, else a point a lane
+    // either way) where that leaves 512 workgroups, else a point a lane; the step is
+    // felt by bf16 fields just below it (128 x 361 x 720: 41 us, the bytes take 27)
     const int vw = f.cpw > 16 ? V16 / 2 : V16;
     const bool wide = inner >= vw && outer * cdiv(inner, vw) >= (int64_t)512 * 64 * f.wp;
     const int V = wide ? vw : 1;

@@ -28,8 +28,8 @@
 // ns_panel a step per launch, ns_product a tiled product per launch.  What
 // bounds them: the first two their chain of barriers and LDS round trips (2 to 8
 // us a step), the third launches of 5 us each up to about 512 x 512 and the
-// matrix cores above: 4096 x 4096 with three products 1.0 to 1.2 PFLOP/s of
-// float16 work, where a large float16 library product reaches 1.3 to 1.5.
+// matrix cores above: at 4096 x 4096 they do 0.84 to 0.97 PFLOP/s of float16 work,
+// where a large float16 library product reaches 1.3 to 1.5 (4.3 to 4.6 ms for five steps).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -479,10 +479,9 @@ __device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t total) {
 }
 
 // Tile number -> tile row and column, by bands of kBand tile rows, column by
-// column within a band, so that neighbouring numbers form squares and a die's
-// tiles share operands in its L2: in all 2643 us at 4096 x 4096
-// bf16 and 419 us at 1024 x 4096 float32, without die_order 2772 and 447 us, with
-// neither it nor bands 2666 and 449 us.  Symmetric results have the lower triangle only.
+// column within a band, so that neighbouring numbers form squares and a die's tiles share
+// operands in its L2: in all 419 us at 1024 x 4096, without die_order 447 us, with
+// neither it nor bands 449 us.  Symmetric results have the lower triangle only.
 constexpr int kBand = 8;
 
 template <Epilogue E>
