@@ -140,9 +140,8 @@ def prepare(case, seed):
         st["bias"] = None
         if case["bias"]:
             # logarithms of quadrature weights from pole to pole; a twentieth of the points is masked out
-            n = lk[0]
-            w = torch.sin((torch.arange(n, device="cuda", dtype=torch.float32) + 0.5) * (math.pi / n)).log()
-            w = w.repeat(case["seqs"])
+            w = torch.cat([torch.sin((torch.arange(n, device="cuda", dtype=torch.float32) + 0.5) * (math.pi / n)).log()
+                           for n in lk])
             st["bias"] = torch.where(torch.rand(w.shape, generator=gen, device="cuda") < 0.05, -math.inf, w)
         if case["op"] == "attn_bwd":
             o, st["lse"] = _attn_fwd_plain(st)
