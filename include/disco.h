@@ -364,6 +364,124 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
                     int32_t cols, int32_t steps, const float* coeffs, float eps, void* workspace,
                     int64_t workspace_bytes, void* stream);
 
+/* ---- Attention over points ----------------------------------------------
+ * Global mixing beside the convolution's local one: softmax attention over the
+ * points of fields or the tokens of series, with quadrature weights as an
+ * additive term of each key (the AttentionS2 page: softmax attention whose sums
+ * over the sphere are quadratures).  For query i and key j of one sequence, and
+ * query head h reading key head h / (hq / hkv):
+ *   x_ij = scale * q_i . k_j + key_bias_j,  lse_i = log sum_j exp x_ij
+ *   o_i  = sum_j exp(x_ij - lse_i) v_j
+ * Tokens of all sequences lie one after another ("packed").  cu_q and cu_k,
+ * [n_seq + 1] in DEVICE memory, hold each sequence's first token and the end of
+ * the last; NULL stands for n_seq sequences of equal length (a dense batch).
+ * Boundaries out of order or out of range are cut to the tensors; tokens before
+ * the first and behind the last sequence are not read, and their results are
+ * left as they were.
+ *  - causal != 0: query i of a sequence of Lq queries and Lk keys sees keys
+ *    j <= i + Lk - Lq (the last query sees all keys).
+ *  - key_bias [total_k] float32 or NULL; -inf, or anything below -1e30, leaves
+ *    a key out, whatever k and v hold there.  It is a constant: no gradient.
+ *  - a query that sees no key gets o = 0, lse = -inf and gradients of zero.
+ *  - what a causal query does not see has to be finite all the same: a NaN or an
+ *    infinity there may reach queries up to 63 keys earlier.
+ * float32 tensors are computed in float32; for bfloat16 ones products are of
+ * bfloat16 operands summed in float32, with the weights exp(x - max) and the
+ * gradients of x rounded to bfloat16 (the bf16 bar).  Sums run in a fixed order:
+ * results are reproducible.  Any alignment and strides are taken; head sizes,
+ * strides and addresses that are multiples of 16 bytes are much faster. */
+typedef struct disco_attention_desc {
+    int64_t total_q, total_k;       /* tokens of all sequences; tokens * heads < 2^31 - 4096 */
+    int32_t n_seq;                  /* >= 1 */
+    int32_t hq, hkv;                /* heads of q and o, of k and v; hkv divides hq */
+    int32_t dk, dv;                 /* sizes of a head of q and k, of v and o: 1..128 */
+    int32_t dtype;                  /* of every tensor but lse and key_bias */
+    int32_t causal;
+    float   scale;                  /* finite, > 0 */
+    /* strides in elements, token to token and head to head (a head's elements
+     * lie together); those of results may be columns of one buffer */
+    int64_t q_stride[2], k_stride[2], v_stride[2], o_stride[2];
+    int64_t go_stride[2], gq_stride[2], gk_stride[2], gv_stride[2];   /* the gradient call only */
+} disco_attention_desc;
+
+/* Bytes of device workspace of the forward call (few rows over many keys are
+ * split along the keys and joined), or a negative status. */
+int64_t disco_attention_fwd_workspace(const disco_attention_desc* desc);
+
+/* o [total_q, hq, dv]; lse [total_q, hq] float32, dense, or NULL (the gradient
+ * needs it). */
+int disco_attention_fwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
+                        const float* key_bias, const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace of the gradient call, or a negative status. */
+int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc);
+
+/* Gradients of sum(go * o): gq, and gk with gv, NULL to skip (not all); from the
+ * forward's o and lse.  gk and gv are summed over the heads of their group. */
+int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
+                        const float* key_bias, const int32_t* cu_q, const int32_t* cu_k, const void* o,
+                        const float* lse, const void* go, void* gq, void* gk, void* gv, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* ---- Norm and rotation of queries and keys -------------------------------
+ * Each head of q [tokens, hq, d] and k [tokens, hkv, d] is divided by its root
+ * mean square and turned by its token's position:
+ *   n = x / sqrt(mean(x^2) + eps) * weight      (weight [d] float32, NULL for ones)
+ *   pair p < rot/2 turns by positions[token, p * axes / (rot/2)] * inv_freq[p]
+ * Pairs are (p, p + rot/2), or (2 p, 2 p + 1) where interleaved != 0; elements
+ * from rot on do not turn.  positions [tokens, axes], int32 or float32 (times of a
+ * series; colatitude and longitude of a point, where whole frequencies are
+ * periodic in longitude); scaled tables for long series are the caller's
+ * inv_freq.  Angles are taken in float64.  Heads are independent: a NaN stays in
+ * its own. */
+typedef struct disco_qk_desc {
+    int64_t tokens;                 /* < 2^31 */
+    int32_t hq, hkv, d;             /* hkv may be 0; d in 1..256 */
+    int32_t dtype;                  /* of every tensor but weights, positions and inv_freq */
+    int32_t rot;                    /* elements that turn: even, 0..d */
+    int32_t axes;                   /* 1..4 */
+    int32_t positions_int32;        /* != 0: int32, else float32 */
+    int32_t interleaved;
+    float   eps;
+    int64_t q_stride[2], k_stride[2];           /* token to token, head to head, in elements */
+    int64_t q_out_stride[2], k_out_stride[2];   /* of the results: q_out, k_out; gq, gk of the gradient */
+    int64_t gq_stride[2], gk_stride[2];         /* of gq_out, gk_out; the gradient call only */
+} disco_qk_desc;
+
+int disco_qk_norm_rope_fwd(const disco_qk_desc* desc, const void* q, const void* k, const float* q_weight,
+                           const float* k_weight, const void* positions, const float* inv_freq, void* q_out,
+                           void* k_out, void* stream);
+
+/* Bytes of device workspace of the weights' gradients, or a negative status. */
+int64_t disco_qk_norm_rope_bwd_workspace(int32_t d);
+
+/* Gradients of sum(gq_out * q_out) + sum(gk_out * k_out) in q, k (what went into
+ * the forward) and, where given, the weights ([d] float32, over all tokens and
+ * heads; they need the workspace).  No tokens: weights' gradients of zero. */
+int disco_qk_norm_rope_bwd(const disco_qk_desc* desc, const void* q, const void* k, const void* gq_out,
+                           const void* gk_out, const float* q_weight, const float* k_weight, const void* positions,
+                           const float* inv_freq, void* gq, void* gk, float* gq_weight, float* gk_weight,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- Dropout ---------------------------------------------------------------
+ *   y = residual + (kept ? x / (1 - P) : 0),   P = t / 65536, t = round(65536 p)
+ * Element e of n is kept where half-word e % 8 (the low half of a word first) of
+ * block e / 8 is not below t; a block is the four words of the counter-based
+ * generator Philox4x32 (ten rounds) at counter (block, offset) under the key
+ * seed.  So the mask is a function of (seed, offset, e): the gradient computes it
+ * again from the same three, and nothing is stored.  step (device memory, or
+ * NULL) is added to offset, so that a captured call draws anew at each replay.
+ * x, residual (or NULL) of x_dtype, y of y_dtype; y may be x where the types are
+ * the same.  p lies in [0, 1 - 2^-17); n is at most 2^40.  A dropped element is
+ * zero whatever x holds. */
+int disco_dropout_fwd(const void* x, int x_dtype, const void* residual, void* y, int y_dtype, int64_t n, double p,
+                      uint64_t seed, uint64_t offset, const int64_t* step, void* stream);
+
+/* gx = kept ? gy / (1 - P) : 0; the residual's gradient is gy itself. */
+int disco_dropout_bwd(const void* gy, int gy_dtype, void* gx, int gx_dtype, int64_t n, double p, uint64_t seed,
+                      uint64_t offset, const int64_t* step, void* stream);
+
 /* Per-kernel timing, for benchmarks and profiling (not part of the pages'
  * method).  With enable != 0, every kernel the library launches from then on
  * is bracketed by a pair of HIP events recorded on its launch stream; with 0,

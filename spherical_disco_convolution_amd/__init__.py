@@ -21,6 +21,13 @@ Entry points (same names as the C ABI, without the ``disco_`` prefix):
     layer_norm_bwd(x, gy, mean, rstd, gamma, gsum=...) -> (gx, ggamma, gbeta)
     orthogonalize(m, ...) -> o                  Newton-Schulz products
     muon_step(w, grad, momentum, lr, ...) -> (w, momentum, w16)   one optimiser step
+  global mixing beside it:
+    attention_fwd(q, k, v, key_bias=..., cu_q=..., causal=...) -> (o, lse)
+    attention_bwd(q, k, v, o, lse, go, ...) -> (gq, gk, gv)
+    qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, ...) -> (q_out, k_out)
+    qk_norm_rope_bwd(q, k, gq_out, gk_out, ...) -> (gq, gk, gq_weight, gk_weight)
+    dropout_fwd(x, p, seed, offset, residual=...) -> y
+    dropout_bwd(gy, p, seed, offset) -> gx
 
 With stream=s a call's kernels run on s, and its results are there once s has
 come to them.  Inputs have to be ready on s (s.wait_stream where another stream
@@ -61,6 +68,22 @@ class _Desc(ctypes.Structure):
         ("kernel_shape", ctypes.c_int32 * 2),
         ("theta_cutoff", ctypes.c_double),
     ]
+
+
+class _AttentionDesc(ctypes.Structure):
+    _fields_ = [
+        ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+        ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+    ] + [(n + "_stride", ctypes.c_int64 * 2) for n in ("q", "k", "v", "o", "go", "gq", "gk", "gv")]
+
+
+class _QkDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+        ("positions_int32", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+    ] + [(n + "_stride", ctypes.c_int64 * 2) for n in ("q", "k", "q_out", "k_out", "gq", "gk")]
 
 
 def _load():
@@ -113,6 +136,19 @@ def _load():
                                            ctypes.c_float, ctypes.c_int, ctypes.c_float,
                                            ctypes.c_float, I32, I32, I32, I32, P, ctypes.c_float, P,
                                            I64, P]),
+        "disco_attention_fwd_workspace": (I64, [ctypes.POINTER(_AttentionDesc)]),
+        "disco_attention_fwd": (ctypes.c_int, [ctypes.POINTER(_AttentionDesc), P, P, P, P, P, P, P, P, P, I64, P]),
+        "disco_attention_bwd_workspace": (I64, [ctypes.POINTER(_AttentionDesc)]),
+        "disco_attention_bwd": (ctypes.c_int, [ctypes.POINTER(_AttentionDesc), P, P, P, P, P, P, P, P, P, P, P, P, P,
+                                               I64, P]),
+        "disco_qk_norm_rope_fwd": (ctypes.c_int, [ctypes.POINTER(_QkDesc), P, P, P, P, P, P, P, P, P]),
+        "disco_qk_norm_rope_bwd_workspace": (I64, [I32]),
+        "disco_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(_QkDesc), P, P, P, P, P, P, P, P, P, P, P, P, P, I64,
+                                                  P]),
+        "disco_dropout_fwd": (ctypes.c_int, [P, ctypes.c_int, P, P, ctypes.c_int, I64, D, ctypes.c_uint64,
+                                             ctypes.c_uint64, P, P]),
+        "disco_dropout_bwd": (ctypes.c_int, [P, ctypes.c_int, P, ctypes.c_int, I64, D, ctypes.c_uint64,
+                                             ctypes.c_uint64, P, P]),
         "disco_kernel_timing": (ctypes.c_int, [ctypes.c_int]),
         "disco_kernel_timing_read": (ctypes.c_int, [ctypes.c_char_p, I32, ctypes.POINTER(D),
                                                     ctypes.POINTER(I64), I32]),
@@ -133,7 +169,10 @@ EXPORTED = ("disco_psi_build", "disco_psi_query", "disco_psi_export", "disco_psi
             "disco_fused_is_spectral", "disco_contract_transpose", "disco_einsum_grad_xk",
             "disco_einsum_grad_w", "disco_fused_bwd", "disco_layer_norm_fwd",
             "disco_layer_norm_bwd_workspace", "disco_layer_norm_bwd", "disco_orthogonalize_workspace",
-            "disco_orthogonalize", "disco_muon_step", "disco_kernel_timing", "disco_kernel_timing_read",
+            "disco_orthogonalize", "disco_muon_step", "disco_attention_fwd_workspace", "disco_attention_fwd",
+            "disco_attention_bwd_workspace", "disco_attention_bwd", "disco_qk_norm_rope_fwd",
+            "disco_qk_norm_rope_bwd_workspace", "disco_qk_norm_rope_bwd", "disco_dropout_fwd",
+            "disco_dropout_bwd", "disco_kernel_timing", "disco_kernel_timing_read",
             "disco_last_error", "disco_version")
 
 
@@ -764,3 +803,306 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
         lr, beta, int(nesterov), weight_decay, scale, groups, rows, cols, steps, _coeffs(coeffs), eps,
         ws.data_ptr() if ws is not None else None, nws, _stream()), "muon_step")
     return w_out, momentum_out, w16
+
+
+# ----------------------------------------------------------------------------
+# attention
+# ----------------------------------------------------------------------------
+def _tokens(t, name):
+    """(tokens, heads, d, (token stride, head stride)) of [T, H, D] or of a batch
+    [B, T, H, D] whose sequences lie one after another."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
+    size, st = t.shape, t.stride()
+    if size[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"the elements of {name}'s heads must lie together")
+    ts = st[-3]
+    if t.dim() == 4:
+        if size[1] == 1:
+            ts = st[0]
+        elif size[0] > 1 and st[0] != size[1] * ts and t.numel():
+            raise ValueError(f"{name}'s sequences must lie one after another")
+    n = math.prod(size[:-2])
+    return n, size[-2], size[-1], (ts if n > 1 else size[-2] * size[-1], st[-2] if size[-2] > 1 else size[-1])
+
+
+def _set_stride(desc, name, stride):
+    s = getattr(desc, name + "_stride")
+    s[0], s[1] = stride
+
+
+def _like(t, name, shape, dtype, make):
+    """A result: `t` as given, or a new dense tensor of make's device."""
+    if t is None:
+        return make.new_empty(shape, dtype=dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    return t
+
+
+def _boundaries(cu, name, n_seq):
+    torch = _torch()
+    if cu is None:
+        return None
+    if cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous() or cu.shape[0] < 2:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of sequences + 1 boundaries")
+    if cu.shape[0] != n_seq + 1:
+        raise ValueError(f"{name} has {cu.shape[0]} boundaries, expected {n_seq + 1}")
+    return cu.data_ptr()
+
+
+def _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale):
+    """The description of a call, and the pointers of its options."""
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"q, k and v must have the same dtype (got {q.dtype}, {k.dtype}, {v.dtype})")
+    if not q.dim() == k.dim() == v.dim():
+        raise ValueError("q, k and v must have the same number of dimensions")
+    d = _AttentionDesc()
+    tq, hq, dk, sq = _tokens(q, "q")
+    tk, hkv, dk2, sk = _tokens(k, "k")
+    tv, hv, dv, sv = _tokens(v, "v")
+    if dk2 != dk:
+        raise ValueError(f"heads of k have {dk2} elements, those of q {dk}")
+    if (tv, hv) != (tk, hkv) or v.shape[:-1] != k.shape[:-1]:
+        raise ValueError(f"v has shape {tuple(v.shape)}, k {tuple(k.shape)}: tokens and heads must agree")
+    if hkv < 1 or hq % hkv:
+        raise ValueError(f"the heads of k and v ({hkv}) must divide those of q ({hq})")
+    if q.dim() == 4:
+        if cu_q is not None or cu_k is not None:
+            raise ValueError("boundaries are for packed tensors [tokens, heads, d]")
+        if k.shape[0] != q.shape[0]:
+            raise ValueError(f"q has {q.shape[0]} sequences, k {k.shape[0]}")
+        n_seq = q.shape[0]
+    else:
+        n_seq = cu_q.shape[0] - 1 if cu_q is not None else cu_k.shape[0] - 1 if cu_k is not None else 1
+    n_seq = max(n_seq, 1)
+    _int32(n_seq, hq, hkv, dk, dv)
+    d.total_q, d.total_k, d.n_seq, d.hq, d.hkv, d.dk, d.dv = tq, tk, n_seq, hq, hkv, dk, dv
+    d.dtype, d.causal = _dtype_code(q), int(bool(causal))
+    d.scale = dk ** -0.5 if scale is None and dk else 1.0 if scale is None else float(scale)
+    for name, s in (("q", sq), ("k", sk), ("v", sv)):
+        _set_stride(d, name, s)
+    return d, (_f32_ptr(key_bias, "key_bias", k.shape[:-2]) if key_bias is None or key_bias.dim() != 1 else
+               _f32_ptr(key_bias, "key_bias", (tk,)), _boundaries(cu_q, "cu_q", n_seq), _boundaries(cu_k, "cu_k", n_seq))
+
+
+def attention_fwd(q, k, v, key_bias=None, cu_q=None, cu_k=None, causal: bool = False, scale: float | None = None,
+                  out=None, need_lse: bool = True, stream=None):
+    """Softmax attention o_i = sum_j softmax_j(scale q_i.k_j + key_bias_j) v_j.
+
+    q [T, Hq, dk], k [S, Hkv, dk], v [S, Hkv, dv] hold the tokens of all
+    sequences one after another, with int32 boundaries cu_q, cu_k (sequences + 1,
+    on the device; None: one sequence), or are a batch [B, T, Hq, dk] etc. of
+    equal lengths.  Hkv divides Hq: query head h reads head h // (Hq / Hkv).  Token
+    and head strides are free (columns of a projection's output).  key_bias
+    (float32, a value a key: the logarithms of quadrature weights): -inf, or
+    anything below -1e30, leaves a key out.  causal: query i sees keys up to
+    i + Lk - Lq of its sequence.  A query that sees none gets zeros and
+    lse = -inf.  scale None: dk ** -0.5.
+
+    Returns (o, lse): o in q's dtype, [T, Hq, dv]; lse float32 [T, Hq], None with
+    need_lse=False.  What belongs to no sequence is left as it was."""
+    if stream is not None:
+        return _on(stream, attention_fwd, q, k, v, key_bias, cu_q, cu_k, causal, scale, out, need_lse)
+    torch = _torch()
+    d, (bptr, cq, ck) = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
+    out = _like(out, "out", tuple(q.shape[:-1]) + (v.shape[-1],), q.dtype, q)
+    _set_stride(d, "o", _tokens(out, "out")[3])
+    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if need_lse else None
+    nws = _lib.disco_attention_fwd_workspace(ctypes.byref(d))
+    if nws < 0:
+        _check(nws, "attention_fwd")
+    ws = _workspace(nws, q)
+    _check(_lib.disco_attention_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck,
+                                    out.data_ptr(), lse.data_ptr() if need_lse else None,
+                                    ws.data_ptr() if ws is not None else None, nws, _stream()), "attention_fwd")
+    return out, lse
+
+
+def attention_bwd(q, k, v, o, lse, go, key_bias=None, cu_q=None, cu_k=None, causal: bool = False,
+                  scale: float | None = None, need_gq: bool = True, need_gkv: bool = True, gq=None, gk=None, gv=None,
+                  stream=None):
+    """Gradients (gq, gk, gv) of sum(go * attention_fwd(q, k, v)[0]), in q's dtype;
+    entries not asked for are None.  o and lse are the forward's.  gq, gk and gv may
+    be given, as columns of one buffer too; gk and gv are summed over the heads of
+    their group."""
+    if stream is not None:
+        return _on(stream, attention_bwd, q, k, v, o, lse, go, key_bias, cu_q, cu_k, causal, scale, need_gq, need_gkv,
+                   gq, gk, gv)
+    d, (bptr, cq, ck) = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
+    oshape = tuple(q.shape[:-1]) + (v.shape[-1],)
+    for t, name in ((o, "o"), (go, "go")):
+        _like(t, name, oshape, q.dtype, q)
+        _set_stride(d, name, _tokens(t, name)[3])
+    if lse is None:
+        raise ValueError("lse of the forward pass is needed")
+    lptr = _f32_ptr(lse, "lse", q.shape[:-1])
+    gq = _like(gq, "gq", q.shape, q.dtype, q) if need_gq else None
+    gk = _like(gk, "gk", k.shape, q.dtype, q) if need_gkv else None
+    gv = _like(gv, "gv", v.shape, q.dtype, q) if need_gkv else None
+    for t, name in ((gq, "gq"), (gk, "gk"), (gv, "gv")):
+        if t is not None:
+            _set_stride(d, name, _tokens(t, name)[3])
+    nws = _lib.disco_attention_bwd_workspace(ctypes.byref(d))
+    if nws < 0:
+        _check(nws, "attention_bwd")
+    ws = _workspace(nws, q)
+    _check(_lib.disco_attention_bwd(
+        ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck, o.data_ptr(), lptr, go.data_ptr(),
+        gq.data_ptr() if need_gq else None, gk.data_ptr() if need_gkv else None, gv.data_ptr() if need_gkv else None,
+        ws.data_ptr() if ws is not None else None, nws, _stream()), "attention_bwd")
+    return gq, gk, gv
+
+
+# ----------------------------------------------------------------------------
+# norm and rotation of queries and keys
+# ----------------------------------------------------------------------------
+def _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps):
+    torch = _torch()
+    if k.dtype != q.dtype:
+        raise ValueError(f"q and k must have the same dtype (got {q.dtype}, {k.dtype})")
+    tokens, hq, dim, sq = _tokens(q, "q")
+    tk, hkv, dim2, sk = _tokens(k, "k")
+    if k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or dim2 != dim:
+        raise ValueError(f"q has shape {tuple(q.shape)}, k {tuple(k.shape)}: only the heads may differ")
+    _int32(hq, hkv, dim)
+    d = _QkDesc()
+    d.tokens, d.hq, d.hkv, d.d, d.dtype = tokens, hq, hkv, dim, _dtype_code(q)
+    d.rot, d.axes, d.interleaved, d.eps = 0, 1, int(bool(interleaved)), float(eps)
+    _set_stride(d, "q", sq)
+    _set_stride(d, "k", sk)
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq must both be given or both be None")
+    pptr = fptr = None
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have one dimension")
+        fptr = _f32_ptr(inv_freq, "inv_freq", inv_freq.shape)
+        d.rot = 2 * inv_freq.shape[0]
+        lead = tuple(q.shape[:-2])
+        d.axes = positions.shape[-1] if positions.dim() == len(lead) + 1 else 1
+        _need(positions, "positions", lead + ((d.axes,) if positions.dim() == len(lead) + 1 else ()))
+        if positions.dtype not in (torch.int32, torch.float32):
+            raise ValueError(f"positions must be int32 or float32 (got {positions.dtype})")
+        d.positions_int32 = int(positions.dtype == torch.int32)
+        pptr = positions.data_ptr()
+    return d, (_f32_ptr(q_weight, "q_weight", (dim,)), _f32_ptr(k_weight, "k_weight", (dim,)), pptr, fptr)
+
+
+def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, interleaved: bool = False,
+                     eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of each head of q [T, Hq, d] and k [T, Hkv, d] (or with
+    a batch dimension before), times weights [d], then its pairs turned by position:
+    pair p by positions[t, p * axes // pairs] * inv_freq[p], for the first
+    2 * len(inv_freq) elements.  Pairs are (p, p + pairs), or (2p, 2p + 1) with
+    interleaved.  positions: int32 or float32, [T] or [T, axes].  Without positions
+    and inv_freq nothing turns.  Returns (q_out, k_out) in q's dtype."""
+    if stream is not None:
+        return _on(stream, qk_norm_rope_fwd, q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps, q_out,
+                   k_out)
+    d, (qw, kw, pptr, fptr) = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
+    q_out = _like(q_out, "q_out", q.shape, q.dtype, q)
+    k_out = _like(k_out, "k_out", k.shape, q.dtype, k)
+    _set_stride(d, "q_out", _tokens(q_out, "q_out")[3])
+    _set_stride(d, "k_out", _tokens(k_out, "k_out")[3])
+    _check(_lib.disco_qk_norm_rope_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), qw, kw, pptr, fptr,
+                                       q_out.data_ptr(), k_out.data_ptr(), _stream()), "qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, gq_out, gk_out, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                     interleaved: bool = False, eps: float = 1e-6, need_gweights: bool = True, gq=None, gk=None,
+                     stream=None):
+    """Gradients (gq, gk, gq_weight, gk_weight) of sum(gq_out * q_out) +
+    sum(gk_out * k_out); q and k are what went into the forward.  The weights'
+    gradients are float32 sums over tokens and heads (None with
+    need_gweights=False).  gq and gk may be given, as columns of one buffer too."""
+    if stream is not None:
+        return _on(stream, qk_norm_rope_bwd, q, k, gq_out, gk_out, q_weight, k_weight, positions, inv_freq, interleaved,
+                   eps, need_gweights, gq, gk)
+    torch = _torch()
+    d, (qw, kw, pptr, fptr) = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
+    _like(gq_out, "gq_out", q.shape, q.dtype, q)
+    _like(gk_out, "gk_out", k.shape, q.dtype, k)
+    gq = _like(gq, "gq", q.shape, q.dtype, q)
+    gk = _like(gk, "gk", k.shape, q.dtype, k)
+    for t, field, name in ((gq_out, "gq", "gq_out"), (gk_out, "gk", "gk_out"), (gq, "q_out", "gq"), (gk, "k_out", "gk")):
+        _set_stride(d, field, _tokens(t, name)[3])
+    gqw = gkw = ws = None
+    nws = 0
+    if need_gweights:
+        gqw = q.new_empty((d.d,), dtype=torch.float32)
+        gkw = torch.empty_like(gqw)
+        nws = _lib.disco_qk_norm_rope_bwd_workspace(d.d)
+        if nws < 0:
+            _check(nws, "qk_norm_rope_bwd")
+        ws = _workspace(nws, q)
+    _check(_lib.disco_qk_norm_rope_bwd(
+        ctypes.byref(d), q.data_ptr(), k.data_ptr(), gq_out.data_ptr(), gk_out.data_ptr(), qw, kw, pptr, fptr,
+        gq.data_ptr(), gk.data_ptr(), gqw.data_ptr() if need_gweights else None,
+        gkw.data_ptr() if need_gweights else None, ws.data_ptr() if ws is not None else None, nws, _stream()),
+        "qk_norm_rope_bwd")
+    return gq, gk, gqw, gkw
+
+
+# ----------------------------------------------------------------------------
+# dropout
+# ----------------------------------------------------------------------------
+def _random_state(seed, offset, step):
+    """seed and offset as unsigned 64-bit words, and the pointer of step."""
+    for v, name in ((seed, "seed"), (offset, "offset")):
+        if not -2 ** 63 <= v < 2 ** 64:
+            raise ValueError(f"{name} must fit 64 bits (got {v})")
+    if step is not None:
+        if step.dtype != _torch().int64 or step.numel() != 1:
+            raise ValueError("step must be an int64 tensor of one element")
+        step = step.data_ptr()
+    return seed & (2 ** 64 - 1), offset & (2 ** 64 - 1), step
+
+
+def dropout_fwd(x, p: float, seed: int, offset: int = 0, step=None, residual=None, y=None, out_dtype=None, stream=None):
+    """y = residual + x / (1 - p) where kept, residual where dropped (p rounded to
+    a multiple of 2 ** -16).  The mask is a function of (seed, offset, element), never
+    stored: give each call of a training step an offset of its own, and its gradient
+    the same.  step: int64 on the device, added to offset (a captured call draws anew
+    at each replay if the graph, or the program between replays, counts it up).  y
+    has out_dtype, or x's dtype, and may be x."""
+    if stream is not None:
+        return _on(stream, dropout_fwd, x, p, seed, offset, step, residual, y, out_dtype)
+    torch = _torch()
+    _need(x, "x", x.shape)
+    seed, offset, sptr = _random_state(seed, offset, step)
+    if residual is not None:
+        _need(residual, "residual", x.shape)
+        if residual.dtype != x.dtype:
+            raise ValueError(f"residual must have x's dtype ({x.dtype})")
+    if y is None:
+        y = torch.empty_like(x, dtype=x.dtype if out_dtype is None else out_dtype)
+    else:
+        _need(y, "y", x.shape)
+        _same_dtype(y, "y", out_dtype)
+    _check(_lib.disco_dropout_fwd(x.data_ptr(), _dtype_code(x), residual.data_ptr() if residual is not None else None,
+                                  y.data_ptr(), _dtype_code(y), x.numel(), p, seed, offset, sptr, _stream()),
+           "dropout_fwd")
+    return y
+
+
+def dropout_bwd(gy, p: float, seed: int, offset: int = 0, step=None, gx=None, gx_dtype=None, stream=None):
+    """gx = gy / (1 - p) where the forward of the same (seed, offset + step) kept,
+    else 0; the residual's gradient is gy itself.  gx has gx_dtype, or float32, and
+    may be gy."""
+    if stream is not None:
+        return _on(stream, dropout_bwd, gy, p, seed, offset, step, gx, gx_dtype)
+    torch = _torch()
+    _need(gy, "gy", gy.shape)
+    seed, offset, sptr = _random_state(seed, offset, step)
+    if gx is None:
+        gx = torch.empty_like(gy, dtype=torch.float32 if gx_dtype is None else gx_dtype)
+    else:
+        _need(gx, "gx", gy.shape)
+        _same_dtype(gx, "gx", gx_dtype)
+    _check(_lib.disco_dropout_bwd(gy.data_ptr(), _dtype_code(gy), gx.data_ptr(), _dtype_code(gx), gy.numel(), p, seed,
+                                  offset, sptr, _stream()), "dropout_bwd")
+    return gx

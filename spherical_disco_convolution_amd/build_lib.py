@@ -29,6 +29,11 @@ SOURCES = [
     "training_api.cpp",
     "kernels_layer_norm.hip",
     "kernels_orthogonalize.hip",
+    "attention_api.cpp",
+    "kernels_attention.hip",
+    "kernels_attention_bwd.hip",
+    "kernels_qk_norm_rope.hip",
+    "kernels_dropout.hip",
     "spectral_host.cpp",
     "kernel_timing.cpp",
 ]

@@ -1,0 +1,298 @@
+// Device parts shared by the attention kernels, forward and backward.
+//
+// For a sequence of Lq queries and Lk keys, query head h reading key head
+// h / G (G = hq / hkv):
+//   x_ij = scale q_i . k_j + b_j        (-inf where j is left out)
+//   l_i = log sum_j exp x_ij,  p_ij = exp(x_ij - l_i),  o_i = sum_j p_ij v_j
+// The G heads of a group are rows of one tile: row r of a sequence and key head
+// is query r / G of head r % G, so their keys and values are read once, and the
+// sums over a group in the gradients of k and v need no second pass.
+//
+// Every product runs on the matrix cores as (rows from LDS) x (columns in
+// registers).  The 32 x 32 result leaves lane L with column L % 32 and rows
+// 8 (e / 4) + 4 (L / 32) + e % 4, e = 0..15: eight (bf16) or four (float32)
+// consecutive e are themselves an operand of the next product, whose other
+// operand is read with the same order of the summed rows.  So scores, weights
+// and their gradients never leave registers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "disco_internal.h"
+#include "kernels_common.h"
+
+namespace disco {
+namespace attn {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int16_t v4i16_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) int32_t lds_i32;
+typedef __attribute__((address_space(3))) floatx4 lds_f32x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) v4i16_t lds_v4i16;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+// biases below this leave a key out, as -inf does: masks made of a type's
+// lowest value, which no sum could tell from each other
+constexpr float kLowest = -1e30f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    bf16x2_t v;
+    v[0] = (__bf16)a;
+    v[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// The value of lane ^ 32 joined with this lane's
+__device__ __forceinline__ float other_half(float x, float* mine) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    *mine = __uint_as_float(r[0]);
+    return __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float half_max(float x) {
+    float a;
+    const float b = other_half(x, &a);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float half_sum(float x) {
+    float a;
+    const float b = other_half(x, &a);
+    return a + b;
+}
+
+// One operand of a product: 16 bytes a lane, KE summed elements in a wave's
+// fragment (lane L: row or column L % 32, elements (L / 32) KE/2 .. + KE/2 - 1).
+template <typename T>
+struct Op;
+
+template <>
+struct Op<bf16_t> {
+    typedef bf16x8_t Frag;
+    static constexpr int KE = 16;
+    static __device__ __forceinline__ floatx16 mma(Frag a, Frag b, floatx16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // elements e0 .. e0 + 7 of a product's result, rounded to bfloat16: the
+    // weights are at most 1 (2^8 while a maximum lags), so this costs each 2^-9
+    static __device__ __forceinline__ Frag from(const floatx16& s, int e0) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[e0 + 2 * i], s[e0 + 2 * i + 1]);
+        return __builtin_bit_cast(Frag, w);
+    }
+};
+
+template <>
+struct Op<float> {
+    typedef floatx4 Frag;
+    static constexpr int KE = 8;
+    static __device__ __forceinline__ floatx16 mma(Frag a, Frag b, floatx16 c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag from(const floatx16& s, int e0) {
+        Frag f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = s[e0 + i];
+        return f;
+    }
+};
+
+// A tile of rows in LDS: RB bytes a row, 16-byte chunks at chunk ^ turn(row).
+// The turn spreads over the banks both the 16-byte reads of 16 rows (one chunk)
+// and the transposing reads of four rows (four chunks).
+template <typename T, int DP>
+struct Tile {
+    static constexpr int EPC = 16 / (int)sizeof(T);     // elements of a chunk
+    static constexpr int USED = DP / EPC;               // chunks that products read
+    static constexpr int NCH = USED <= 4 ? 4 : USED <= 8 ? 8 : USED <= 16 ? 16 : 32;
+    static constexpr int RB = 16 * NCH;
+    static __device__ __forceinline__ int turn(int row) {
+        if constexpr (NCH == 4) return (row >> 2) & 3;
+        if constexpr (NCH == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+        if constexpr (NCH == 16) return ((row & 3) << 2) | ((row >> 2) & 3);
+        return (((row >> 2) & 1) << 3) | ((row & 3) << 1) | ((row >> 3) & 1);
+    }
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) {
+        return (uint32_t)(row * RB + ((chunk ^ turn(row)) << 4));
+    }
+    // rows row0 .. row0 + 31 as an operand, summed elements of chunks 2 c, 2 c + 1
+    static __device__ __forceinline__ typename Op<T>::Frag rows(uint32_t base, int row0, int c, int lane) {
+        const uint32_t p = base + at(row0 + (lane & 31), 2 * c + (lane >> 5));
+        return __builtin_bit_cast(typename Op<T>::Frag, *(const lds_u32x4*)(uintptr_t)p);
+    }
+    // columns 32 dt .. + 31 as an operand, summed over rows row0 .. row0 + KE - 1 in
+    // the order of a product's result
+    static __device__ __forceinline__ typename Op<T>::Frag columns(uint32_t base, int row0, int dt, int lane) {
+        const int h = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            const int s = lane & 15, g = (lane >> 4) & 1;
+            const int d = 32 * dt + 16 * g + 4 * (s & 3);
+            const uint32_t sub = (d & 7) * 2;
+            const int r = row0 + 4 * h + (s >> 2);
+            const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(base + at(r, d >> 3) + sub));
+            const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(base + at(r + 8, d >> 3) + sub));
+            return __builtin_bit_cast(typename Op<T>::Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int d = 32 * dt + (lane & 31);
+            floatx4 f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = *(const lds_f32*)(uintptr_t)(base + at(row0 + 4 * h + i, d >> 2) + (d & 3) * 4);
+            return f;
+        }
+    }
+};
+
+// 16 bytes of a row from element d0, zeros past D.  FAST: D, strides and
+// addresses are multiples of 16 bytes.
+template <typename T, bool FAST>
+__device__ __forceinline__ u32x4 load_chunk(const T* row, int d0, int D, bool valid) {
+    u32x4 w = {0, 0, 0, 0};
+    if (!valid || d0 >= D) return w;
+    if constexpr (FAST) return *reinterpret_cast<const u32x4*>(row + d0);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t v = d0 + i < D ? (uint32_t)row[d0 + i] : 0u;
+            w[i / 2] |= v << (16 * (i & 1));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = d0 + i < D ? __float_as_uint(row[d0 + i]) : 0u;
+    }
+    return w;
+}
+
+// A row that a lane keeps in registers, as an operand
+template <typename T, int DP, bool FAST>
+__device__ __forceinline__ void load_columns(typename Op<T>::Frag* f, const T* row, int D, bool valid, int lane) {
+    constexpr int EPC = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int c = 0; c < DP / Op<T>::KE; ++c)
+        f[c] = __builtin_bit_cast(typename Op<T>::Frag,
+                                  load_chunk<T, FAST>(row, (2 * c + (lane >> 5)) * EPC, D, valid));
+}
+
+// Four elements d0 .. d0 + 3 of a row, past D left alone
+template <typename T, bool FAST>
+__device__ __forceinline__ void store4(T* row, int d0, int D, const float* v) {
+    if (d0 >= D) return;
+    if constexpr (FAST) {
+        if constexpr (sizeof(T) == 2) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            *reinterpret_cast<u32x2*>(row + d0) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        } else {
+            *reinterpret_cast<floatx4*>(row + d0) = floatx4{v[0], v[1], v[2], v[3]};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d0 + i < D) store_f(row, d0 + i, v[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Which sequence, head and part a workgroup works on
+// ---------------------------------------------------------------------------
+struct Span {
+    int64_t first;   // of the packed tokens
+    int len;
+};
+
+// Boundaries out of order or out of range are cut to what the tensors hold.
+__device__ __forceinline__ Span span_of(const int32_t* cu, int s, int n_seq, int64_t total) {
+    if (cu == nullptr) {
+        const int64_t len = total / n_seq;
+        return {s * len, (int)len};
+    }
+    const int64_t a = min(max((int64_t)cu[s], (int64_t)0), total);
+    const int64_t b = min(max((int64_t)cu[s + 1], a), total);
+    return {a, (int)(b - a)};
+}
+
+// Tiles of T rows, `per` rows a token.  Without boundaries the sequences have
+// equal counts.  With them tile `slot` belongs to the last sequence s with
+// first(s) per / T + s <= slot, which leaves every sequence the tiles it needs
+// and at most one that it does not: no list has to be built beforehand.
+__host__ __device__ inline int64_t tile_slots(bool packed, int64_t total, int n_seq, int per, int T) {
+    if (!packed) return n_seq * ((total / n_seq * per + T - 1) / T);
+    return total * per / T + n_seq;
+}
+
+__device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int64_t total, int per, int T, int slot, int* seq,
+                                       int* tile, int* tiles) {
+    if (cu == nullptr) {
+        const int nt = (int)((total / n_seq * per + T - 1) / T);
+        *seq = slot / nt;
+        *tile = slot - *seq * nt;
+        *tiles = nt;
+        return *seq < n_seq;
+    }
+    auto first = [&](int s) {
+        return (int)(min(max((int64_t)cu[s], (int64_t)0), total) * per / T) + s;
+    };
+    int lo = 0, hi = n_seq;      // first(lo) <= slot < first(hi), if the boundaries are in order
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first(mid) <= slot) lo = mid;
+        else hi = mid;
+    }
+    const Span sp = span_of(cu, lo, n_seq, total);
+    *seq = lo;
+    *tile = slot - first(lo);
+    *tiles = (int)(((int64_t)sp.len * per + T - 1) / T);
+    return *tile >= 0 && *tile < *tiles;
+}
+
+// Workgroups go round the eight dies by their index; each die gets whole key
+// heads (or an even share of one), so that its L2 holds their keys and values.
+__host__ __device__ inline int64_t grid_size(int64_t per_head, int hkv) {
+    if (hkv < 8 && 8 % hkv == 0) {
+        const int share = 8 / hkv;
+        return (per_head + share - 1) / share * 8;
+    }
+    return per_head * hkv;
+}
+
+__device__ __forceinline__ bool head_of(int id, int per_head, int hkv, int* head, int* idx) {
+    if (hkv % 8 == 0) {
+        const int j = id >> 3;
+        *head = (id & 7) + 8 * (j / per_head);
+        *idx = j % per_head;
+        return true;
+    }
+    if (8 % hkv == 0) {
+        const int share = 8 / hkv, x = id & 7;
+        *head = x % hkv;
+        *idx = (id >> 3) * share + x / hkv;
+        return *idx < per_head;
+    }
+    *head = id % hkv;
+    *idx = id / hkv;
+    return true;
+}
+
+// Row r of a sequence's tile rows: token r / G, head r % G
+__device__ __forceinline__ void row_of(int r, int G, int* token, int* head) {
+    *token = G == 1 ? r : r / G;
+    *head = r - *token * G;
+}
+
+__device__ __forceinline__ float bias2(float b) {   // in units of log 2
+    return b < kLowest ? -kInf : b * kLog2e;
+}
+
+}  // namespace attn
+}  // namespace disco

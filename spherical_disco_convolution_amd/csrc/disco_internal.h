@@ -231,6 +231,72 @@ struct OrthoCall {
 size_t orthogonalize_workspace(int batch, int rows, int cols);
 int launch_orthogonalize(const OrthoCall& c, void* stream);
 
+// Attention (kernels_attention.hip, kernels_attention_bwd.hip).  Strides are in
+// elements, ts from token to token and hs from head to head.
+struct AttnArgs {
+    int dtype;
+    const void *q, *k, *v, *o, *go;
+    void *out, *gq, *gk, *gv;
+    float* lse;                  // written by the forward, or NULL
+    const float* lse_in;
+    const float* bias;           // of a key, or NULL
+    const int32_t *cu_q, *cu_k;  // boundaries in device memory, or NULL: equal counts
+    float* delta;                // [total_q, hq], workspace
+    float *part, *part2, *part_lse;   // results of each split, workspace
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, go_ts, go_hs, gq_ts, gq_hs, gk_ts, gk_hs, gv_ts, gv_hs;
+    int64_t total_q, total_k;
+    int n_seq, hq, hkv, G, dk, dv, causal;
+    float scale;
+    int slots, splits;           // of one launch
+};
+// How a call is cut up: by its sizes, types and alignment alone.
+struct AttnPlan {
+    int waves;        // of a workgroup, 32 rows (or keys) each
+    int splits;       // parts of the axis that a workgroup walks over
+    bool fast;        // 16-byte accesses
+};
+AttnPlan attn_plan_fwd(const AttnArgs& a);
+AttnPlan attn_plan_bwd_q(const AttnArgs& a);
+AttnPlan attn_plan_bwd_kv(const AttnArgs& a);
+int attn_launched(const char* what);
+int launch_attention_fwd(const AttnArgs& a, void* stream);
+int launch_attention_bwd(const AttnArgs& a, void* stream);
+
+// Norm and rotation of queries and keys (kernels_qk_norm_rope.hip)
+struct QkCall {
+    int dtype, backward;
+    const void *q, *k, *gq, *gk;
+    void *q_out, *k_out;         // results, or the gradients of q and k
+    const float *q_weight, *k_weight;
+    const void* positions;
+    int pos_is_int, axes;
+    const float* inv_freq;
+    int rot, interleaved;
+    float eps;
+    int64_t q_ts, q_hs, k_ts, k_hs, gq_ts, gq_hs, gk_ts, gk_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    int64_t tokens;
+    int hq, hkv, d;
+    float* partial;              // workspace of the weights' gradients, or NULL
+    float *gq_weight, *gk_weight;
+    int head_parts, heads_each;  // of one launch
+};
+size_t qk_norm_rope_bwd_workspace(int d);
+int launch_qk_norm_rope(const QkCall& c, void* stream);
+
+// Dropout (kernels_dropout.hip)
+struct DropoutCall {
+    const void* x;
+    int x_dtype;
+    const void* residual;        // of x_dtype, or NULL
+    void* y;
+    int y_dtype;
+    int64_t n;
+    uint32_t threshold;          // of 65536
+    uint64_t seed, offset;
+    const int64_t* step;         // device memory, added to offset, or NULL
+};
+int launch_dropout(const DropoutCall& c, void* stream);
+
 // Scope around one kernel launch: while disco_kernel_timing(1) is in effect,
 // records a HIP event on the launch stream at construction and at
 // destruction, for disco_kernel_timing_read.  The name must be a string

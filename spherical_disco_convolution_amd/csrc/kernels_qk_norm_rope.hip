@@ -1,0 +1,362 @@
+// Root-mean-square norm of each head of queries and keys, and the rotation of
+// its pairs by the token's position, in one pass; and its gradient.
+//
+//   r = 1/sqrt(1/D sum_d x_d^2 + eps),  n_d = x_d r w_d
+//   (y_a, y_b) = (n_a cos f - n_b sin f, n_a sin f + n_b cos f),  f = position * frequency
+// and, with gn = gy turned back and t = gn w,
+//   gx = r (t - x r^2 1/D sum_d t_d x_d),   gw_d = sum over tokens and heads of gn_d x_d r.
+//
+// HBM bounds both: each element is read and written once.  A group of lanes
+// takes a token and walks over its heads, so that an angle is taken once for all
+// heads (in float64: a float32 product has lost the angle of position 10^6).  A
+// lane holds V pairs of a head in registers, between the sum and the output.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "disco_internal.h"
+#include "kernels_common.h"
+
+namespace disco {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 1024;    // workgroups of the gradient, and rows of partial sums
+
+// V consecutive elements, at any element alignment (gfx950 global memory takes
+// wide accesses at any)
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float* f) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[V]; };
+    const U u = *reinterpret_cast<const U*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = load_f(u.e, i);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float* f) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[V]; };
+    U u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store_f(u.e, i, f[i]);
+    *reinterpret_cast<U*>(p) = u;
+}
+
+// Where a lane's V pairs of slot p lie: elements a .. a + V - 1 and b .. b + V - 1.
+// Pairs of the half layout are (i, i + R/2); side by side they are 2 V elements
+// in a row, as are the elements behind the R that turn.
+struct Place {
+    int a, b;
+    bool turns, has_a, has_b;
+};
+template <int V, bool INTER>
+__device__ __forceinline__ Place place(int p, int D, int R) {
+    Place s;
+    const int i = p * V;
+    s.turns = i < R / 2;
+    if (s.turns && !INTER) {
+        s.a = i;
+        s.b = i + R / 2;
+    } else {
+        s.a = s.turns ? 2 * i : R + 2 * (i - R / 2);
+        s.b = s.a + V;
+    }
+    s.has_a = s.a < D;
+    s.has_b = s.b < D;
+    return s;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_pairs(const T* row, const Place& s, float* f) {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) f[i] = 0.0f;
+    if (s.has_a) load_v<T, V>(row + s.a, f);
+    if (s.has_b) load_v<T, V>(row + s.b, f + V);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* row, const Place& s, const float* f) {
+    if (s.has_a) store_v<T, V>(row + s.a, f);
+    if (s.has_b) store_v<T, V>(row + s.b, f + V);
+}
+
+template <int V, bool INTER>
+__device__ __forceinline__ void turn(float* f, const float* cs, const float* sn) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float& x = f[INTER ? 2 * i : i];
+        float& y = f[INTER ? 2 * i + 1 : V + i];
+        const float a = x, b = y;
+        x = a * cs[i] - b * sn[i];
+        y = a * sn[i] + b * cs[i];
+    }
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+template <int V>
+__device__ __forceinline__ void angles(const QkCall& c, int64_t tok, int p, bool turns, float sign, float* cs, float* sn) {
+    const int pairs = c.rot / 2;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        cs[i] = 1.0f;
+        sn[i] = 0.0f;
+        if (!turns) continue;
+        const int k = p * V + i;
+        const int64_t at = tok * c.axes + (int64_t)k * c.axes / pairs;
+        const double pos = c.pos_is_int ? (double)((const int32_t*)c.positions)[at] : (double)((const float*)c.positions)[at];
+        const double rev = pos * (double)c.inv_freq[k] * 0.15915494309189533577;   // turns
+        float s, q;
+        sincospif(2.0f * (float)(rev - rint(rev)), &s, &q);
+        cs[i] = q;
+        sn[i] = sign * s;
+    }
+}
+
+// V pairs a lane and slot, L lanes a token, N slots a lane
+template <typename T, int V, int L, int N, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_fwd(QkCall c) {
+    const int lane = threadIdx.x % L;
+    const int64_t tok = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    if (tok >= c.tokens) return;
+    const int heads = c.hq + c.hkv;
+    const int h0 = blockIdx.y * c.heads_each, h1 = min(h0 + c.heads_each, heads);
+    Place s[N];
+    float cs[N][V], sn[N][V], wq[N][2 * V], wk[N][2 * V];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int p = lane + n * L;
+        s[n] = place<V, INTER>(p, c.d, c.rot);
+        angles<V>(c, tok, p, s[n].turns, 1.0f, cs[n], sn[n]);
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) wq[n][i] = wk[n][i] = 1.0f;
+        if (c.q_weight) load_pairs<float, V>(c.q_weight, s[n], wq[n]);
+        if (c.k_weight) load_pairs<float, V>(c.k_weight, s[n], wk[n]);
+    }
+    const float inv_d = 1.0f / (float)c.d;
+    for (int hd = h0; hd < h1; ++hd) {
+        const bool isq = hd < c.hq;
+        const int64_t hh = isq ? hd : hd - c.hq;
+        const T* x = isq ? (const T*)c.q + tok * c.q_ts + hh * c.q_hs : (const T*)c.k + tok * c.k_ts + hh * c.k_hs;
+        T* y = isq ? (T*)c.q_out + tok * c.qo_ts + hh * c.qo_hs : (T*)c.k_out + tok * c.ko_ts + hh * c.ko_hs;
+        float f[N][2 * V], sq = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            load_pairs<T, V>(x, s[n], f[n]);
+#pragma unroll
+            for (int i = 0; i < 2 * V; ++i) sq = fmaf(f[n][i], f[n][i], sq);
+        }
+        const float r = 1.0f / sqrtf(group_sum<L>(sq) * inv_d + c.eps);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+            for (int i = 0; i < 2 * V; ++i) f[n][i] *= r * (isq ? wq[n][i] : wk[n][i]);
+            if (s[n].turns) turn<V, INTER>(f[n], cs[n], sn[n]);
+            store_pairs<T, V>(y, s[n], f[n]);
+        }
+    }
+}
+
+template <typename T, int V, int L, int N, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_bwd(QkCall c) {
+    constexpr int TOK = kThreads / L;
+    const int lane = threadIdx.x % L;
+    const int heads = c.hq + c.hkv;
+    Place s[N];
+    float wq[N][2 * V], wk[N][2 * V], gwq[N][2 * V], gwk[N][2 * V];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        s[n] = place<V, INTER>(lane + n * L, c.d, c.rot);
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+            wq[n][i] = wk[n][i] = 1.0f;
+            gwq[n][i] = gwk[n][i] = 0.0f;
+        }
+        if (c.q_weight) load_pairs<float, V>(c.q_weight, s[n], wq[n]);
+        if (c.k_weight) load_pairs<float, V>(c.k_weight, s[n], wk[n]);
+    }
+    const float inv_d = 1.0f / (float)c.d;
+    // a unit is a token and a share of its heads
+    const int64_t units = c.tokens * c.head_parts;
+    for (int64_t u0 = (int64_t)blockIdx.x * TOK; u0 < units; u0 += (int64_t)gridDim.x * TOK) {
+        const int64_t u = u0 + threadIdx.x / L;
+        if (u >= units) continue;
+        const int64_t tok = c.head_parts == 1 ? u : u / c.head_parts;
+        const int h0 = (int)(u - tok * c.head_parts) * c.heads_each, h1 = min(h0 + c.heads_each, heads);
+        float cs[N][V], sn[N][V];
+#pragma unroll
+        for (int n = 0; n < N; ++n) angles<V>(c, tok, lane + n * L, s[n].turns, -1.0f, cs[n], sn[n]);
+        for (int hd = h0; hd < h1; ++hd) {
+            const bool isq = hd < c.hq;
+            const int64_t hh = isq ? hd : hd - c.hq;
+            const T* x = isq ? (const T*)c.q + tok * c.q_ts + hh * c.q_hs : (const T*)c.k + tok * c.k_ts + hh * c.k_hs;
+            const T* g = isq ? (const T*)c.gq + tok * c.gq_ts + hh * c.gq_hs : (const T*)c.gk + tok * c.gk_ts + hh * c.gk_hs;
+            T* y = isq ? (T*)c.q_out : (T*)c.k_out;
+            float f[N][2 * V], t[N][2 * V], sq = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                load_pairs<T, V>(x, s[n], f[n]);
+                load_pairs<T, V>(g, s[n], t[n]);
+                if (s[n].turns) turn<V, INTER>(t[n], cs[n], sn[n]);
+#pragma unroll
+                for (int i = 0; i < 2 * V; ++i) {
+                    sq = fmaf(f[n][i], f[n][i], sq);
+                    dot = fmaf(f[n][i], t[n][i] * (isq ? wq[n][i] : wk[n][i]), dot);
+                }
+            }
+            sq = group_sum<L>(sq);
+            dot = group_sum<L>(dot);
+            const float r = 1.0f / sqrtf(sq * inv_d + c.eps);
+            const float back = r * r * inv_d * dot;
+            y += isq ? tok * c.qo_ts + hh * c.qo_hs : tok * c.ko_ts + hh * c.ko_hs;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                float o[2 * V];
+#pragma unroll
+                for (int i = 0; i < 2 * V; ++i) {
+                    const float gn = t[n][i];
+                    o[i] = r * (gn * (isq ? wq[n][i] : wk[n][i]) - f[n][i] * back);
+                    const float gw = gn * f[n][i] * r;
+                    gwq[n][i] += isq ? gw : 0.0f;
+                    gwk[n][i] += isq ? 0.0f : gw;
+                }
+                store_pairs<T, V>(y, s[n], o);
+            }
+        }
+    }
+    if (!c.partial) return;
+    // sums of the workgroup's units: lanes of the same place meet in LDS
+    __shared__ float red[kThreads / 64][2][2 * V * N * L];
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+            float q = gwq[n][i], k = gwk[n][i];
+#pragma unroll
+            for (int d = L; d < 64; d *= 2) {
+                q += __shfl_xor(q, d, 64);
+                k += __shfl_xor(k, d, 64);
+            }
+            if ((threadIdx.x & 63) < L) {
+                const int at = (n * L + lane) * 2 * V + i;
+                red[wave][0][at] = q;
+                red[wave][1][at] = k;
+            }
+        }
+    __syncthreads();
+    if (threadIdx.x >= L) return;
+    float* row = c.partial + (int64_t)blockIdx.x * 2 * c.d;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+            const int d = i < V ? s[n].a + i : s[n].b + i - V;
+            if (!(i < V ? s[n].has_a : s[n].has_b)) continue;
+            float q = 0.0f, k = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kThreads / 64; ++w) {
+                q += red[w][0][(n * L + lane) * 2 * V + i];
+                k += red[w][1][(n * L + lane) * 2 * V + i];
+            }
+            row[d] = q;
+            row[c.d + d] = k;
+        }
+}
+
+// Column sums of the partial rows [rows][2 d]: sixteen columns and sixteen
+// shares of the rows a workgroup, in a fixed order
+__global__ __launch_bounds__(256) void qk_reduce(const float* __restrict__ partial, float* gqw, float* gkw, int rows, int d) {
+    __shared__ float red[16][17];
+    const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+    float v = 0.0f;
+    if (col < 2 * d)
+        for (int r = part; r < rows; r += 16) v += partial[(int64_t)r * 2 * d + col];
+    red[part][threadIdx.x & 15] = v;
+    __syncthreads();
+    if (part != 0 || col >= 2 * d) return;
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += red[i][threadIdx.x];
+    float* out = col < d ? gqw : gkw;
+    if (out) out[col < d ? col : col - d] = v;
+}
+
+int bwd_blocks(int64_t units, int L) {
+    return (int)std::min<int64_t>((units * L + kThreads - 1) / kThreads, kMaxBlocks);
+}
+
+// pairs a lane holds: four where whole vectors fall on one side of every border
+int pairs_a_lane(int d, int rot) { return rot % 8 == 0 && d % 8 == 0 ? 4 : 1; }
+
+// Shares of a token's heads: all in one where the tokens alone fill the chip.
+// 33024 tokens of 16 heads go in one share each; 8 tokens of 18 heads in 18.
+int head_parts(int64_t tokens, int heads, int L) {
+    const int64_t waves = (tokens * L + 63) / 64;
+    if (waves >= 2048) return 1;
+    return (int)std::min<int64_t>(heads, 2048 / std::max<int64_t>(waves, 1));
+}
+
+int lanes_of(int d, int V) {
+    const int slots = ((d + 1) / 2 + V - 1) / V;
+    int L = 4;
+    while (L < slots && L < 64) L *= 2;
+    return L;
+}
+
+template <typename T, int V, int L, int N>
+int go(QkCall c, hipStream_t st) {
+    const int heads = c.hq + c.hkv;
+    c.head_parts = head_parts(c.tokens, heads, L);
+    c.heads_each = (heads + c.head_parts - 1) / c.head_parts;
+    c.head_parts = (heads + c.heads_each - 1) / c.heads_each;
+    if (!c.backward) {
+        KernelTimer timer("qk_fwd", st);
+        const dim3 grid((unsigned)((c.tokens + kThreads / L - 1) / (kThreads / L)), (unsigned)c.head_parts);
+        if (c.interleaved) qk_fwd<T, V, L, N, true><<<grid, kThreads, 0, st>>>(c);
+        else qk_fwd<T, V, L, N, false><<<grid, kThreads, 0, st>>>(c);
+    } else {
+        const int blocks = bwd_blocks(c.tokens * c.head_parts, L);
+        {
+            KernelTimer timer("qk_bwd", st);
+            if (c.interleaved) qk_bwd<T, V, L, N, true><<<blocks, kThreads, 0, st>>>(c);
+            else qk_bwd<T, V, L, N, false><<<blocks, kThreads, 0, st>>>(c);
+        }
+        if (c.partial) {
+            KernelTimer timer("qk_reduce", st);
+            qk_reduce<<<(2 * c.d + 15) / 16, 256, 0, st>>>(c.partial, c.gq_weight, c.gk_weight, blocks, c.d);
+        }
+    }
+    const hipError_t e = hipGetLastError();
+    if (e == hipSuccess) return DISCO_OK;
+    return set_error(DISCO_EHIP, "qk_norm_rope: launch failed: %s", hipGetErrorString(e));
+}
+
+template <typename T>
+int typed(const QkCall& c, hipStream_t st) {
+    if (pairs_a_lane(c.d, c.rot) == 4) {
+        switch (lanes_of(c.d, 4)) {
+            case 4: return go<T, 4, 4, 1>(c, st);
+            case 8: return go<T, 4, 8, 1>(c, st);
+            case 16: return go<T, 4, 16, 1>(c, st);
+            default: return go<T, 4, 32, 1>(c, st);
+        }
+    }
+    if (lanes_of(c.d, 1) <= 16) return go<T, 1, 16, 1>(c, st);
+    return go<T, 1, 64, 2>(c, st);
+}
+
+}  // namespace
+
+size_t qk_norm_rope_bwd_workspace(int d) { return (size_t)kMaxBlocks * 2 * d * sizeof(float); }
+
+int launch_qk_norm_rope(const QkCall& c, void* stream) {
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return c.dtype == DISCO_F32 ? typed<float>(c, st) : typed<bf16_t>(c, st);
+}
+
+}  // namespace disco
