@@ -15,6 +15,7 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// 16-byte accesses, and rows near enough for the 32-bit offsets of a tile's copies
 bool wide(const AttnArgs& a) {
     const int epc = a.dtype == DISCO_F32 ? 4 : 8;
     if (a.dk % epc || a.dv % epc) return false;
@@ -24,6 +25,9 @@ bool wide(const AttnArgs& a) {
     for (const void* p : {a.q, a.k, a.v, a.o, a.go, (const void*)a.out, (const void*)a.gq, (const void*)a.gk,
                           (const void*)a.gv})
         if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+    const int64_t size = 16 / epc, reach = ((int64_t)1 << 31) / (64 * size);
+    for (int64_t s : {a.k_ts, a.v_ts})
+        if (s >= reach) return false;
     return true;
 }
 

@@ -204,6 +204,65 @@ __device__ __forceinline__ void store4(T* row, int d0, int D, const float* v) {
 }
 
 // ---------------------------------------------------------------------------
+// Tiles from global memory straight into LDS
+// ---------------------------------------------------------------------------
+constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer: the copy writes zeros
+
+// 16 bytes a lane from base + off (zeros for kNowhere) to LDS at + 16 lane; no
+// registers are written, and completion counts as a vector memory operation.
+// off reaches 2^31 bytes: the caller checks that a tile's rows lie that near.
+__device__ __forceinline__ void copy16(u32x4 buffer, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(off), "s"(buffer), "s"(at)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ u32x4 buffer_of(const void* p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    u32x4 b;
+    b[0] = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    b[1] = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    b[2] = 0x7fffffffu;   // bytes
+    b[3] = 0x00027000u;   // raw, 32-bit elements
+    return b;
+}
+
+// All of the workgroup's copies, reads and writes so far are done
+__device__ __forceinline__ void all_arrived() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A tile of R rows, NW waves: instruction j of a wave moves 1 KiB of it
+template <typename T, int DP, int R, int NW>
+struct Copy {
+    typedef Tile<T, DP> L;
+    static constexpr int N = R * L::RB / 1024 / NW;
+    static_assert(N >= 1 && R * L::RB == N * 1024 * NW, "whole instructions");
+    uint32_t off[N];     // from the tile's first row
+    int row[N];
+    // rows ts elements apart, d elements long
+    __device__ __forceinline__ void init(int64_t ts, int d, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = (j * NW + wave) * 64 + lane, c = id % L::NCH;
+            row[j] = id / L::NCH;
+            const int src = (c ^ L::turn(row[j])) * L::EPC;
+            off[j] = src < d ? (uint32_t)((row[j] * ts + src) * (int64_t)sizeof(T)) : kNowhere;
+        }
+    }
+    // rows whose bit in `out` is set, and those from `rows` on, become zeros
+    __device__ __forceinline__ void start(const T* first, uint32_t at, int rows, uint64_t out, int wave) const {
+        const u32x4 b = buffer_of(first);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const bool ok = row[j] < rows && !((out >> row[j]) & 1);
+            copy16(b, ok ? off[j] : kNowhere, at + (uint32_t)(j * NW + wave) * 1024u);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
 // Which sequence, head and part a workgroup works on
 // ---------------------------------------------------------------------------
 struct Span {
