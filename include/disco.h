@@ -397,7 +397,7 @@ typedef struct disco_attention_desc {
     int32_t dk, dv;                 /* sizes of a head of q and k, of v and o: 1..128 */
     int32_t dtype;                  /* of every tensor but lse and key_bias */
     int32_t causal;
-    float   scale;                  /* finite, > 0 */
+    float   scale;                  /* 1e-6 .. 1e6 */
     /* strides in elements, token to token and head to head (a head's elements
      * lie together); those of results may be columns of one buffer */
     int64_t q_stride[2], k_stride[2], v_stride[2], o_stride[2];

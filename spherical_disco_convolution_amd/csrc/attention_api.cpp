@@ -157,8 +157,9 @@ int check_desc(const disco_attention_desc* d, AttnArgs* a) {
     if (d->dk < 1 || d->dv < 1) return set_error(DISCO_EINVAL, "head sizes must be >= 1 (got %d, %d)", d->dk, d->dv);
     if (d->dk > 128 || d->dv > 128)
         return set_error(DISCO_EUNSUPPORTED, "head sizes of at most 128 (got %d, %d)", d->dk, d->dv);
-    if (!std::isfinite(d->scale) || !(d->scale > 0.0f))
-        return set_error(DISCO_EINVAL, "scale must be finite and > 0 (got %g)", (double)d->scale);
+    // a bias is taken in units of the raw score
+    if (!(d->scale >= 1e-6f && d->scale <= 1e6f))
+        return set_error(DISCO_EINVAL, "scale must lie in [1e-6, 1e6] (got %g)", (double)d->scale);
     // rows of a tile are counted in 32 bits, tiles of a launch too
     constexpr int64_t kMost = INT32_MAX - 4096;
     if (d->total_k > kMost || d->total_q > kMost || d->total_q * d->hq > kMost || d->total_k * d->hkv > kMost)
@@ -178,6 +179,8 @@ int check_desc(const disco_attention_desc* d, AttnArgs* a) {
     // every sequence costs a tile for each key head and split
     if ((int64_t)d->n_seq * d->hkv * 128 > kMost)
         return set_error(DISCO_EUNSUPPORTED, "too many sequences in one call (%d of %d key heads)", d->n_seq, d->hkv);
+    a->each_q = (int)(d->total_q / d->n_seq);
+    a->each_k = (int)(d->total_k / d->n_seq);
     a->q_ts = d->q_stride[0], a->q_hs = d->q_stride[1];
     a->k_ts = d->k_stride[0], a->k_hs = d->k_stride[1];
     a->v_ts = d->v_stride[0], a->v_hs = d->v_stride[1];

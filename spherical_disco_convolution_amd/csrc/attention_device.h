@@ -155,6 +155,48 @@ struct Tile {
     }
 };
 
+// Where a lane reads the operands of a tile whose place in LDS is known when
+// compiled: addresses are taken once, what changes goes into the instructions.
+template <typename T, int DP>
+struct Reader {
+    typedef Tile<T, DP> L;
+    typedef typename Op<T>::Frag Frag;
+    static constexpr int KE = Op<T>::KE, NT = DP / 32;
+    uint32_t base, row[DP / KE], col[NT][2];
+    int lane;
+    __device__ __forceinline__ void init(uint32_t b, int ln) {
+        base = b;
+        lane = ln;
+#pragma unroll
+        for (int c = 0; c < DP / KE; ++c) row[c] = b + L::at(ln & 31, 2 * c + (ln >> 5));
+        if constexpr (sizeof(T) == 2) {
+            const int s = ln & 15, r = 4 * (ln >> 5) + (s >> 2);
+#pragma unroll
+            for (int d = 0; d < NT; ++d)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = 32 * d + 16 * ((ln >> 4) & 1) + 4 * (s & 3);
+                    col[d][j] = b + L::at(r + 8 * j, e >> 3) + (e & 7) * 2;
+                }
+        }
+    }
+    // the tile `off` bytes from base; rows 32 k .. + 31, chunks 2 c and 2 c + 1
+    __device__ __forceinline__ Frag rows(uint32_t off, int k, int c) const {
+        return __builtin_bit_cast(Frag, *(const lds_u32x4*)(uintptr_t)(row[c] + (off + k * 32 * L::RB)));
+    }
+    // columns 32 d .. + 31, summed over rows KE b .. in a result's order
+    __device__ __forceinline__ Frag columns(uint32_t off, int b, int d) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t o = off + b * KE * L::RB;
+            const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][0] + o));
+            const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][1] + o));
+            return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return L::columns(base + off, b * KE, d, lane);
+        }
+    }
+};
+
 // 16 bytes of a row from element d0, zeros past D.  FAST: D, strides and
 // addresses are multiples of 16 bytes.
 template <typename T, bool FAST>
@@ -214,7 +256,7 @@ constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer: the copy writ
 __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t off, uint32_t at) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
-                 : "v"(off), "s"(buffer), "s"(at)
+                 : "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(at))
                  : "memory", "m0");
 }
 
@@ -233,34 +275,46 @@ __device__ __forceinline__ void all_arrived() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// A tile of R rows, NW waves: instruction j of a wave moves 1 KiB of it
-template <typename T, int DP, int R, int NW>
+// A tile of 64 rows, NW waves: instruction j of a wave moves 1 KiB of it, and
+// its rows lie 64 / N further on than those of instruction j - 1
+template <typename T, int DP, int NW>
 struct Copy {
     typedef Tile<T, DP> L;
-    static constexpr int N = R * L::RB / 1024 / NW;
-    static_assert(N >= 1 && R * L::RB == N * 1024 * NW, "whole instructions");
-    uint32_t off[N];     // from the tile's first row
-    int row[N];
-    // rows ts elements apart, d elements long
-    __device__ __forceinline__ void init(int64_t ts, int d, int wave, int lane) {
+    static constexpr int N = 64 * L::RB / 1024 / NW;
+    static_assert(N >= 1 && 64 * L::RB == N * 1024 * NW, "whole instructions");
+    int row;             // of instruction 0
+    __device__ __forceinline__ void init(int wave, int lane) { row = (wave * 64 + lane) / L::NCH; }
+    // offsets of rows ts elements apart, d elements long
+    __device__ __forceinline__ void offsets(uint32_t* off, int64_t ts, int d, int lane) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int id = (j * NW + wave) * 64 + lane, c = id % L::NCH;
-            row[j] = id / L::NCH;
-            const int src = (c ^ L::turn(row[j])) * L::EPC;
-            off[j] = src < d ? (uint32_t)((row[j] * ts + src) * (int64_t)sizeof(T)) : kNowhere;
+            const int r = row + j * (64 / N), src = ((lane % L::NCH) ^ L::turn(r)) * L::EPC;
+            off[j] = src < d ? (uint32_t)((r * ts + src) * (int64_t)sizeof(T)) : kNowhere;
         }
     }
-    // rows whose bit in `out` is set, and those from `rows` on, become zeros
-    __device__ __forceinline__ void start(const T* first, uint32_t at, int rows, uint64_t out, int wave) const {
-        const u32x4 b = buffer_of(first);
+    // two tiles of the same rows; a row whose bit in `out` is set becomes zeros
+    __device__ __forceinline__ void start(const T* p, const uint32_t* po, uint32_t pat, const T* q, const uint32_t* qo,
+                                          uint32_t qat, uint64_t out, int wave) const {
+        const u32x4 pb = buffer_of(p), qb = buffer_of(q);
+        if (out == 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                copy16(pb, po[j], pat + (uint32_t)(j * NW + wave) * 1024u);
+                copy16(qb, qo[j], qat + (uint32_t)(j * NW + wave) * 1024u);
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const bool ok = row[j] < rows && !((out >> row[j]) & 1);
-            copy16(b, ok ? off[j] : kNowhere, at + (uint32_t)(j * NW + wave) * 1024u);
+            const bool ok = !((out >> (j * (64 / N))) >> row & 1);
+            copy16(pb, ok ? po[j] : kNowhere, pat + (uint32_t)(j * NW + wave) * 1024u);
+            copy16(qb, ok ? qo[j] : kNowhere, qat + (uint32_t)(j * NW + wave) * 1024u);
         }
     }
 };
+
+// bits n .. 63
+__device__ __forceinline__ uint64_t from_bit(int n) { return n >= 64 ? 0 : ~(uint64_t)0 << max(n, 0); }
 
 // ---------------------------------------------------------------------------
 // Which sequence, head and part a workgroup works on
@@ -271,47 +325,43 @@ struct Span {
 };
 
 // Boundaries out of order or out of range are cut to what the tensors hold.
-__device__ __forceinline__ Span span_of(const int32_t* cu, int s, int n_seq, int64_t total) {
-    if (cu == nullptr) {
-        const int64_t len = total / n_seq;
-        return {s * len, (int)len};
-    }
-    const int64_t a = min(max((int64_t)cu[s], (int64_t)0), total);
-    const int64_t b = min(max((int64_t)cu[s + 1], a), total);
-    return {a, (int)(b - a)};
+// Without boundaries every sequence has `each` tokens.
+__device__ __forceinline__ Span span_of(const int32_t* cu, int s, int each, int total) {
+    if (cu == nullptr) return {(int64_t)s * each, each};
+    const int a = min(max(uniform(cu[s]), 0), total), b = min(max(uniform(cu[s + 1]), a), total);
+    return {a, b - a};
 }
 
-// Tiles of T rows, `per` rows a token.  Without boundaries the sequences have
-// equal counts.  With them tile `slot` belongs to the last sequence s with
-// first(s) per / T + s <= slot, which leaves every sequence the tiles it needs
-// and at most one that it does not: no list has to be built beforehand.
-__host__ __device__ inline int64_t tile_slots(bool packed, int64_t total, int n_seq, int per, int T) {
+// Tiles of T rows (a power of two), `per` rows a token.  Without boundaries the
+// sequences have equal counts.  With them tile `slot` belongs to the last
+// sequence s with first(s) per / T + s <= slot, which leaves every sequence the
+// tiles it needs and at most one that it does not: no list has to be built
+// beforehand.  Tokens times heads stay below 2^31 - 4096.
+inline int64_t tile_slots(bool packed, int64_t total, int n_seq, int per, int T) {
     if (!packed) return n_seq * ((total / n_seq * per + T - 1) / T);
     return total * per / T + n_seq;
 }
 
-__device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int64_t total, int per, int T, int slot, int* seq,
+__device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int total, int each, int per, int T, int slot, int* seq,
                                        int* tile, int* tiles) {
     if (cu == nullptr) {
-        const int nt = (int)((total / n_seq * per + T - 1) / T);
-        *seq = slot / nt;
+        const int nt = (each * per + T - 1) / T;
+        *seq = n_seq == 1 ? 0 : slot / nt;
         *tile = slot - *seq * nt;
         *tiles = nt;
         return *seq < n_seq;
     }
-    auto first = [&](int s) {
-        return (int)(min(max((int64_t)cu[s], (int64_t)0), total) * per / T) + s;
-    };
+    auto first = [&](int s) { return min(max(uniform(cu[s]), 0), total) * per / T + s; };
     int lo = 0, hi = n_seq;      // first(lo) <= slot < first(hi), if the boundaries are in order
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (first(mid) <= slot) lo = mid;
         else hi = mid;
     }
-    const Span sp = span_of(cu, lo, n_seq, total);
+    const Span sp = span_of(cu, lo, 0, total);
     *seq = lo;
     *tile = slot - first(lo);
-    *tiles = (int)(((int64_t)sp.len * per + T - 1) / T);
+    *tiles = (sp.len * per + T - 1) / T;
     return *tile >= 0 && *tile < *tiles;
 }
 

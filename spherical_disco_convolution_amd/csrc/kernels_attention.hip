@@ -2,6 +2,7 @@
 #include "attention_device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace disco {
 
@@ -10,41 +11,50 @@ using namespace attn;
 namespace {
 
 constexpr int kKeys = 64;   // keys of a tile
-// A maximum may lag by 2^8: weights then reach 2^8, which bfloat16 holds as well as 1.
-constexpr float kLag = 8.0f;
+// The running maximum may lag: weights of 2^60 keep as many digits as weights of
+// 1, in bfloat16 too.  So a tile's maximum is taken only where the sum of its
+// weights passes this bound, or where the row has seen no key yet.
+constexpr float kMostSum = 1.152921504606846976e18f;
 
-// A workgroup of NW waves has 32 NC rows a wave and walks over the keys of its
-// part in tiles of 64: one pass with the running maximum and sum.
-template <typename T, int DP, int NW, int NC, bool BIAS, bool FAST>
-__global__ __launch_bounds__(64 * NW, (NC == 1 && NW < 8) ? 2 : 1) void attn_fwd(AttnArgs a) {
+// A workgroup of NW waves has 32 rows a wave and walks over the keys of its part
+// in tiles of 64: one pass with a reference close to the running maximum, and
+// the running sum.
+template <typename T, int DP, int NW, bool BIAS, bool FAST>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1) void attn_fwd(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
-    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NC * NW, KB = 32 / KE, TB = kKeys * L::RB;
+    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, TB = kKeys * L::RB;
     constexpr int STAGES = FAST ? 2 : 1;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * 2 * TB];
-    __shared__ __attribute__((aligned(16))) float bias_s[2][kKeys];
+    __shared__ __attribute__((aligned(16))) float bias_s[STAGES][kKeys];
     const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
-    const uint32_t bias_base = (uint32_t)(uintptr_t)(lds_f32*)&bias_s[0][0];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
-    const int split = idx % a.splits;
-    if (!locate(a.cu_q, a.n_seq, a.total_q, a.G, TR, idx / a.splits, &seq, &tile, &tiles)) return;
+    const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
+    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, &seq, &tile, &tiles)) return;
     if (a.causal) tile = tiles - 1 - tile;   // the longest rows first
-    const Span sq = span_of(a.cu_q, seq, a.n_seq, a.total_q);
-    const Span sk = span_of(a.cu_k, seq, a.n_seq, a.total_k);
+    const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
+    const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
     // keys that the tile's first and last row see
-    int t_first, t_last, unused;
-    row_of(tile * TR, a.G, &t_first, &unused);
-    row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
-    const int most = uniform(a.causal ? min(max(t_last + ahead + 1, 0), lk) : lk);
-    const int least = uniform(a.causal ? min(max(t_first + ahead + 1, 0), lk) : lk);
+    int most = lk, least = lk;
+    if (a.causal) {
+        int t_first, t_last, unused;
+        row_of(tile * TR, a.G, &t_first, &unused);
+        row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
+        most = uniform(min(max(t_last + ahead + 1, 0), lk));
+        least = uniform(min(max(t_first + ahead + 1, 0), lk));
+    }
     // this part's tiles of keys
     const int all = (most + kKeys - 1) / kKeys;
-    const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+    int t0 = 0, t1 = all;
+    if (a.splits > 1) {
+        t0 = (int)((int64_t)all * split / a.splits);
+        t1 = (int)((int64_t)all * (split + 1) / a.splits);
+    }
 
     const T* K = (const T*)a.k + sk.first * a.k_ts + (int64_t)hk * a.k_hs;
     const T* V = (const T*)a.v + sk.first * a.v_ts + (int64_t)hk * a.v_hs;
@@ -58,197 +68,184 @@ __global__ __launch_bounds__(64 * NW, (NC == 1 && NW < 8) ? 2 : 1) void attn_fwd
         const float b = key < lk ? B[key] : -kInf;
         return b < kLowest ? -kInf : b * per_scale;
     };
-    Copy<T, DP, kKeys, FAST ? NW : 1> ck, cv;
+    typedef Copy<T, DP, FAST ? NW : 1> C;
+    C copy;
+    uint32_t koff[C::N], voff[C::N];
     float bias = 0.0f;
-    auto start = [&](int t) {   // the copies of tile t; `bias` is tile t's
-        const uint32_t at = base + (uint32_t)(t & 1) * (2 * TB);
-        uint64_t out = 0;
-        if constexpr (BIAS) {
-            out = __ballot(bias == -kInf);
-            if (wave == 0) bias_s[t & 1][lane] = bias;
-        }
+    auto start = [&](int t, int stage) {   // the copies of tile t; `bias` is tile t's
+        const uint32_t at = base + (uint32_t)stage * (2 * TB);
         const int64_t k0 = (int64_t)t * kKeys;
-        ck.start(K + k0 * a.k_ts, at, lk - (int)k0, out, wave);
-        cv.start(V + k0 * a.v_ts, at + TB, lk - (int)k0, out, wave);
+        uint64_t out = from_bit(lk - (int)k0);
+        if constexpr (BIAS) {
+            out |= __ballot(bias == -kInf);
+            if (wave == 0) bias_s[stage][lane] = bias;
+        }
+        copy.start(K + k0 * a.k_ts, koff, at, V + k0 * a.v_ts, voff, at + TB, out, wave);
     };
     if constexpr (FAST) {
-        ck.init(a.k_ts, a.dk, wave, lane);
-        cv.init(a.v_ts, a.dv, wave, lane);
+        copy.init(wave, lane);
+        copy.offsets(koff, a.k_ts, a.dk, lane);
+        copy.offsets(voff, a.v_ts, a.dv, lane);
         if (t0 < t1) {
             if constexpr (BIAS) bias = bias_of(t0 * kKeys);
-            start(t0);
+            start(t0, 0);
             if constexpr (BIAS) bias = bias_of((t0 + 1) * kKeys);
         }
     }
 
     // queries, and how many keys each sees
-    Frag qf[NC][DP / KE];
-    int lim[NC];
-    const int row0 = tile * TR + wave * 32 * NC;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        int token, g;
-        const int r = row0 + 32 * n + (lane & 31);
-        row_of(r, a.G, &token, &g);
-        const T* p = (const T*)a.q + (sq.first + token) * a.q_ts + (int64_t)(hk * a.G + g) * a.q_hs;
-        load_columns<T, DP, FAST>(qf[n], p, a.dk, r < rows, lane);
-        lim[n] = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
-    }
+    Frag qf[DP / KE];
+    const int r = tile * TR + wave * 32 + (lane & 31);
+    int token, g;
+    row_of(r, a.G, &token, &g);
+    const int head = hk * a.G + g;
+    load_columns<T, DP, FAST>(qf, (const T*)a.q + (sq.first + token) * a.q_ts + (int64_t)head * a.q_hs, a.dk, r < rows, lane);
+    const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
 
-    floatx16 o[NC][NT];
-    float m[NC], l[NC];
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    const uint32_t bbase = (uint32_t)(uintptr_t)(lds_f32*)&bias_s[0][0] + 16 * h;
+    floatx16 o[NT];
+    float m = -kInf, l = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        m[n] = -kInf;
-        l[n] = 0.0f;
+    for (int d = 0; d < NT; ++d)
 #pragma unroll
-        for (int d = 0; d < NT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[n][d][e] = 0.0f;
-    }
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
 
-    for (int t = t0; t < t1; ++t) {
+    auto step = [&](auto stage_c, int t) {
+        constexpr int stage = decltype(stage_c)::value;
+        constexpr uint32_t koffs = stage * 2 * TB, voffs = koffs + TB;
         const int k0 = t * kKeys;
-        const uint32_t kbase = base + (FAST ? (uint32_t)(t & 1) * (2 * TB) : 0u), vbase = kbase + TB;
-        const uint32_t bbase = bias_base + (FAST ? (uint32_t)(t & 1) * (kKeys * 4) : 0u);
         if constexpr (FAST) {
             all_arrived();
             if (t + 1 < t1) {
-                start(t + 1);
+                start(t + 1, stage ^ 1);
                 if constexpr (BIAS) bias = bias_of(k0 + 2 * kKeys);
             }
         } else {
             __syncthreads();
+            uint64_t out = from_bit(lk - k0);
             if constexpr (BIAS) {
                 bias = bias_of(k0);
+                out |= __ballot(bias == -kInf);
                 if (wave == 0) bias_s[0][lane] = bias;
             }
-            const uint64_t out = BIAS ? __ballot(bias == -kInf) : 0;
-#pragma unroll
-            for (int i = 0; i < kKeys * L::NCH / (64 * NW); ++i) {
-                const int id = tid + i * 64 * NW, row = id / L::NCH, c = id % L::NCH;
-                const bool ok = k0 + row < lk && !((out >> row) & 1);
+#pragma unroll 1
+            for (int id = tid; id < kKeys * L::NCH; id += 64 * NW) {
+                const int row = id / L::NCH, c = id % L::NCH;
+                const bool ok = !((out >> row) & 1);
                 const int64_t key = k0 + row;
-                const u32x4 kw = load_chunk<T, FAST>(K + key * a.k_ts, c * L::EPC, a.dk, ok);
-                const u32x4 vw = load_chunk<T, FAST>(V + key * a.v_ts, c * L::EPC, a.dv, ok);
-                *(lds_u32x4*)(uintptr_t)(kbase + L::at(row, c)) = kw;
-                *(lds_u32x4*)(uintptr_t)(vbase + L::at(row, c)) = vw;
+                *(lds_u32x4*)(uintptr_t)(base + L::at(row, c)) = load_chunk<T, FAST>(K + key * a.k_ts, c * L::EPC, a.dk, ok);
+                *(lds_u32x4*)(uintptr_t)(base + TB + L::at(row, c)) = load_chunk<T, FAST>(V + key * a.v_ts, c * L::EPC, a.dv, ok);
             }
             __syncthreads();
         }
 
-        floatx16 s[NC][kKeys / 32];
+        floatx16 s[kKeys / 32];
 #pragma unroll
         for (int kt = 0; kt < kKeys / 32; ++kt) {
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
                 floatx4 b = {0, 0, 0, 0};
-                if constexpr (BIAS) b = *(const lds_f32x4*)(uintptr_t)(bbase + 4 * (32 * kt + 8 * e4 + 4 * h));
+                if constexpr (BIAS)
+                    b = *(const lds_f32x4*)(uintptr_t)(bbase + 4 * (stage * kKeys + 32 * kt + 8 * e4));
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][kt][4 * e4 + e] = b[e];
+                for (int e = 0; e < 4; ++e) s[kt][4 * e4 + e] = b[e];
             }
 #pragma unroll
-            for (int c = 0; c < DP / KE; ++c) {
-                const Frag f = L::rows(kbase, 32 * kt, c, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) s[n][kt] = Op<T>::mma(f, qf[n][c], s[n][kt]);
-            }
+            for (int c = 0; c < DP / KE; ++c) s[kt] = Op<T>::mma(rd.rows(koffs, kt, c), qf[c], s[kt]);
         }
         if (k0 + kKeys > least) {   // some row does not see all of the tile
+            const int room = lim - k0 - 4 * h;
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
+            for (int kt = 0; kt < kKeys / 32; ++kt)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (32 * kt + 8 * (e / 4) + e % 4 >= room) s[kt][e] = -kInf;
+        }
+        Frag pf[kKeys / KE];
+        float sum;
+        bool late = m == -kInf;   // rows whose reference is taken anew; the others keep their bits
+        for (;;) {
+            if (__any(late)) {
+                float mx = s[0][0];
 #pragma unroll
                 for (int kt = 0; kt < kKeys / 32; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (k0 + 32 * kt + 8 * (e / 4) + 4 * h + e % 4 >= lim[n]) s[n][kt][e] = -kInf;
-        }
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            float mx = s[n][0][0];
-#pragma unroll
-            for (int kt = 0; kt < kKeys / 32; ++kt)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[n][kt][e]);
-            mx = half_max(mx) * scale2;
-            if (__any(mx > m[n] + kLag)) {
-                const float mnew = fmaxf(m[n], mx);
-                const float shrink = exp2_fast(m[n] - (mnew == -kInf ? 0.0f : mnew));
-                m[n] = mnew;
-                l[n] *= shrink;
+                    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kt][e]);
+                mx = half_max(mx) * scale2;
+                const float mnew = late ? fmaxf(m, mx) : m;
+                const float shrink = exp2_fast(m - (mnew == -kInf ? 0.0f : mnew));
+                m = mnew;
+                l *= shrink;
 #pragma unroll
                 for (int d = 0; d < NT; ++d)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[n][d][e] *= shrink;
+                    for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
             }
-            const float use = m[n] == -kInf ? 0.0f : m[n];
-            float sum[4] = {0, 0, 0, 0};
+            const float use = m == -kInf ? 0.0f : m;
+            float part[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int kt = 0; kt < kKeys / 32; ++kt)
+            for (int kt = 0; kt < kKeys / 32; ++kt) {
+                floatx16 p;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float p = exp2_fast(fmaf(s[n][kt][e], scale2, -use));
-                    s[n][kt][e] = p;
-                    sum[e % 4] += p;
+                    p[e] = exp2_fast(fmaf(s[kt][e], scale2, -use));
+                    part[e % 4] += p[e];
                 }
-            l[n] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
 #pragma unroll
-        for (int kt = 0; kt < kKeys / 32; ++kt)
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                Frag pf[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) pf[n] = Op<T>::from(s[n][kt], b * KE / 2);
-#pragma unroll
-                for (int d = 0; d < NT; ++d) {
-                    const Frag f = L::columns(vbase, 32 * kt + b * KE, d, lane);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) o[n][d] = Op<T>::mma(f, pf[n], o[n][d]);
-                }
+                for (int b = 0; b < KB; ++b) pf[kt * KB + b] = Op<T>::from(p, b * KE / 2);
             }
+            sum = (part[0] + part[1]) + (part[2] + part[3]);
+            if (!__any(sum > kMostSum)) break;
+            late = half_max(sum) > kMostSum;
+        }
+        l += sum;
+#pragma unroll
+        for (int b = 0; b < kKeys / KE; ++b)
+#pragma unroll
+            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns(voffs, b, d), pf[b], o[d]);
+    };
+    if constexpr (FAST) {
+        for (int t = t0; t < t1; t += 2) {
+            step(std::integral_constant<int, 0>(), t);
+            if (t + 1 < t1) step(std::integral_constant<int, 1>(), t + 1);
+        }
+    } else {
+        for (int t = t0; t < t1; ++t) step(std::integral_constant<int, 0>(), t);
     }
 
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int r = row0 + 32 * n + (lane & 31);
-        const float sum = half_sum(l[n]);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const float lse = sum == 0.0f ? -kInf : m[n] * kLn2 + logf(sum);
-        if (r >= rows) continue;
-        int token, g;
-        row_of(r, a.G, &token, &g);
-        const int64_t tok = sq.first + token;
-        const int head = hk * a.G + g;
-        if (a.splits > 1) {
-            const int64_t cell = ((int64_t)split * a.total_q + tok) * a.hq + head;
-            float* part = a.part + cell * a.dv;
-            if (h == 0) a.part_lse[cell] = lse;
-#pragma unroll
-            for (int d = 0; d < NT; ++d)
-#pragma unroll
-                for (int e4 = 0; e4 < 4; ++e4) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = o[n][d][4 * e4 + e] * inv;
-                    store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dv, v);
-                }
-            continue;
-        }
-        if (a.lse && h == 0) a.lse[tok * a.hq + head] = lse;
-        T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
+    const float total = half_sum(l);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float lse = total == 0.0f ? -kInf : m * kLn2 + logf(total);
+    if (r >= rows) return;
+    const int64_t tok = sq.first + token;
+    if (a.splits > 1) {
+        const int64_t cell = ((int64_t)split * a.total_q + tok) * a.hq + head;
+        float* part = a.part + cell * a.dv;
+        if (h == 0) a.part_lse[cell] = lse;
 #pragma unroll
         for (int d = 0; d < NT; ++d)
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
                 float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = o[n][d][4 * e4 + e] * inv;
-                store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dv, v);
+                for (int e = 0; e < 4; ++e) v[e] = o[d][4 * e4 + e] * inv;
+                store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dv, v);
             }
+        return;
     }
+    if (a.lse && h == 0) a.lse[tok * a.hq + head] = lse;
+    T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
+#pragma unroll
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = o[d][4 * e4 + e] * inv;
+            store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dv, v);
+        }
 }
 
 constexpr int kMostSplits = 128;
@@ -305,8 +302,8 @@ int fwd_go(AttnArgs a, hipStream_t st) {
     const int64_t grid = grid_size((int64_t)a.slots * a.splits, a.hkv);
     {
         KernelTimer timer("attn_fwd", st);
-        if (a.bias) attn_fwd<T, DP, NW, 1, true, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
-        else attn_fwd<T, DP, NW, 1, false, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
+        if (a.bias) attn_fwd<T, DP, NW, true, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
+        else attn_fwd<T, DP, NW, false, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
     }
     if (a.splits > 1) {
         KernelTimer timer("attn_join", st);

@@ -32,10 +32,10 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q(AttnArgs a) {
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
     const int split = idx % a.splits;
-    if (!locate(a.cu_q, a.n_seq, a.total_q, a.G, TR, idx / a.splits, &seq, &tile, &tiles)) return;
+    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, idx / a.splits, &seq, &tile, &tiles)) return;
     if (a.causal) tile = tiles - 1 - tile;
-    const Span sq = span_of(a.cu_q, seq, a.n_seq, a.total_q);
-    const Span sk = span_of(a.cu_k, seq, a.n_seq, a.total_k);
+    const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
+    const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
     Frag qf[NC][DP / KE], gf[NC][DP / KE];
@@ -204,9 +204,9 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_kv(AttnArgs a) {
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
     const int split = idx % a.splits;
-    if (!locate(a.cu_k, a.n_seq, a.total_k, 1, TK, idx / a.splits, &seq, &tile, &tiles)) return;
-    const Span sq = span_of(a.cu_q, seq, a.n_seq, a.total_q);
-    const Span sk = span_of(a.cu_k, seq, a.n_seq, a.total_k);
+    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, idx / a.splits, &seq, &tile, &tiles)) return;
+    const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
+    const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
     Frag kf[NC][DP / KE], vf[NC][DP / KE];
