@@ -35,7 +35,7 @@ bool wide(const AttnArgs& a) {
 // each with `least` steps at least
 int parts(int64_t tiles, int64_t steps, int64_t want, int64_t least) {
     if (tiles <= 0 || tiles >= want / 2) return 1;
-    return (int)std::max<int64_t>(1, std::min({want / tiles, steps / least, (int64_t)128}));
+    return (int)std::max<int64_t>(1, std::min({want / tiles, steps / least, (int64_t)256}));
 }
 
 }  // namespace
@@ -44,9 +44,9 @@ AttnPlan attn_plan_fwd(const AttnArgs& a) {
     AttnPlan p{};
     p.fast = wide(a);
     const int64_t rows = ceil_div(a.total_q, a.n_seq) * a.G, keys = ceil_div(a.total_k, a.n_seq);
-    p.waves = p.fast && rows <= 32 ? 1 : 4;
+    p.waves = !p.fast || rows > 64 ? 4 : rows > 32 ? 2 : 1;
     const int64_t tiles = a.n_seq * ceil_div(rows, 32 * p.waves) * a.hkv;
-    p.splits = parts(tiles, ceil_div(keys, 64), p.waves == 1 ? 2048 : 512, 2);
+    p.splits = parts(tiles, ceil_div(keys, 64), 512, 2);
     return p;
 }
 
@@ -177,7 +177,7 @@ int check_desc(const disco_attention_desc* d, AttnArgs* a) {
     a->causal = d->causal != 0;
     a->scale = d->scale;
     // every sequence costs a tile for each key head and split
-    if ((int64_t)d->n_seq * d->hkv * 128 > kMost)
+    if ((int64_t)d->n_seq * d->hkv * 256 > kMost)
         return set_error(DISCO_EUNSUPPORTED, "too many sequences in one call (%d of %d key heads)", d->n_seq, d->hkv);
     a->each_q = (int)(d->total_q / d->n_seq);
     a->each_k = (int)(d->total_k / d->n_seq);

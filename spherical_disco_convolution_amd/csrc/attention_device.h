@@ -260,6 +260,14 @@ __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t off, uint32_t at) 
                  : "memory", "m0");
 }
 
+// 4 bytes a lane in the same way
+__device__ __forceinline__ void copy4(u32x4 buffer, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(at))
+                 : "memory", "m0");
+}
+
 __device__ __forceinline__ u32x4 buffer_of(const void* p) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     u32x4 b;
@@ -270,45 +278,39 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p) {
     return b;
 }
 
-// All of the workgroup's copies, reads and writes so far are done
+// All of the workgroup's reads and writes of LDS so far are done, and its copies
+// but for the last N of each wave
+template <int N = 0>
 __device__ __forceinline__ void all_arrived() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// A tile of 64 rows, NW waves: instruction j of a wave moves 1 KiB of it, and
-// its rows lie 64 / N further on than those of instruction j - 1
-template <typename T, int DP, int NW>
+// A tile of R rows, NW waves: instruction j of a wave moves 1 KiB of it, and its
+// rows lie R / N further on than those of instruction j - 1
+template <typename T, int DP, int R, int NW>
 struct Copy {
     typedef Tile<T, DP> L;
-    static constexpr int N = 64 * L::RB / 1024 / NW;
-    static_assert(N >= 1 && 64 * L::RB == N * 1024 * NW, "whole instructions");
+    static constexpr int N = R * L::RB / 1024 / NW;
+    static_assert(N >= 1 && R * L::RB == N * 1024 * NW && R <= 64, "whole instructions");
     int row;             // of instruction 0
     __device__ __forceinline__ void init(int wave, int lane) { row = (wave * 64 + lane) / L::NCH; }
     // offsets of rows ts elements apart, d elements long
     __device__ __forceinline__ void offsets(uint32_t* off, int64_t ts, int d, int lane) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int r = row + j * (64 / N), src = ((lane % L::NCH) ^ L::turn(r)) * L::EPC;
+            const int r = row + j * (R / N), src = ((lane % L::NCH) ^ L::turn(r)) * L::EPC;
             off[j] = src < d ? (uint32_t)((r * ts + src) * (int64_t)sizeof(T)) : kNowhere;
         }
     }
-    // two tiles of the same rows; a row whose bit in `out` is set becomes zeros
-    __device__ __forceinline__ void start(const T* p, const uint32_t* po, uint32_t pat, const T* q, const uint32_t* qo,
-                                          uint32_t qat, uint64_t out, int wave) const {
-        const u32x4 pb = buffer_of(p), qb = buffer_of(q);
-        if (out == 0) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                copy16(pb, po[j], pat + (uint32_t)(j * NW + wave) * 1024u);
-                copy16(qb, qo[j], qat + (uint32_t)(j * NW + wave) * 1024u);
-            }
-            return;
-        }
+    // rows whose bit in `out` is set become zeros
+    __device__ __forceinline__ void start(const T* p, const uint32_t* off, uint32_t at, uint64_t out, int wave) const {
+        const u32x4 b = buffer_of(p);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const bool ok = !((out >> (j * (64 / N))) >> row & 1);
-            copy16(pb, ok ? po[j] : kNowhere, pat + (uint32_t)(j * NW + wave) * 1024u);
-            copy16(qb, ok ? qo[j] : kNowhere, qat + (uint32_t)(j * NW + wave) * 1024u);
+            uint32_t drop;   // all ones if this lane's row is left out
+            if constexpr (R <= 32 || N > 1) drop = (uint32_t)__builtin_amdgcn_sbfe((int)(uint32_t)(out >> (j * (R / N))), row, 1);
+            else drop = (out >> row) & 1 ? ~0u : 0u;
+            copy16(b, off[j] | (drop & kNowhere), at + (uint32_t)(j * NW + wave) * 1024u);
         }
     }
 };

@@ -10,23 +10,71 @@ using namespace attn;
 
 namespace {
 
-constexpr int kKeys = 64;   // keys of a tile
+// Asks the scheduler to lay out what stands before it in this order: AHEAD reads
+// of LDS, then M times a matrix instruction with the reads and the vector
+// instructions that fit beside it.
+template <int M, int AHEAD, int READS, int VALU, int TRANS>
+__device__ __forceinline__ void mix() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+        __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+    }
+}
+
+// A key's bias as the first summand of its scores: a product of its own, of the
+// bias in three bfloat16 parts (24 bits) with ones.  -inf stays -inf.
+template <typename T>
+struct Bias;
+
+template <>
+struct Bias<bf16_t> {
+    typedef uint32_t Word __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ Word pack(float b) {
+        const bf16_t hi = f32_to_bf16(b);
+        const float r = b == -kInf ? 0.0f : b - bf16_to_f32(hi);
+        const bf16_t mid = f32_to_bf16(r);
+        return Word{hi | (uint32_t)mid << 16, f32_to_bf16(r - bf16_to_f32(mid))};
+    }
+    static __device__ __forceinline__ floatx16 spread(Word w) {
+        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, u32x4{w[0], w[1], 0, 0});
+        const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4{0x3f803f80u, 0x3f80u, 0, 0});
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ones, floatx16{}, 0, 0, 0);
+    }
+};
+
+template <>
+struct Bias<float> {
+    typedef float Word;
+    static __device__ __forceinline__ Word pack(float b) { return b; }
+    static __device__ __forceinline__ floatx16 spread(Word w) {
+        return __builtin_amdgcn_mfma_f32_32x32x2f32(w, 1.0f, floatx16{}, 0, 0, 0);
+    }
+};
+
 // The running maximum may lag: weights of 2^60 keep as many digits as weights of
 // 1, in bfloat16 too.  So a tile's maximum is taken only where the sum of its
 // weights passes this bound, or where the row has seen no key yet.
 constexpr float kMostSum = 1.152921504606846976e18f;
 
-// A workgroup of NW waves has 32 rows a wave and walks over the keys of its part
-// in tiles of 64: one pass with a reference close to the running maximum, and
-// the running sum.
-template <typename T, int DP, int NW, bool BIAS, bool FAST>
+// A workgroup of NW waves has 32 rows a wave and walks over the keys of its
+// part in tiles of KT: one pass with a reference close to the running maximum, and
+// the running sum.  Three tiles are under way in a wave: while tile i's scores
+// become weights on the vector units, the matrix cores take the scores of i + 1
+// and the values of i - 1, which depend on none of it.
+template <typename T, int DP, int NW, int KT, bool BIAS, bool FAST>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1) void attn_fwd(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
-    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, TB = kKeys * L::RB;
-    constexpr int STAGES = FAST ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * 2 * TB];
-    __shared__ __attribute__((aligned(16))) float bias_s[STAGES][kKeys];
+    typedef typename Bias<T>::Word Word;
+    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, NK = KT / 32, TB = KT * L::RB;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TB];   // two stages of keys, then of values
+    // biases, and zeros for the upper half of the lanes
+    __shared__ __attribute__((aligned(16))) Word bias_s[BIAS ? 2 : 1][2][KT];
+    __shared__ __attribute__((aligned(16))) float raw_s[BIAS && FAST ? 2 : 1][64];
     const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
@@ -49,7 +97,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
         least = uniform(min(max(t_first + ahead + 1, 0), lk));
     }
     // this part's tiles of keys
-    const int all = (most + kKeys - 1) / kKeys;
+    const int all = (most + KT - 1) / KT;
     int t0 = 0, t1 = all;
     if (a.splits > 1) {
         t0 = (int)((int64_t)all * split / a.splits);
@@ -63,180 +111,204 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 
     // a key's bias in units of the raw score, which starts the score's sum; -inf
     // where the key is left out.  What lies there stays out of every product.
-    auto bias_of = [&](int k0) -> float {
-        const int key = k0 + lane;
-        const float b = key < lk ? B[key] : -kInf;
-        return b < kLowest ? -kInf : b * per_scale;
-    };
-    typedef Copy<T, DP, FAST ? NW : 1> C;
+    auto scaled = [&](float b, int key) -> float { return key >= lk || b < kLowest ? -kInf : b * per_scale; };
+    typedef Copy<T, DP, KT, FAST ? NW : 1> C;
     C copy;
     uint32_t koff[C::N], voff[C::N];
-    float bias = 0.0f;
-    auto start = [&](int t, int stage) {   // the copies of tile t; `bias` is tile t's
-        const uint32_t at = base + (uint32_t)stage * (2 * TB);
-        const int64_t k0 = (int64_t)t * kKeys;
-        uint64_t out = from_bit(lk - (int)k0);
-        if constexpr (BIAS) {
-            out |= __ballot(bias == -kInf);
-            if (wave == 0) bias_s[stage][lane] = bias;
+    // Tiles of this part are counted from 0, tile i has stage i % 2.  KT rows from
+    // tile i's first into LDS at `at`; rows of `out` become zeros.
+    const int n_tiles = t1 - t0;
+    auto start = [&](const T*& next, int64_t ts, int d, const uint32_t* off, uint32_t at, uint64_t out) {
+        const T* q = next;
+        next += KT * ts;
+        if constexpr (FAST) {
+            copy.start(q, off, at, out, wave);
+        } else {
+#pragma unroll 1
+            for (int id = tid; id < KT * L::NCH; id += 64 * NW) {
+                const int row = id / L::NCH, c = id % L::NCH;
+                *(lds_u32x4*)(uintptr_t)(at + L::at(row, c)) =
+                    load_chunk<T, FAST>(q + row * ts, c * L::EPC, d, !((out >> row) & 1));
+            }
         }
-        copy.start(K + k0 * a.k_ts, koff, at, V + k0 * a.v_ts, voff, at + TB, out, wave);
     };
-    if constexpr (FAST) {
-        copy.init(wave, lane);
-        copy.offsets(koff, a.k_ts, a.dk, lane);
-        copy.offsets(voff, a.v_ts, a.dv, lane);
-        if (t0 < t1) {
-            if constexpr (BIAS) bias = bias_of(t0 * kKeys);
-            start(t0, 0);
-            if constexpr (BIAS) bias = bias_of((t0 + 1) * kKeys);
+    // rows of the next tile to be asked for
+    const T *knext = K + (int64_t)t0 * KT * a.k_ts, *vnext = V + (int64_t)t0 * KT * a.v_ts;
+    const float* bnext = BIAS ? B + t0 * KT : nullptr;
+    uint64_t outs[2];   // rows left out of the tiles under way
+    auto start_keys = [&](int i, int stage, float b) {
+        outs[stage] = from_bit(lk - (t0 + i) * KT);
+        if constexpr (BIAS) {
+            b = scaled(b, (t0 + i) * KT + lane);
+            outs[stage] |= __ballot(b == -kInf);
+            if (wave == 0 && lane < KT) bias_s[stage][0][lane] = Bias<T>::pack(b);
         }
-    }
+        start(knext, a.k_ts, a.dk, koff, base + (uint32_t)stage * TB, outs[stage]);
+    };
+    auto start_values = [&](int stage) {
+        start(vnext, a.v_ts, a.dv, voff, base + (uint32_t)(2 + stage) * TB, outs[stage]);
+    };
+    auto bias_of = [&](int i) -> float {
+        const int key = (t0 + i) * KT + lane;
+        return key < lk ? B[key] : 0.0f;
+    };
+    auto start_bias = [&](int i, int stage) {   // by the first wave
+        const uint32_t off = (t0 + i) * KT + lane < lk ? (uint32_t)lane * 4u : kNowhere;
+        copy4(buffer_of(bnext + i * KT), off, (uint32_t)(uintptr_t)(lds_f32*)&raw_s[stage][0]);
+    };
 
     // queries, and how many keys each sees
-    Frag qf[DP / KE];
     const int r = tile * TR + wave * 32 + (lane & 31);
     int token, g;
     row_of(r, a.G, &token, &g);
+    const int64_t tok = sq.first + token;
     const int head = hk * a.G + g;
-    load_columns<T, DP, FAST>(qf, (const T*)a.q + (sq.first + token) * a.q_ts + (int64_t)head * a.q_hs, a.dk, r < rows, lane);
     const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
-
-    Reader<T, DP> rd;
-    rd.init(base, lane);
-    const uint32_t bbase = (uint32_t)(uintptr_t)(lds_f32*)&bias_s[0][0] + 16 * h;
-    floatx16 o[NT];
     float m = -kInf, l = 0.0f;
+    Frag qf[DP / KE], pf[2][KT / KE];
+    floatx16 o[NT], s[2][NK];
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    typedef __attribute__((address_space(3))) Word lds_word;
+    const uint32_t bbase = (uint32_t)(uintptr_t)(lds_word*)&bias_s[0][h][lane & 31];
 
-    auto step = [&](auto stage_c, int t) {
-        constexpr int stage = decltype(stage_c)::value;
-        constexpr uint32_t koffs = stage * 2 * TB, voffs = koffs + TB;
-        const int k0 = t * kKeys;
-        if constexpr (FAST) {
-            all_arrived();
-            if (t + 1 < t1) {
-                start(t + 1, stage ^ 1);
-                if constexpr (BIAS) bias = bias_of(k0 + 2 * kKeys);
-            }
-        } else {
-            __syncthreads();
-            uint64_t out = from_bit(lk - k0);
-            if constexpr (BIAS) {
-                bias = bias_of(k0);
-                out |= __ballot(bias == -kInf);
-                if (wave == 0) bias_s[0][lane] = bias;
-            }
-#pragma unroll 1
-            for (int id = tid; id < kKeys * L::NCH; id += 64 * NW) {
-                const int row = id / L::NCH, c = id % L::NCH;
-                const bool ok = !((out >> row) & 1);
-                const int64_t key = k0 + row;
-                *(lds_u32x4*)(uintptr_t)(base + L::at(row, c)) = load_chunk<T, FAST>(K + key * a.k_ts, c * L::EPC, a.dk, ok);
-                *(lds_u32x4*)(uintptr_t)(base + TB + L::at(row, c)) = load_chunk<T, FAST>(V + key * a.v_ts, c * L::EPC, a.dv, ok);
-            }
-            __syncthreads();
+    auto score = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value;
+#pragma unroll
+        for (int kt = 0; kt < NK; ++kt) {
+            floatx16& x = s[st][kt];
+            x = floatx16{};
+            if constexpr (BIAS) x = Bias<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * st * KT + 32 * kt)));
+#pragma unroll
+            for (int c = 0; c < DP / KE; ++c) x = Op<T>::mma(rd.rows(st * TB, kt, c), qf[c], x);
         }
-
-        floatx16 s[kKeys / 32];
+    };
+    auto weigh = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value;
 #pragma unroll
-        for (int kt = 0; kt < kKeys / 32; ++kt) {
+        for (int b = 0; b < KT / KE; ++b)
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                floatx4 b = {0, 0, 0, 0};
-                if constexpr (BIAS)
-                    b = *(const lds_f32x4*)(uintptr_t)(bbase + 4 * (stage * kKeys + 32 * kt + 8 * e4));
+            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[st][b], o[d]);
+    };
+    // scores to weights, and this lane's part of their sum
+    auto soften = [&](const floatx16* x, Frag* w) -> float {
+        const float use = m == -kInf ? 0.0f : m;
+        float part[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[kt][4 * e4 + e] = b[e];
+        for (int kt = 0; kt < NK; ++kt) {
+            floatx16 p;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                p[e] = exp2_fast(fmaf(x[kt][e], scale2, -use));
+                part[e % 4] += p[e];
             }
 #pragma unroll
-            for (int c = 0; c < DP / KE; ++c) s[kt] = Op<T>::mma(rd.rows(koffs, kt, c), qf[c], s[kt]);
+            for (int b = 0; b < KB; ++b) w[kt * KB + b] = Op<T>::from(p, b * KE / 2);
         }
-        if (k0 + kKeys > least) {   // some row does not see all of the tile
+        return (part[0] + part[1]) + (part[2] + part[3]);
+    };
+    float raw = 0.0f;
+    auto step = [&](auto stage_c, int i) {
+        constexpr int st = decltype(stage_c)::value;
+        const int k0 = (t0 + i) * KT;
+        all_arrived();   // keys i + 1 and values i - 1; all waves have left keys i and values i - 2
+        start_values(st);
+        if constexpr (BIAS && !FAST) raw = bias_of(i + 2);
+        start_keys(i + 2, st, raw);
+        if constexpr (BIAS && FAST) {
+            if (wave == 0) start_bias(i + 4, st);
+            raw = raw_s[st ^ 1][lane];   // of tile i + 3
+        }
+        if (k0 + KT > least) {   // some row does not see all of the tile
             const int room = lim - k0 - 4 * h;
 #pragma unroll
-            for (int kt = 0; kt < kKeys / 32; ++kt)
+            for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (32 * kt + 8 * (e / 4) + e % 4 >= room) s[kt][e] = -kInf;
+                    if (32 * kt + 8 * (e / 4) + e % 4 >= room) s[st][kt][e] = -kInf;
         }
-        Frag pf[kKeys / KE];
-        float sum;
-        bool late = m == -kInf;   // rows whose reference is taken anew; the others keep their bits
-        for (;;) {
-            if (__any(late)) {
-                float mx = s[0][0];
+        score(std::integral_constant<int, st ^ 1>());   // behind the last tile: not used
+        weigh(std::integral_constant<int, st ^ 1>());
+        float sum = soften(s[st], pf[st]);
+        // NK DP / KE products for the scores and as many for the values (2 percent
+        // faster than in the compiler's order)
+        if constexpr (sizeof(T) == 2) mix<NK * DP / 8, 6, 2, 320 / DP, 128 / DP>();
+        // rows whose reference is taken anew; the others keep their bits
+        bool late = m == -kInf;
+        if (__any(late || sum > kMostSum)) {
+            late = late || half_max(sum) > kMostSum;
+            float mx = s[st][0][0];
 #pragma unroll
-                for (int kt = 0; kt < kKeys / 32; ++kt)
+            for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kt][e]);
-                mx = half_max(mx) * scale2;
-                const float mnew = late ? fmaxf(m, mx) : m;
-                const float shrink = exp2_fast(m - (mnew == -kInf ? 0.0f : mnew));
-                m = mnew;
-                l *= shrink;
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[st][kt][e]);
+            mx = half_max(mx) * scale2;
+            const float mnew = late ? fmaxf(m, mx) : m;
+            const float shrink = exp2_fast(m - (mnew == -kInf ? 0.0f : mnew));
+            m = mnew;
+            l *= shrink;
 #pragma unroll
-                for (int d = 0; d < NT; ++d)
+            for (int d = 0; d < NT; ++d)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
-            }
-            const float use = m == -kInf ? 0.0f : m;
-            float part[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int kt = 0; kt < kKeys / 32; ++kt) {
-                floatx16 p;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    p[e] = exp2_fast(fmaf(s[kt][e], scale2, -use));
-                    part[e % 4] += p[e];
-                }
-#pragma unroll
-                for (int b = 0; b < KB; ++b) pf[kt * KB + b] = Op<T>::from(p, b * KE / 2);
-            }
-            sum = (part[0] + part[1]) + (part[2] + part[3]);
-            if (!__any(sum > kMostSum)) break;
-            late = half_max(sum) > kMostSum;
+                for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
+            sum = soften(s[st], pf[st]);
         }
         l += sum;
-#pragma unroll
-        for (int b = 0; b < kKeys / KE; ++b)
-#pragma unroll
-            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns(voffs, b, d), pf[b], o[d]);
     };
+
     if constexpr (FAST) {
-        for (int t = t0; t < t1; t += 2) {
-            step(std::integral_constant<int, 0>(), t);
-            if (t + 1 < t1) step(std::integral_constant<int, 1>(), t + 1);
+        copy.init(wave, lane);
+        copy.offsets(koff, a.k_ts, a.dk, lane);
+        copy.offsets(voff, a.v_ts, a.dv, lane);
+    }
+    if (n_tiles > 0) {
+        float b[2] = {0.0f, 0.0f};
+        if constexpr (BIAS) {
+            b[0] = bias_of(0);
+            b[1] = bias_of(1);
+            raw = bias_of(2);
         }
-    } else {
-        for (int t = t0; t < t1; ++t) step(std::integral_constant<int, 0>(), t);
+        start_keys(0, 0, b[0]);
+        start_keys(1, 1, b[1]);
+        if constexpr (BIAS) {
+            if (FAST && wave == 0) start_bias(3, 1);
+            for (int i = tid; i < 2 * KT; i += 64 * NW) bias_s[i / KT][1][i % KT] = Word{};
+        }
+        // no values before the first: zeros, with weights of zero
+        for (int i = tid; i < TB / 16; i += 64 * NW)
+            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < KT / KE; ++i) pf[1][i] = Frag{};
+        load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, r < rows, lane);
+        all_arrived();
+        score(std::integral_constant<int, 0>());
+        int i = 0;
+        for (;;) {
+            step(std::integral_constant<int, 0>(), i);
+            if (++i == n_tiles) break;
+            step(std::integral_constant<int, 1>(), i);
+            if (++i == n_tiles) break;
+        }
+        all_arrived();
+        if (n_tiles & 1) weigh(std::integral_constant<int, 0>());
+        else weigh(std::integral_constant<int, 1>());
     }
 
     const float total = half_sum(l);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const float lse = total == 0.0f ? -kInf : m * kLn2 + logf(total);
     if (r >= rows) return;
-    const int64_t tok = sq.first + token;
-    if (a.splits > 1) {
-        const int64_t cell = ((int64_t)split * a.total_q + tok) * a.hq + head;
-        float* part = a.part + cell * a.dv;
-        if (h == 0) a.part_lse[cell] = lse;
-#pragma unroll
-        for (int d = 0; d < NT; ++d)
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = o[d][4 * e4 + e] * inv;
-                store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dv, v);
-            }
-        return;
+    const int64_t cell = ((int64_t)split * a.total_q + tok) * a.hq + head;
+    if (h == 0) {
+        if (a.splits > 1) a.part_lse[cell] = lse;
+        else if (a.lse) a.lse[cell] = lse;
     }
-    if (a.lse && h == 0) a.lse[tok * a.hq + head] = lse;
-    T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
+    float* part = a.part + cell * a.dv;
+    T* orow = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
@@ -244,90 +316,99 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = o[d][4 * e4 + e] * inv;
-            store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dv, v);
+            if (a.splits > 1) store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dv, v);
+            else store4<T, FAST>(orow, 32 * d + 8 * e4 + 4 * h, a.dv, v);
         }
 }
 
-constexpr int kMostSplits = 128;
+constexpr int kMostSplits = 256, kJoinWaves = 16;
 
 // Joins the parts of each row: a workgroup a row, its waves share the parts.
 //   l = log sum_s exp l_s,  o = sum_s exp(l_s - l) o_s
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
-    __shared__ float w_s[kMostSplits], red[4][128];
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join(AttnArgs a) {
+    constexpr int P = kMostSplits / 64;
+    __shared__ float w_s[kMostSplits], red[kJoinWaves][128];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t cell = blockIdx.x, tok = cell / a.hq;
     const int head = (int)(cell - tok * a.hq);
     // tokens before the first and behind the last sequence stay as they are
     if (a.cu_q && (tok < a.cu_q[0] || tok >= a.cu_q[a.n_seq])) return;
     const int64_t stride = a.total_q * a.hq;
-    const float l0 = lane < a.splits ? a.part_lse[lane * stride + cell] : -kInf;
-    const float l1 = lane + 64 < a.splits ? a.part_lse[(lane + 64) * stride + cell] : -kInf;
-    float mx = fmaxf(l0, l1);
+    float l[P], mx = -kInf, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        l[i] = lane + 64 * i < a.splits ? a.part_lse[(lane + 64 * i) * stride + cell] : -kInf;
+        mx = fmaxf(mx, l[i]);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
     const float use = mx == -kInf ? 0.0f : mx;
-    const float w0 = exp2_fast((l0 - use) * kLog2e), w1 = exp2_fast((l1 - use) * kLog2e);
-    float sum = w0 + w1;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const float w = exp2_fast((l[i] - use) * kLog2e);
+        if (wave == 0) w_s[lane + 64 * i] = w;
+        sum += w;
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
-    if (wave == 0) {
-        w_s[lane] = w0;
-        w_s[lane + 64] = w1;
-    }
     __syncthreads();
     float v0 = 0.0f, v1 = 0.0f;
     const float* p = a.part + cell * a.dv;
-    const bool has0 = lane < a.dv, has1 = lane + 64 < a.dv;
+    const int d0 = min(lane, a.dv - 1), d1 = min(lane + 64, a.dv - 1);
 #pragma unroll 8
-    for (int s = wave; s < a.splits; s += 4) {
+    for (int s = wave; s < a.splits; s += kJoinWaves) {
         const float* q = p + s * stride * a.dv;
-        const float w = w_s[s];
-        if (has0) v0 = fmaf(w, q[lane], v0);
-        if (has1) v1 = fmaf(w, q[lane + 64], v1);
+        v0 = fmaf(w_s[s], q[d0], v0);
+        v1 = fmaf(w_s[s], q[d1], v1);
     }
     red[wave][lane] = v0;
     red[wave][lane + 64] = v1;
     __syncthreads();
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (a.lse && threadIdx.x == 0) a.lse[cell] = sum == 0.0f ? -kInf : use + logf(sum);
-    T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
     const int d = threadIdx.x;
-    if (d < a.dv) store_f(out, d, ((red[0][d] + red[1][d]) + (red[2][d] + red[3][d])) * inv);
+    if (d >= a.dv) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinWaves; ++i) v += red[i][d];
+    store_f((T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs, d, v * inv);
 }
 
-template <typename T, int DP, int NW, bool FAST>
+template <typename T, int DP, int NW, int KT, bool FAST>
 int fwd_go(AttnArgs a, hipStream_t st) {
     a.slots = (int)tile_slots(a.cu_q != nullptr, a.total_q, a.n_seq, a.G, 32 * NW);
     const int64_t grid = grid_size((int64_t)a.slots * a.splits, a.hkv);
     {
         KernelTimer timer("attn_fwd", st);
-        if (a.bias) attn_fwd<T, DP, NW, true, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
-        else attn_fwd<T, DP, NW, false, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
+        if (a.bias) attn_fwd<T, DP, NW, KT, true, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
+        else attn_fwd<T, DP, NW, KT, false, FAST><<<(unsigned)grid, 64 * NW, 0, st>>>(a);
     }
     if (a.splits > 1) {
         KernelTimer timer("attn_join", st);
-        attn_join<T><<<(unsigned)(a.total_q * a.hq), 256, 0, st>>>(a);
+        attn_join<T><<<(unsigned)(a.total_q * a.hq), 64 * kJoinWaves, 0, st>>>(a);
     }
     return attn_launched("attention_fwd");
 }
 
+template <typename T, int DP, int KT>
+int fwd_waves(const AttnArgs& a, int waves, hipStream_t st) {
+    if (waves == 1) return fwd_go<T, DP, 1, KT, true>(a, st);
+    if (waves == 2) return fwd_go<T, DP, 2, KT, true>(a, st);
+    return fwd_go<T, DP, 4, KT, true>(a, st);
+}
+
 template <typename T>
-int fwd_typed(const AttnArgs& a, hipStream_t st) {
+int fwd_typed(AttnArgs a, hipStream_t st) {
     const AttnPlan p = attn_plan_fwd(a);
-    AttnArgs b = a;
-    b.splits = p.splits;
-    if (!p.fast) return fwd_go<T, 128, 4, false>(b, st);
-#define DISCO_ATTN(DP)                                             \
-    do {                                                           \
-        if (p.waves == 1) return fwd_go<T, DP, 1, true>(b, st);    \
-        return fwd_go<T, DP, 4, true>(b, st);                      \
-    } while (0)
+    a.splits = p.splits;
+    // keys of a tile: 64 where two waves of a SIMD still hold their scores
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32;
+    if (!p.fast) return fwd_go<T, 128, 4, KT, false>(a, st);
     const int d = std::max(a.dk, a.dv);
-    if (d <= 32) DISCO_ATTN(32);
-    if (d <= 64) DISCO_ATTN(64);
-    DISCO_ATTN(128);
-#undef DISCO_ATTN
+    if (d <= 32) return fwd_waves<T, 32, KT>(a, p.waves, st);
+    if (d <= 64) return fwd_waves<T, 64, KT>(a, p.waves, st);
+    return fwd_waves<T, 128, 32>(a, p.waves, st);
 }
 
 }  // namespace
