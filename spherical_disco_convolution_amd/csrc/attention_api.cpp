@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "api_checks.h"
 #include "disco_internal.h"
@@ -28,6 +29,9 @@ bool wide(const AttnArgs& a) {
     const int64_t size = 16 / epc, reach = ((int64_t)1 << 31) / (64 * size);
     for (int64_t s : {a.k_ts, a.v_ts})
         if (s >= reach) return false;
+    if (a.go)   // a step's rows of the gradient of k and v: up to 33 tokens of G heads
+        for (const auto& s : {std::make_pair(a.q_ts, a.q_hs), std::make_pair(a.go_ts, a.go_hs)})
+            if (s.first >= reach || s.second >= reach / a.G) return false;
     return true;
 }
 

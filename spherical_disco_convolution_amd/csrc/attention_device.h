@@ -197,6 +197,52 @@ struct Reader {
     }
 };
 
+// Asks the scheduler to lay out what stands before it in this order: AHEAD reads
+// of LDS, then M times a matrix instruction with the reads and the vector
+// instructions that fit beside it.
+template <int M, int AHEAD, int READS, int VALU, int TRANS>
+__device__ __forceinline__ void mix() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+        __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+    }
+}
+
+// A value of a row (a key's bias, say) as the first summand of its products: one
+// of its own, of the value in three bfloat16 parts (24 bits) with ones.  -inf stays
+// -inf.  The upper half of the lanes gives zeros.
+template <typename T>
+struct Addend;
+
+template <>
+struct Addend<bf16_t> {
+    typedef uint32_t Word __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ Word pack(float b) {
+        const bf16_t hi = f32_to_bf16(b);
+        const float r = b == -kInf ? 0.0f : b - bf16_to_f32(hi);
+        const bf16_t mid = f32_to_bf16(r);
+        return Word{hi | (uint32_t)mid << 16, f32_to_bf16(r - bf16_to_f32(mid))};
+    }
+    static __device__ __forceinline__ floatx16 spread(Word w) {
+        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, u32x4{w[0], w[1], 0, 0});
+        const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4{0x3f803f80u, 0x3f80u, 0, 0});
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ones, floatx16{}, 0, 0, 0);
+    }
+};
+
+template <>
+struct Addend<float> {
+    typedef float Word;
+    static __device__ __forceinline__ Word pack(float b) { return b; }
+    static __device__ __forceinline__ floatx16 spread(Word w) {
+        return __builtin_amdgcn_mfma_f32_32x32x2f32(w, 1.0f, floatx16{}, 0, 0, 0);
+    }
+};
+
 // 16 bytes of a row from element d0, zeros past D.  FAST: D, strides and
 // addresses are multiples of 16 bytes.
 template <typename T, bool FAST>
@@ -290,8 +336,10 @@ __device__ __forceinline__ void all_arrived() {
 template <typename T, int DP, int R, int NW>
 struct Copy {
     typedef Tile<T, DP> L;
-    static constexpr int N = R * L::RB / 1024 / NW;
-    static_assert(N >= 1 && R * L::RB == N * 1024 * NW && R <= 64, "whole instructions");
+    static constexpr int ALL = R * L::RB / 1024, N = ALL < NW ? 1 : ALL / NW;
+    static_assert(ALL * 1024 == R * L::RB && (ALL < NW || N * NW == ALL) && R <= 64, "whole instructions");
+    // a small tile leaves waves without a share
+    static __device__ __forceinline__ bool shares(int wave) { return ALL >= NW || wave < ALL; }
     int row;             // of instruction 0
     __device__ __forceinline__ void init(int wave, int lane) { row = (wave * 64 + lane) / L::NCH; }
     // offsets of rows ts elements apart, d elements long
@@ -304,6 +352,7 @@ struct Copy {
     }
     // rows whose bit in `out` is set become zeros
     __device__ __forceinline__ void start(const T* p, const uint32_t* off, uint32_t at, uint64_t out, int wave) const {
+        if (!shares(wave)) return;
         const u32x4 b = buffer_of(p);
 #pragma unroll
         for (int j = 0; j < N; ++j) {

@@ -10,51 +10,6 @@ using namespace attn;
 
 namespace {
 
-// Asks the scheduler to lay out what stands before it in this order: AHEAD reads
-// of LDS, then M times a matrix instruction with the reads and the vector
-// instructions that fit beside it.
-template <int M, int AHEAD, int READS, int VALU, int TRANS>
-__device__ __forceinline__ void mix() {
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-        __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
-    }
-}
-
-// A key's bias as the first summand of its scores: a product of its own, of the
-// bias in three bfloat16 parts (24 bits) with ones.  -inf stays -inf.
-template <typename T>
-struct Bias;
-
-template <>
-struct Bias<bf16_t> {
-    typedef uint32_t Word __attribute__((ext_vector_type(2)));
-    static __device__ __forceinline__ Word pack(float b) {
-        const bf16_t hi = f32_to_bf16(b);
-        const float r = b == -kInf ? 0.0f : b - bf16_to_f32(hi);
-        const bf16_t mid = f32_to_bf16(r);
-        return Word{hi | (uint32_t)mid << 16, f32_to_bf16(r - bf16_to_f32(mid))};
-    }
-    static __device__ __forceinline__ floatx16 spread(Word w) {
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, u32x4{w[0], w[1], 0, 0});
-        const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4{0x3f803f80u, 0x3f80u, 0, 0});
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ones, floatx16{}, 0, 0, 0);
-    }
-};
-
-template <>
-struct Bias<float> {
-    typedef float Word;
-    static __device__ __forceinline__ Word pack(float b) { return b; }
-    static __device__ __forceinline__ floatx16 spread(Word w) {
-        return __builtin_amdgcn_mfma_f32_32x32x2f32(w, 1.0f, floatx16{}, 0, 0, 0);
-    }
-};
-
 // The running maximum may lag: weights of 2^60 keep as many digits as weights of
 // 1, in bfloat16 too.  So a tile's maximum is taken only where the sum of its
 // weights passes this bound, or where the row has seen no key yet.
@@ -69,7 +24,7 @@ template <typename T, int DP, int NW, int KT, bool BIAS, bool FAST>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1) void attn_fwd(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
-    typedef typename Bias<T>::Word Word;
+    typedef typename Addend<T>::Word Word;
     constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, NK = KT / 32, TB = KT * L::RB;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TB];   // two stages of keys, then of values
     // biases, and zeros for the upper half of the lanes
@@ -141,7 +96,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
         if constexpr (BIAS) {
             b = scaled(b, (t0 + i) * KT + lane);
             outs[stage] |= __ballot(b == -kInf);
-            if (wave == 0 && lane < KT) bias_s[stage][0][lane] = Bias<T>::pack(b);
+            if (wave == 0 && lane < KT) bias_s[stage][0][lane] = Addend<T>::pack(b);
         }
         start(knext, a.k_ts, a.dk, koff, base + (uint32_t)stage * TB, outs[stage]);
     };
@@ -182,7 +137,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
         for (int kt = 0; kt < NK; ++kt) {
             floatx16& x = s[st][kt];
             x = floatx16{};
-            if constexpr (BIAS) x = Bias<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * st * KT + 32 * kt)));
+            if constexpr (BIAS) x = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * st * KT + 32 * kt)));
 #pragma unroll
             for (int c = 0; c < DP / KE; ++c) x = Op<T>::mma(rd.rows(st * TB, kt, c), qf[c], x);
         }

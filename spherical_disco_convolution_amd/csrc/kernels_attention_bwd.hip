@@ -9,6 +9,7 @@
 #include "attention_device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace disco {
 
@@ -16,344 +17,496 @@ using namespace attn;
 
 namespace {
 
-constexpr int kStep = 64;   // keys (gq) or rows (gk, gv) of a step
+constexpr int kStep = 32;   // keys (gq) or rows (gk, gv) of a step
 
-template <typename T, int DP, int NW, int NC, bool BIAS, bool FAST>
-__global__ __launch_bounds__(64 * NW) void attn_bwd_q(AttnArgs a) {
+// A workgroup of NW waves has 32 rows a wave and walks over the keys of its part.
+// Three steps are under way in a wave: while the scores of step i become ds on the
+// vector units, the matrix cores take the scores and dp of step i + 1 and the
+// gradient's part of step i - 1.
+template <typename T, int DP, int NW, bool BIAS, bool FAST>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_bwd_q(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
-    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NC * NW, KB = 32 / KE;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStep * L::RB];
-    __shared__ __attribute__((aligned(16))) float bias_s[kStep];
-    const uint32_t kbase = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
-    const uint32_t vbase = kbase + kStep * L::RB;
+    typedef typename Addend<T>::Word Word;
+    constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[6 * TB];   // four stages of keys, two of values
+    __shared__ __attribute__((aligned(16))) Word bias_s[BIAS ? 2 : 1][2][kStep];
+    __shared__ __attribute__((aligned(16))) float raw_s[BIAS && FAST ? 2 : 1][64];
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
-    const int split = idx % a.splits;
-    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, idx / a.splits, &seq, &tile, &tiles)) return;
+    const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
+    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, &seq, &tile, &tiles)) return;
     if (a.causal) tile = tiles - 1 - tile;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
-    Frag qf[NC][DP / KE], gf[NC][DP / KE];
-    int lim[NC];
-    float lse2[NC], delta[NC];
-    const int row0 = tile * TR + wave * 32 * NC;
+    const int r = tile * TR + wave * 32 + (lane & 31);
+    int token, g;
+    row_of(r, a.G, &token, &g);
+    const int64_t tok = sq.first + token;
+    const int head = hk * a.G + g;
+    const bool mine = r < rows;
+    const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
+    Frag qf[DP / KE], gf[DP / KE];
+    load_columns<T, DP, FAST>(gf, (const T*)a.go + tok * a.go_ts + (int64_t)head * a.go_hs, a.dv, mine, lane);
+    float delta = 0.0f;
+    const T* orow = (const T*)a.o + tok * a.o_ts + (int64_t)head * a.o_hs;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        int token, g;
-        const int r = row0 + 32 * n + (lane & 31);
-        const bool ok = r < rows;
-        row_of(r, a.G, &token, &g);
-        const int64_t tok = sq.first + token;
-        const int head = hk * a.G + g;
-        load_columns<T, DP, FAST>(qf[n], (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, ok, lane);
-        load_columns<T, DP, FAST>(gf[n], (const T*)a.go + tok * a.go_ts + (int64_t)head * a.go_hs, a.dv, ok, lane);
-        lim[n] = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
-        // rows that see nothing have no gradient: their l is -inf
-        const float lse = ok ? a.lse_in[tok * a.hq + head] : -kInf;
-        lse2[n] = lse == -kInf ? kInf : lse * kLog2e;
-        float d = 0.0f;
-        const T* orow = (const T*)a.o + tok * a.o_ts + (int64_t)head * a.o_hs;
+    for (int c = 0; c < DP / KE; ++c) {
+        const u32x4 ow = load_chunk<T, FAST>(orow, (2 * c + h) * L::EPC, a.dv, mine);
+        const u32x4 gw = __builtin_bit_cast(u32x4, gf[c]);
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) {
-            const u32x4 ow = load_chunk<T, FAST>(orow, (2 * c + h) * L::EPC, a.dv, ok);
-            const u32x4 gw = __builtin_bit_cast(u32x4, gf[n][c]);
+        for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d = fmaf(__uint_as_float(ow[i] << 16), __uint_as_float(gw[i] << 16), d);
-                    d = fmaf(__uint_as_float(ow[i] & 0xffff0000u), __uint_as_float(gw[i] & 0xffff0000u), d);
-                }
+                delta = fmaf(__uint_as_float(ow[i] << 16), __uint_as_float(gw[i] << 16), delta);
+                delta = fmaf(__uint_as_float(ow[i] & 0xffff0000u), __uint_as_float(gw[i] & 0xffff0000u), delta);
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d = fmaf(__uint_as_float(ow[i]), __uint_as_float(gw[i]), d);
+                delta = fmaf(__uint_as_float(ow[i]), __uint_as_float(gw[i]), delta);
             }
         }
-        delta[n] = half_sum(d);
-        if (split == 0 && h == 0 && ok) a.delta[tok * a.hq + head] = delta[n];
     }
+    delta = half_sum(delta);
+    if (split == 0 && h == 0 && mine) a.delta[tok * a.hq + head] = delta;
     if (!a.gq) return;   // only delta is wanted
-    int t_first, t_last, unused;
-    row_of(tile * TR, a.G, &t_first, &unused);
-    row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
-    const int most = a.causal ? min(max(t_last + ahead + 1, 0), lk) : lk;
-    const int least = a.causal ? min(max(t_first + ahead + 1, 0), lk) : lk;
+    load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, mine, lane);
+    // rows that see nothing have no gradient: their l is -inf
+    const float lse = mine ? a.lse_in[tok * a.hq + head] : -kInf;
+    const float lse2 = lse == -kInf ? kInf : lse * kLog2e;
+
+    int most = lk, least = lk;
+    if (a.causal) {
+        int t_first, t_last, unused;
+        row_of(tile * TR, a.G, &t_first, &unused);
+        row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
+        most = uniform(min(max(t_last + ahead + 1, 0), lk));
+        least = uniform(min(max(t_first + ahead + 1, 0), lk));
+    }
     const int all = (most + kStep - 1) / kStep;
-    const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+    int t0 = 0, t1 = all;
+    if (a.splits > 1) {
+        t0 = (int)((int64_t)all * split / a.splits);
+        t1 = (int)((int64_t)all * (split + 1) / a.splits);
+    }
+    const int n_steps = t1 - t0;
 
-    const T* K = (const T*)a.k + sk.first * a.k_ts + (int64_t)hk * a.k_hs;
-    const T* V = (const T*)a.v + sk.first * a.v_ts + (int64_t)hk * a.v_hs;
     const float* B = BIAS ? a.bias + sk.first : nullptr;
-    const float scale2 = a.scale * kLog2e;
-
-    floatx16 gq[NC][NT];
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int d = 0; d < NT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) gq[n][d][e] = 0.0f;
-
-    for (int t = t0; t < t1; ++t) {
-        const int k0 = t * kStep;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kStep * L::NCH / (64 * NW); ++i) {
-            const int id = tid + i * 64 * NW, row = id / L::NCH, c = id % L::NCH;
-            bool ok = k0 + row < lk;
-            if constexpr (BIAS) ok = ok && !(B[min(k0 + row, lk - 1)] < kLowest);
-            const int64_t key = k0 + row;
-            const u32x4 kw = load_chunk<T, FAST>(K + key * a.k_ts, c * L::EPC, a.dk, ok);
-            const u32x4 vw = load_chunk<T, FAST>(V + key * a.v_ts, c * L::EPC, a.dv, ok);
-            *(lds_u32x4*)(uintptr_t)(kbase + L::at(row, c)) = kw;
-            *(lds_u32x4*)(uintptr_t)(vbase + L::at(row, c)) = vw;
+    const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
+    typedef Copy<T, DP, kStep, FAST ? NW : 1> C;
+    C copy;
+    uint32_t koff[C::N], voff[C::N];
+    const T* knext = (const T*)a.k + (sk.first + (int64_t)t0 * kStep) * a.k_ts + (int64_t)hk * a.k_hs;
+    const T* vnext = (const T*)a.v + (sk.first + (int64_t)t0 * kStep) * a.v_ts + (int64_t)hk * a.v_hs;
+    // keys and values of step i; what lies at a key that is left out stays out
+    auto start = [&](int i, int stage, float b) {
+        const int k0 = (t0 + i) * kStep;
+        uint64_t out = from_bit(lk - k0);
+        if constexpr (BIAS) {
+            b = k0 + lane >= lk || b < kLowest ? -kInf : b * per_scale;
+            out |= __ballot(b == -kInf);
+            if (wave == 0 && lane < kStep) bias_s[stage & 1][0][lane] = Addend<T>::pack(b);
         }
-        if constexpr (BIAS)
-            if (tid < kStep) bias_s[tid] = k0 + tid < lk ? bias2(B[k0 + tid]) : -kInf;
-        __syncthreads();
-        const bool cut = k0 + kStep > least;
-#pragma unroll
-        for (int kt = 0; kt < kStep / 32; ++kt) {
-            floatx16 s[NC], dp[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[n][e] = dp[n][e] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < DP / KE; ++c) {
-                const Frag f = L::rows(kbase, 32 * kt, c, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) s[n] = Op<T>::mma(f, qf[n][c], s[n]);
+        const uint32_t kat = base + (uint32_t)stage * TB, vat = base + (uint32_t)(4 + (stage & 1)) * TB;
+        if constexpr (FAST) {
+            copy.start(knext, koff, kat, out, wave);
+            copy.start(vnext, voff, vat, out, wave);
+        } else {
+#pragma unroll 1
+            for (int id = tid; id < kStep * L::NCH; id += 64 * NW) {
+                const int row = id / L::NCH, c = id % L::NCH;
+                const bool ok = !((out >> row) & 1);
+                *(lds_u32x4*)(uintptr_t)(kat + L::at(row, c)) = load_chunk<T, FAST>(knext + row * a.k_ts, c * L::EPC, a.dk, ok);
+                *(lds_u32x4*)(uintptr_t)(vat + L::at(row, c)) = load_chunk<T, FAST>(vnext + row * a.v_ts, c * L::EPC, a.dv, ok);
             }
+        }
+        knext += kStep * a.k_ts;
+        vnext += kStep * a.v_ts;
+    };
+    auto bias_of = [&](int i) -> float {
+        const int key = (t0 + i) * kStep + lane;
+        return key < lk ? B[key] : 0.0f;
+    };
+    auto start_bias = [&](int i, int stage) {   // by the first wave
+        const int k0 = (t0 + i) * kStep;
+        copy4(buffer_of(B + k0), k0 + lane < lk ? (uint32_t)lane * 4u : kNowhere, (uint32_t)(uintptr_t)(lds_f32*)&raw_s[stage][0]);
+    };
+
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    typedef __attribute__((address_space(3))) Word lds_word;
+    const uint32_t bbase = (uint32_t)(uintptr_t)(lds_word*)&bias_s[0][h][lane & 31];
+    floatx16 gq[NT], s[2], dp[2];
+    Frag sf[2][KB];
 #pragma unroll
-            for (int c = 0; c < DP / KE; ++c) {
-                const Frag f = L::rows(vbase, 32 * kt, c, lane);
+    for (int d = 0; d < NT; ++d)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) dp[n] = Op<T>::mma(f, gf[n][c], dp[n]);
-            }
+        for (int e = 0; e < 16; ++e) gq[d][e] = 0.0f;
+
+    auto score = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        s[p] = dp[p] = floatx16{};
+        if constexpr (BIAS) s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * p * kStep)));
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
+        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), qf[c], s[p]);
 #pragma unroll
-                for (int e4 = 0; e4 < 4; ++e4) {
-                    const int key = 32 * kt + 8 * e4 + 4 * h;
-                    floatx4 b = {0, 0, 0, 0};
-                    if constexpr (BIAS) b = *(const lds_f32x4*)(uintptr_t)((uint32_t)(uintptr_t)(lds_f32*)&bias_s[0] + 4 * key);
+        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((4 + p) * TB, 0, c), gf[c], dp[p]);
+    };
+    auto collect = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[n][4 * e4 + e], scale2, b[e] - lse2[n]);
-                        if (cut && k0 + key + e >= lim[n]) x = -kInf;
-                        s[n][4 * e4 + e] = exp2_fast(x) * (dp[n][4 * e4 + e] - delta[n]);
-                    }
-                }
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                Frag sf[NC];
+            for (int d = 0; d < NT; ++d) gq[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[st & 1][b], gq[d]);
+    };
+    float raw = 0.0f;
+    auto step = [&](auto stage_c, int i) {
+        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        const int k0 = (t0 + i) * kStep;
+        all_arrived();   // step i + 1; all waves have left the keys of i - 2 and the values of i
+        if constexpr (BIAS && !FAST) raw = bias_of(i + 2);
+        start(i + 2, (st + 2) & 3, raw);
+        if constexpr (BIAS && FAST) {
+            if (wave == 0) start_bias(i + 4, p);
+            raw = raw_s[p ^ 1][lane];   // of step i + 3
+        }
+        if (k0 + kStep > least) {   // some row does not see all of it
+            const int room = lim - k0 - 4 * h;
 #pragma unroll
-                for (int n = 0; n < NC; ++n) sf[n] = Op<T>::from(s[n], b * KE / 2);
+            for (int e = 0; e < 16; ++e)
+                if (8 * (e / 4) + e % 4 >= room) s[p][e] = -kInf;
+        }
+        score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
+        collect(std::integral_constant<int, (st + 3) & 3>());
+        floatx16 ds;
 #pragma unroll
-                for (int d = 0; d < NT; ++d) {
-                    const Frag f = L::columns(kbase, 32 * kt + b * KE, d, lane);
+        for (int e = 0; e < 16; ++e) ds[e] = exp2_fast(fmaf(s[p][e], scale2, -lse2)) * (dp[p][e] - delta);
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) gq[n][d] = Op<T>::mma(f, sf[n], gq[n][d]);
-                }
-            }
+        for (int b = 0; b < KB; ++b) sf[p][b] = Op<T>::from(ds, b * KE / 2);
+        if constexpr (sizeof(T) == 2) mix<3 * DP / 16, 6, 2, 320 / DP, 128 / DP>();
+    };
+
+    if constexpr (FAST) {
+        copy.init(wave, lane);
+        copy.offsets(koff, a.k_ts, a.dk, lane);
+        copy.offsets(voff, a.v_ts, a.dv, lane);
+    }
+    if (n_steps > 0) {
+        float b[2] = {0.0f, 0.0f};
+        if constexpr (BIAS) {
+            b[0] = bias_of(0);
+            b[1] = bias_of(1);
+            raw = bias_of(2);
+        }
+        start(0, 0, b[0]);
+        start(1, 1, b[1]);
+        if constexpr (BIAS) {
+            if (FAST && wave == 0) start_bias(3, 1);
+            if (tid < 2 * kStep) bias_s[tid / kStep][1][tid % kStep] = Word{};
+        }
+        // no step before the first: zeros
+        for (int i = tid; i < TB / 16; i += 64 * NW)
+            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < KB; ++i) sf[1][i] = Frag{};
+        all_arrived();
+        score(std::integral_constant<int, 0>());
+        int i = 0;
+        for (;;) {
+            step(std::integral_constant<int, 0>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 1>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 2>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 3>(), i);
+            if (++i == n_steps) break;
+        }
+        all_arrived();
+        switch (n_steps & 3) {
+            case 0: collect(std::integral_constant<int, 3>()); break;
+            case 1: collect(std::integral_constant<int, 0>()); break;
+            case 2: collect(std::integral_constant<int, 1>()); break;
+            default: collect(std::integral_constant<int, 2>()); break;
         }
     }
 
+    if (!mine) return;
+    float* part = a.part + (((int64_t)split * a.total_q + tok) * a.hq + head) * a.dk;
+    T* out = (T*)a.gq + tok * a.gq_ts + (int64_t)head * a.gq_hs;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int r = row0 + 32 * n + (lane & 31);
-        if (r >= rows) continue;
-        int token, g;
-        row_of(r, a.G, &token, &g);
-        const int64_t tok = sq.first + token;
-        const int head = hk * a.G + g;
-        float* part = a.part + (((int64_t)split * a.total_q + tok) * a.hq + head) * a.dk;
-        T* out = (T*)a.gq + tok * a.gq_ts + (int64_t)head * a.gq_hs;
+    for (int d = 0; d < NT; ++d)
 #pragma unroll
-        for (int d = 0; d < NT; ++d)
+        for (int e4 = 0; e4 < 4; ++e4) {
+            float v[4];
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = gq[n][d][4 * e4 + e] * a.scale;
-                if (a.splits > 1) store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dk, v);
-                else store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dk, v);
-            }
-    }
+            for (int e = 0; e < 4; ++e) v[e] = gq[d][4 * e4 + e] * a.scale;
+            if (a.splits > 1) store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dk, v);
+            else store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dk, v);
+        }
 }
 
-// A workgroup has 32 NC keys a wave and walks over the rows of all heads that
-// read its key head.
-template <typename T, int DP, int NW, int NC, bool FAST>
-__global__ __launch_bounds__(64 * NW) void attn_bwd_kv(AttnArgs a) {
+// A workgroup has 32 keys a wave and walks over the rows of all heads that read
+// its key head, in steps of 32.  Three steps are under way in a wave, as above: the
+// scores and dp of step i + 1, the weights of step i, the gradients' parts of
+// step i - 1.  -l and -delta of a row are the first summands of its scores and dp.
+template <typename T, int DP, int NW, bool FAST>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1) void attn_bwd_kv(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
-    constexpr int KE = Op<T>::KE, NT = DP / 32, TK = 32 * NC * NW, KB = 32 / KE;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStep * L::RB];
-    __shared__ __attribute__((aligned(16))) float lse_s[kStep], delta_s[kStep];
-    __shared__ __attribute__((aligned(16))) int32_t lim_s[kStep];
-    const uint32_t qbase = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
-    const uint32_t gbase = qbase + kStep * L::RB;
+    typedef typename Addend<T>::Word Word;
+    constexpr int KE = Op<T>::KE, NT = DP / 32, TK = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * TB];   // four stages of queries, of gradients
+    // [stage][-l, -delta][values, zeros for the upper half of the lanes][row]
+    __shared__ __attribute__((aligned(16))) Word add_s[2][2][2][kStep];
+    __shared__ __attribute__((aligned(16))) float raw_s[2][2][64];
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
-    const int split = idx % a.splits;
-    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, idx / a.splits, &seq, &tile, &tiles)) return;
+    const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
+    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, slot, &seq, &tile, &tiles)) return;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
-    Frag kf[NC][DP / KE], vf[NC][DP / KE];
-    float bias[NC];
-    const int key0 = tile * TK + wave * 32 * NC;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int key = key0 + 32 * n + (lane & 31);
-        bool ok = key < lk;
-        const int64_t tok = sk.first + key;
-        bias[n] = 0.0f;
-        if (a.bias && ok) bias[n] = bias2(a.bias[tok]);
-        ok = ok && bias[n] != -kInf;
-        if (!ok) bias[n] = -kInf;
-        load_columns<T, DP, FAST>(kf[n], (const T*)a.k + tok * a.k_ts + (int64_t)hk * a.k_hs, a.dk, ok, lane);
-        load_columns<T, DP, FAST>(vf[n], (const T*)a.v + tok * a.v_ts + (int64_t)hk * a.v_hs, a.dv, ok, lane);
+    const int key0 = tile * TK + wave * 32, key = key0 + (lane & 31);
+    const int64_t tok = sk.first + key;
+    Frag kf[DP / KE], vf[DP / KE];
+    bool seen = key < lk;
+    float bias = 0.0f;
+    if (a.bias && seen) bias = bias2(a.bias[tok]);
+    seen = seen && bias != -kInf;
+    if (!seen) bias = -kInf;
+    load_columns<T, DP, FAST>(kf, (const T*)a.k + tok * a.k_ts + (int64_t)hk * a.k_hs, a.dk, seen, lane);
+    load_columns<T, DP, FAST>(vf, (const T*)a.v + tok * a.v_ts + (int64_t)hk * a.v_hs, a.dv, seen, lane);
+    // the first row that sees the tile's first key, the first that sees this lane's key,
+    // and the row from which on all of this wave's are seen
+    int r_first = 0, r_mine = 0, r_all = 0;
+    if (a.causal) {
+        r_first = uniform(min(max(tile * TK - ahead, 0), sq.len) * a.G);
+        r_mine = min(max(key - ahead, 0), sq.len) * a.G;
+        r_all = uniform(min(max(min(key0 + 31, lk - 1) - ahead, 0), sq.len) * a.G);
     }
-    // the first row that sees the tile's first key, and the rows from which all see all of it
-    const int r_first = a.causal ? min(max(tile * TK - ahead, 0), sq.len) * a.G : 0;
-    const int r_all = a.causal ? min(max(min(tile * TK + TK, lk) - 1 - ahead, 0), sq.len) * a.G : 0;
     const int b0 = r_first / kStep, all = (rows + kStep - 1) / kStep - b0;
-    const int t0 = b0 + (int)((int64_t)all * split / a.splits), t1 = b0 + (int)((int64_t)all * (split + 1) / a.splits);
-    const float scale2 = a.scale * kLog2e;
+    int t0 = b0, t1 = b0 + all;
+    if (a.splits > 1) {
+        t0 = b0 + (int)((int64_t)all * split / a.splits);
+        t1 = b0 + (int)((int64_t)all * (split + 1) / a.splits);
+    }
+    const int n_steps = t1 - t0;
+    const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
 
-    floatx16 gk[NC][NT], gv[NC][NT];
+    // Row x from a step's first token on is head x % G of token x / G: x is small,
+    // so that a float32 product divides it.
+    typedef Copy<T, DP, kStep, FAST ? NW : 1> C;
+    C copy;
+    copy.init(wave, lane);
+    const float per_g = 1.0f / (float)a.G;
+    auto split_row = [&](int x, int* t, int* gg) {
+        *t = a.G == 1 ? x : (int)(((float)x + 0.5f) * per_g);
+        *gg = x - *t * a.G;
+    };
+    const T* Q = (const T*)a.q + sq.first * a.q_ts + (int64_t)hk * a.G * a.q_hs;
+    const T* O = (const T*)a.go + sq.first * a.go_ts + (int64_t)hk * a.G * a.go_hs;
+    const int64_t cell0 = sq.first * a.hq + (int64_t)hk * a.G;
+    auto first_of = [&](int i, int* token) -> int {   // of step i: its first token, rows past that token's first head
+        const int r0 = (t0 + i) * kStep;
+        *token = a.G == 1 ? r0 : r0 / a.G;
+        return r0 - *token * a.G;
+    };
+    auto start = [&](int i, int stage) {
+        int token;
+        const int x0 = first_of(i, &token), r0 = (t0 + i) * kStep;
+        const T *q = Q + (int64_t)token * a.q_ts, *o = O + (int64_t)token * a.go_ts;
+        const uint32_t qat = base + (uint32_t)stage * TB, oat = base + (uint32_t)(4 + stage) * TB;
+        if constexpr (FAST) {
+            if (!C::shares(wave)) return;
+            const u32x4 qb = buffer_of(q), ob = buffer_of(o);
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int d = 0; d < NT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) gk[n][d][e] = gv[n][d][e] = 0.0f;
+            for (int j = 0; j < C::N; ++j) {
+                const int row = copy.row + j * (kStep / C::N), src = ((lane % L::NCH) ^ L::turn(row)) * L::EPC;
+                int t, gg;
+                split_row(x0 + row, &t, &gg);
+                const bool ok = r0 + row < rows;
+                const uint32_t qo = ((uint32_t)t * (uint32_t)a.q_ts + (uint32_t)gg * (uint32_t)a.q_hs + src) * (uint32_t)sizeof(T);
+                const uint32_t oo = ((uint32_t)t * (uint32_t)a.go_ts + (uint32_t)gg * (uint32_t)a.go_hs + src) * (uint32_t)sizeof(T);
+                const uint32_t at = (uint32_t)(j * NW + wave) * 1024u;
+                copy16(qb, ok && src < a.dk ? qo : kNowhere, qat + at);
+                copy16(ob, ok && src < a.dv ? oo : kNowhere, oat + at);
+            }
+        } else {
+#pragma unroll 1
+            for (int id = tid; id < kStep * L::NCH; id += 64 * NW) {
+                const int row = id / L::NCH, c = id % L::NCH;
+                int t, gg;
+                split_row(x0 + row, &t, &gg);
+                const bool ok = r0 + row < rows;
+                *(lds_u32x4*)(uintptr_t)(qat + L::at(row, c)) =
+                    load_chunk<T, FAST>(q + t * a.q_ts + gg * a.q_hs, c * L::EPC, a.dk, ok);
+                *(lds_u32x4*)(uintptr_t)(oat + L::at(row, c)) =
+                    load_chunk<T, FAST>(o + t * a.go_ts + gg * a.go_hs, c * L::EPC, a.dv, ok);
+            }
+        }
+    };
+    // l of a row (lanes 0 .. 31) and delta (lanes 32 .. 63) of step i
+    const int row = lane & 31;
+    auto raw_of = [&](int i) -> float {
+        int token, t, gg;
+        const int x0 = first_of(i, &token);
+        split_row(x0 + row, &t, &gg);
+        if ((t0 + i) * kStep + row >= rows) return 0.0f;
+        const int64_t cell = cell0 + (int64_t)(token + t) * a.hq + gg;
+        return h == 0 ? a.lse_in[cell] : a.delta[cell];
+    };
+    auto start_raw = [&](int i, int stage) {   // by the first two waves
+        int token, t, gg;
+        const int x0 = first_of(i, &token);
+        split_row(x0 + row, &t, &gg);
+        const bool ok = h == 0 && (t0 + i) * kStep + row < rows;
+        const float* p = (wave == 0 ? a.lse_in : a.delta) + cell0 + (int64_t)token * a.hq;
+        copy4(buffer_of(p), ok ? (uint32_t)(t * a.hq + gg) * 4u : kNowhere, (uint32_t)(uintptr_t)(lds_f32*)&raw_s[stage][wave][0]);
+    };
+    auto put = [&](int i, int stage, float v) {   // by the first wave
+        const bool ok = (t0 + i) * kStep + row < rows;
+        if (h == 0) v = !ok || v == -kInf ? -kInf : -v * per_scale;   // rows that see nothing weigh nothing
+        else v = ok ? -v : 0.0f;
+        add_s[stage][h][0][row] = Addend<T>::pack(v);
+    };
 
-    for (int t = t0; t < t1; ++t) {
-        const int r0 = t * kStep;
-        __syncthreads();
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    typedef __attribute__((address_space(3))) Word lds_word;
+    const uint32_t abase = (uint32_t)(uintptr_t)(lds_word*)&add_s[0][0][h][row];
+    constexpr uint32_t kAdd = (uint32_t)sizeof(Word) * 2 * kStep;
+    floatx16 gk[NT], gv[NT], s[2], dp[2];
+    Frag pf[2][KB], sf[2][KB];
 #pragma unroll
-        for (int i = 0; i < kStep * L::NCH / (64 * NW); ++i) {
-            const int id = tid + i * 64 * NW, row = id / L::NCH, c = id % L::NCH;
-            int token, g;
-            row_of(r0 + row, a.G, &token, &g);
-            const int64_t tok = sq.first + token, head = hk * a.G + g;
-            const bool ok = r0 + row < rows;
-            const u32x4 qw = load_chunk<T, FAST>((const T*)a.q + tok * a.q_ts + head * a.q_hs, c * L::EPC, a.dk, ok);
-            const u32x4 gw = load_chunk<T, FAST>((const T*)a.go + tok * a.go_ts + head * a.go_hs, c * L::EPC, a.dv, ok);
-            *(lds_u32x4*)(uintptr_t)(qbase + L::at(row, c)) = qw;
-            *(lds_u32x4*)(uintptr_t)(gbase + L::at(row, c)) = gw;
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gk[d][e] = gv[d][e] = 0.0f;
+
+    auto score = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p)));
+        dp[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p + 1)));
+#pragma unroll
+        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), kf[c], s[p]);
+#pragma unroll
+        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((4 + st) * TB, 0, c), vf[c], dp[p]);
+    };
+    auto collect = [&](auto stage_c) {
+        constexpr int st = decltype(stage_c)::value, p = st & 1;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int d = 0; d < NT; ++d) {
+                gv[d] = Op<T>::mma(rd.columns((4 + st) * TB, b, d), pf[p][b], gv[d]);
+                gk[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[p][b], gk[d]);
+            }
+    };
+    float raw = 0.0f;
+    auto step = [&](auto stage_c, int i) {
+        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        const int r0 = (t0 + i) * kStep;
+        all_arrived();   // step i + 1; all waves have left step i - 2
+        start(i + 2, (st + 2) & 3);
+        if constexpr (!FAST) raw = raw_of(i + 2);
+        if (wave == 0) put(i + 2, p, raw);
+        if constexpr (FAST) {
+            if (wave < 2) start_raw(i + 4, p);
+            raw = raw_s[p ^ 1][h][row];   // of step i + 3
         }
-        if (tid < kStep) {
-            int token, g;
-            row_of(r0 + tid, a.G, &token, &g);
-            const bool ok = r0 + tid < rows;
-            const int64_t cell = (sq.first + token) * a.hq + hk * a.G + g;
-            const float lse = ok ? a.lse_in[cell] : -kInf;
-            lse_s[tid] = lse == -kInf ? kInf : lse * kLog2e;
-            delta_s[tid] = ok ? a.delta[cell] : 0.0f;
-            lim_s[tid] = a.causal ? token + ahead : 0x7fffffff;
+        if (r0 < r_all) {   // some row does not see all keys of this wave
+            const int hidden = r_mine - r0 - 4 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (8 * (e / 4) + e % 4 < hidden) s[p][e] = -kInf;
         }
-        __syncthreads();
-        const bool cut = r0 < r_all;
+        score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
+        collect(std::integral_constant<int, (st + 3) & 3>());
+        floatx16 w, ds;
 #pragma unroll
-        for (int rt = 0; rt < kStep / 32; ++rt) {
-            floatx16 s[NC], dp[NC];
+        for (int e = 0; e < 16; ++e) {
+            w[e] = exp2_fast(fmaf(s[p][e], scale2, bias));
+            ds[e] = w[e] * dp[p][e];
+        }
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
+        for (int b = 0; b < KB; ++b) {
+            pf[p][b] = Op<T>::from(w, b * KE / 2);
+            sf[p][b] = Op<T>::from(ds, b * KE / 2);
+        }
+        if constexpr (sizeof(T) == 2) mix<2 + DP / 4, 8, 2, DP <= 64 ? 3 : 2, 1>();
+    };
+
+    if (n_steps > 0) {
+        const float a0 = raw_of(0), a1 = raw_of(1);
+        raw = raw_of(2);
+        start(0, 0);
+        start(1, 1);
+        if (wave == 0) {
+            put(0, 0, a0);
+            put(1, 1, a1);
+        }
+        if constexpr (FAST)
+            if (wave < 2) start_raw(3, 1);
+        if (tid < 4 * kStep) add_s[tid >> 6][(tid >> 5) & 1][1][tid & 31] = Word{};
+        // no step before the first: zeros
+        for (int i = tid; i < TB / 16; i += 64 * NW) {
+            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+            *(lds_u32x4*)(uintptr_t)(base + 7 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[n][e] = dp[n][e] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < DP / KE; ++c) {
-                const Frag f = L::rows(qbase, 32 * rt, c, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) s[n] = Op<T>::mma(f, kf[n][c], s[n]);
-            }
-#pragma unroll
-            for (int c = 0; c < DP / KE; ++c) {
-                const Frag f = L::rows(gbase, 32 * rt, c, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) dp[n] = Op<T>::mma(f, vf[n][c], dp[n]);
-            }
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                const int row = 32 * rt + 8 * e4 + 4 * h;
-                const floatx4 l4 = *(const lds_f32x4*)(uintptr_t)((uint32_t)(uintptr_t)(lds_f32*)&lse_s[0] + 4 * row);
-                const floatx4 d4 = *(const lds_f32x4*)(uintptr_t)((uint32_t)(uintptr_t)(lds_f32*)&delta_s[0] + 4 * row);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    const int key = key0 + 32 * n + (lane & 31);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[n][4 * e4 + e], scale2, bias[n] - l4[e]);
-                        if (cut && key > lim_s[row + e]) x = -kInf;
-                        const float p = exp2_fast(x);
-                        s[n][4 * e4 + e] = p;
-                        dp[n][4 * e4 + e] = p * (dp[n][4 * e4 + e] - d4[e]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                Frag pf[NC], sf[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    pf[n] = Op<T>::from(s[n], b * KE / 2);
-                    sf[n] = Op<T>::from(dp[n], b * KE / 2);
-                }
-#pragma unroll
-                for (int d = 0; d < NT; ++d) {
-                    const Frag f = L::columns(gbase, 32 * rt + b * KE, d, lane);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) gv[n][d] = Op<T>::mma(f, pf[n], gv[n][d]);
-                    const Frag e = L::columns(qbase, 32 * rt + b * KE, d, lane);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) gk[n][d] = Op<T>::mma(e, sf[n], gk[n][d]);
-                }
-            }
+        for (int i = 0; i < KB; ++i) pf[1][i] = sf[1][i] = Frag{};
+        all_arrived();
+        score(std::integral_constant<int, 0>());
+        int i = 0;
+        for (;;) {
+            step(std::integral_constant<int, 0>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 1>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 2>(), i);
+            if (++i == n_steps) break;
+            step(std::integral_constant<int, 3>(), i);
+            if (++i == n_steps) break;
+        }
+        all_arrived();
+        switch (n_steps & 3) {
+            case 0: collect(std::integral_constant<int, 3>()); break;
+            case 1: collect(std::integral_constant<int, 0>()); break;
+            case 2: collect(std::integral_constant<int, 1>()); break;
+            default: collect(std::integral_constant<int, 2>()); break;
         }
     }
 
+    if (key >= lk) return;
+    const int64_t cell = ((int64_t)split * a.total_k + tok) * a.hkv + hk;
+    float *pk = a.part + cell * a.dk, *pv = a.part2 + cell * a.dv;
+    T* ok = (T*)a.gk + tok * a.gk_ts + (int64_t)hk * a.gk_hs;
+    T* ov = (T*)a.gv + tok * a.gv_ts + (int64_t)hk * a.gv_hs;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int key = key0 + 32 * n + (lane & 31);
-        if (key >= lk) continue;
-        const int64_t tok = sk.first + key;
-        const int64_t cell = ((int64_t)split * a.total_k + tok) * a.hkv + hk;
-        float* pk = a.part + cell * a.dk;
-        float* pv = a.part2 + cell * a.dv;
-        T* ok = (T*)a.gk + tok * a.gk_ts + (int64_t)hk * a.gk_hs;
-        T* ov = (T*)a.gv + tok * a.gv_ts + (int64_t)hk * a.gv_hs;
+    for (int d = 0; d < NT; ++d)
 #pragma unroll
-        for (int d = 0; d < NT; ++d)
+        for (int e4 = 0; e4 < 4; ++e4) {
+            const int d0 = 32 * d + 8 * e4 + 4 * h;
+            float x[4], y[4];
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                const int d0 = 32 * d + 8 * e4 + 4 * h;
-                float x[4], y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = gk[n][d][4 * e4 + e] * a.scale;
-                    y[e] = gv[n][d][4 * e4 + e];
-                }
-                if (a.splits > 1) {
-                    store4<float, FAST>(pk, d0, a.dk, x);
-                    store4<float, FAST>(pv, d0, a.dv, y);
-                } else {
-                    store4<T, FAST>(ok, d0, a.dk, x);
-                    store4<T, FAST>(ov, d0, a.dv, y);
-                }
+            for (int e = 0; e < 4; ++e) {
+                x[e] = gk[d][4 * e4 + e] * a.scale;
+                y[e] = gv[d][4 * e4 + e];
             }
-    }
+            if (a.splits > 1) {
+                store4<float, FAST>(pk, d0, a.dk, x);
+                store4<float, FAST>(pv, d0, a.dv, y);
+            } else {
+                store4<T, FAST>(ok, d0, a.dk, x);
+                store4<T, FAST>(ov, d0, a.dv, y);
+            }
+        }
 }
 
 // Sum of the parts of [tokens, heads, d], a wave a row; tokens of no sequence
@@ -389,8 +542,8 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
     if (a.total_q > 0) {   // delta, which gk and gv need too
         KernelTimer timer("attn_bwd_q", st);
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
-        if (a.bias) attn_bwd_q<T, DP, NW, 1, true, FAST><<<grid, 64 * NW, 0, st>>>(a);
-        else attn_bwd_q<T, DP, NW, 1, false, FAST><<<grid, 64 * NW, 0, st>>>(a);
+        if (a.bias) attn_bwd_q<T, DP, NW, true, FAST><<<grid, 64 * NW, 0, st>>>(a);
+        else attn_bwd_q<T, DP, NW, false, FAST><<<grid, 64 * NW, 0, st>>>(a);
     }
     if (a.splits > 1)
         sum_parts<T>(a.part, a.gq, a.gq_ts, a.gq_hs, a.total_q, a.hq, a.dk, a.splits, a.cu_q, a.n_seq, st);
@@ -401,7 +554,7 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
         {
             KernelTimer timer("attn_bwd_kv", st);
-            attn_bwd_kv<T, DP, NW, 1, FAST><<<grid, 64 * NW, 0, st>>>(a);
+            attn_bwd_kv<T, DP, NW, FAST><<<grid, 64 * NW, 0, st>>>(a);
         }
         if (a.splits > 1) {
             sum_parts<T>(a.part, a.gk, a.gk_ts, a.gk_hs, a.total_k, a.hkv, a.dk, a.splits, a.cu_k, a.n_seq, st);
