@@ -35,22 +35,51 @@ bool wide(const AttnArgs& a) {
     return true;
 }
 
-// Parts of a walk of `steps` steps so that `tiles` workgroups become about `want`,
-// each with `least` steps at least
-int parts(int64_t tiles, int64_t steps, int64_t want, int64_t least) {
-    if (tiles <= 0 || tiles >= want / 2) return 1;
-    return (int)std::max<int64_t>(1, std::min({want / tiles, steps / least, (int64_t)256}));
+// Parts of the axis that a workgroup walks over.  `tiles` workgroups of `steps`
+// steps of `us` each run `at_once` at a time; parts cost the writing and reading of
+// their float32 results, `bytes` a part, and a launch.  Sequences of a packed call
+// may be of any lengths: one of up to four times the mean is counted on, and its
+// last workgroup ends the call.
+// Gradient of 65 x 128 points, 8 heads of 64: 520 workgroups, 512 at once: one part
+// 447 us (gk, gv) and 324 us (gq), four 345 and 262, joined in 18 us.
+int parts(int64_t n_seq, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 256; ++s) {
+        if (s > 1 && steps / s < 4.0) break;
+        const double rounds = (double)ceil_div(tiles * s, at_once);
+        double t = rounds * (steps / s + 4.0);
+        if (n_seq > 1) t = std::max(t, 4.0 * steps / s + 4.0);
+        t = t * us + (s > 1 ? 8.0 + s * bytes / 2.5e6 : 0.0);
+        if (s == 1 || t < 0.95 * least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
 }
+
+struct Mean {   // of a sequence
+    int64_t rows, keys;
+};
+Mean mean_of(const AttnArgs& a) { return {ceil_div(a.total_q, a.n_seq) * a.G, ceil_div(a.total_k, a.n_seq)}; }
+// float32 products take up to sixteen times as long, at a quarter of the waves' number
+double slower(const AttnArgs& a) { return (a.dtype == DISCO_F32 ? 3.0 : 1.0) * (std::max(a.dk, a.dv) > 64 ? 1.5 : 1.0); }
 
 }  // namespace
 
 AttnPlan attn_plan_fwd(const AttnArgs& a) {
     AttnPlan p{};
     p.fast = wide(a);
-    const int64_t rows = ceil_div(a.total_q, a.n_seq) * a.G, keys = ceil_div(a.total_k, a.n_seq);
-    p.waves = !p.fast || rows > 64 ? 4 : rows > 32 ? 2 : 1;
-    const int64_t tiles = a.n_seq * ceil_div(rows, 32 * p.waves) * a.hkv;
-    p.splits = parts(tiles, ceil_div(keys, 64), 512, 2);
+    const Mean m = mean_of(a);
+    p.waves = !p.fast || m.rows > 64 ? 4 : m.rows > 32 ? 2 : 1;
+    const int64_t tiles = a.n_seq * ceil_div(m.rows, 32 * p.waves) * a.hkv;
+    // more rows than that fill the chip: 129 x 256 points in two parts were no faster
+    if (tiles < 256)
+        p.splits = parts(a.n_seq, tiles, (double)ceil_div(m.keys, 32) * (a.causal ? 0.5 : 1.0), 0.4 * slower(a), 512,
+                         4.0 * a.total_q * a.hq * a.dv);
+    else
+        p.splits = 1;
     return p;
 }
 
@@ -58,8 +87,9 @@ AttnPlan attn_plan_bwd_q(const AttnArgs& a) {
     AttnPlan p{};
     p.fast = wide(a);
     p.waves = 4;
-    const int64_t rows = ceil_div(a.total_q, a.n_seq) * a.G, keys = ceil_div(a.total_k, a.n_seq);
-    p.splits = parts(a.n_seq * ceil_div(rows, 128) * a.hkv, ceil_div(keys, 64), 512, 4);
+    const Mean m = mean_of(a);
+    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.rows, 128) * a.hkv, (double)ceil_div(m.keys, 32) * (a.causal ? 0.5 : 1.0),
+                     0.6 * slower(a), a.dtype == DISCO_F32 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
     return p;
 }
 
@@ -67,8 +97,10 @@ AttnPlan attn_plan_bwd_kv(const AttnArgs& a) {
     AttnPlan p{};
     p.fast = wide(a);
     p.waves = 4;
-    const int64_t rows = ceil_div(a.total_q, a.n_seq) * a.G, keys = ceil_div(a.total_k, a.n_seq);
-    p.splits = parts(a.n_seq * ceil_div(keys, 128) * a.hkv, ceil_div(rows, 64), 512, 4);
+    const Mean m = mean_of(a);
+    const bool one = a.dtype == DISCO_F32 || std::max(a.dk, a.dv) > 64;   // workgroup of a compute unit
+    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.keys, 128) * a.hkv, (double)ceil_div(m.rows, 32) * (a.causal ? 0.5 : 1.0),
+                     0.86 * slower(a) / (one ? 1.5 : 1.0), one ? 256 : 512, 4.0 * a.total_k * a.hkv * (a.dk + a.dv));
     return p;
 }
 

@@ -278,8 +278,38 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 
 constexpr int kMostSplits = 256, kJoinWaves = 16;
 
-// Joins the parts of each row: a workgroup a row, its waves share the parts.
+// Joins the parts of each row:
 //   l = log sum_s exp l_s,  o = sum_s exp(l_s - l) o_s
+// A wave a row, where the parts are few
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_few(AttnArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t cell = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tok = cell / a.hq;
+    const int head = (int)(cell - tok * a.hq);
+    // tokens before the first and behind the last sequence stay as they are
+    if (tok >= a.total_q || (a.cu_q && (tok < a.cu_q[0] || tok >= a.cu_q[a.n_seq]))) return;
+    const int64_t stride = a.total_q * a.hq;
+    float mx = -kInf, sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
+    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, a.part_lse[s * stride + cell]);
+    const float use = mx == -kInf ? 0.0f : mx;
+    const int d0 = min(lane, a.dv - 1), d1 = min(lane + 64, a.dv - 1);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float w = exp2_fast((a.part_lse[s * stride + cell] - use) * kLog2e);
+        const float* q = a.part + (s * stride + cell) * a.dv;
+        sum += w;
+        v0 = fmaf(w, q[d0], v0);
+        v1 = fmaf(w, q[d1], v1);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (a.lse && lane == 0) a.lse[cell] = sum == 0.0f ? -kInf : use + logf(sum);
+    T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
+    if (lane < a.dv) store_f(out, lane, v0 * inv);
+    if (lane + 64 < a.dv) store_f(out, lane + 64, v1 * inv);
+}
+
+// A workgroup a row, its waves share the parts (8 points over 33024 keys, 128 rows
+// of 128 parts: 10 us, a wave a row 120)
 template <typename T>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join(AttnArgs a) {
     constexpr int P = kMostSplits / 64;
@@ -341,7 +371,8 @@ int fwd_go(AttnArgs a, hipStream_t st) {
     }
     if (a.splits > 1) {
         KernelTimer timer("attn_join", st);
-        attn_join<T><<<(unsigned)(a.total_q * a.hq), 64 * kJoinWaves, 0, st>>>(a);
+        if (a.splits <= 8) attn_join_few<T><<<(unsigned)((a.total_q * a.hq + 3) / 4), 256, 0, st>>>(a);
+        else attn_join<T><<<(unsigned)(a.total_q * a.hq), 64 * kJoinWaves, 0, st>>>(a);
     }
     return attn_launched("attention_fwd");
 }

@@ -185,7 +185,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
         for (int e = 0; e < 16; ++e) ds[e] = exp2_fast(fmaf(s[p][e], scale2, -lse2)) * (dp[p][e] - delta);
 #pragma unroll
         for (int b = 0; b < KB; ++b) sf[p][b] = Op<T>::from(ds, b * KE / 2);
-        if constexpr (sizeof(T) == 2) mix<3 * DP / 16, 6, 2, 320 / DP, 128 / DP>();
     };
 
     if constexpr (FAST) {
@@ -439,7 +438,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
             pf[p][b] = Op<T>::from(w, b * KE / 2);
             sf[p][b] = Op<T>::from(ds, b * KE / 2);
         }
-        if constexpr (sizeof(T) == 2) mix<2 + DP / 4, 8, 2, DP <= 64 ? 3 : 2, 1>();
     };
 
     if (n_steps > 0) {
@@ -509,29 +507,39 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         }
 }
 
-// Sum of the parts of [tokens, heads, d], a wave a row; tokens of no sequence
-// stay as they are.
+// Sums of the parts of one or two tensors [tokens, heads, d], a wave a row; tokens
+// of no sequence stay as they are.
+struct Parts {
+    const float* part;
+    void* out;
+    int64_t ts, hs;
+    int d;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void attn_sum(const float* __restrict__ part, T* __restrict__ out, int64_t ts, int64_t hs,
-                                                int64_t total, int heads, int d, int splits, const int32_t* cu, int n_seq) {
+__global__ __launch_bounds__(256) void attn_sum(Parts a, Parts b, int64_t total, int heads, int splits, const int32_t* cu,
+                                                int n_seq) {
     const int lane = threadIdx.x & 63;
-    const int64_t cell = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t tok = cell / heads;
+    const int64_t cell = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tok = cell / heads;
     const int head = (int)(cell - tok * heads);
-    if (tok >= total) return;
-    if (cu && (tok < cu[0] || tok >= cu[n_seq])) return;
-    for (int i = lane; i < d; i += 64) {
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s) v += part[(s * total * heads + cell) * d + i];
-        store_f(out + tok * ts + (int64_t)head * hs, i, v);
+    if (tok >= total || (cu && (tok < cu[0] || tok >= cu[n_seq]))) return;
+    for (int k = 0; k < 2; ++k) {
+        const Parts& p = k == 0 ? a : b;
+        T* out = (T*)p.out + tok * p.ts + (int64_t)head * p.hs;
+        for (int i = lane; i < p.d; i += 64) {
+            float v = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) v += p.part[(s * total * heads + cell) * p.d + i];
+            store_f(out, i, v);
+        }
     }
 }
 
 template <typename T>
-void sum_parts(const float* part, void* out, int64_t ts, int64_t hs, int64_t total, int heads, int d, int splits,
-               const int32_t* cu, int n_seq, hipStream_t st) {
+void sum_parts(const Parts& x, const Parts& y, int64_t total, int heads, int splits, const int32_t* cu, int n_seq,
+               hipStream_t st) {
     KernelTimer timer("attn_sum", st);
-    attn_sum<T><<<(unsigned)((total * heads + 3) / 4), 256, 0, st>>>(part, (T*)out, ts, hs, total, heads, d, splits, cu, n_seq);
+    attn_sum<T><<<(unsigned)((total * heads + 3) / 4), 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
 }
 
 template <typename T, int DP, bool FAST>
@@ -546,7 +554,7 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
         else attn_bwd_q<T, DP, NW, false, FAST><<<grid, 64 * NW, 0, st>>>(a);
     }
     if (a.splits > 1)
-        sum_parts<T>(a.part, a.gq, a.gq_ts, a.gq_hs, a.total_q, a.hq, a.dk, a.splits, a.cu_q, a.n_seq, st);
+        sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);
     if (a.gk && a.total_k > 0) {
         a.slots = (int)tile_slots(a.cu_k != nullptr, a.total_k, a.n_seq, 1, 32 * NW);
         a.splits = pk.splits;
@@ -556,10 +564,9 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
             KernelTimer timer("attn_bwd_kv", st);
             attn_bwd_kv<T, DP, NW, FAST><<<grid, 64 * NW, 0, st>>>(a);
         }
-        if (a.splits > 1) {
-            sum_parts<T>(a.part, a.gk, a.gk_ts, a.gk_hs, a.total_k, a.hkv, a.dk, a.splits, a.cu_k, a.n_seq, st);
-            sum_parts<T>(a.part2, a.gv, a.gv_ts, a.gv_hs, a.total_k, a.hkv, a.dv, a.splits, a.cu_k, a.n_seq, st);
-        }
+        if (a.splits > 1)
+            sum_parts<T>({a.part, a.gk, a.gk_ts, a.gk_hs, a.dk}, {a.part2, a.gv, a.gv_ts, a.gv_hs, a.dv}, a.total_k, a.hkv,
+                         a.splits, a.cu_k, a.n_seq, st);
     }
     return attn_launched("attention_bwd");
 }
