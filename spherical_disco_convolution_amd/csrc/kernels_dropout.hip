@@ -14,7 +14,7 @@
 #include <algorithm>
 
 #include "disco_internal.h"
-#include "kernels_common.h"
+#include "vector_io.h"
 
 namespace disco {
 
@@ -39,23 +39,6 @@ __device__ __forceinline__ Words philox(uint64_t block, uint64_t offset, uint32_
     return {{c0, c1, c2, c3}};
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[8]; };
-    const U u = *reinterpret_cast<const U*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = load_f(u.e, i);
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* f) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[8]; };
-    U u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) store_f(u.e, i, f[i]);
-    *reinterpret_cast<U*>(p) = u;
-}
-
 template <typename TX, typename TY, bool RES>
 __global__ __launch_bounds__(256) void dropout(const TX* x, const TX* res, TY* y, int64_t n, uint32_t threshold, float scale,
                                                uint64_t seed, uint64_t offset, const int64_t* step) {
@@ -65,8 +48,8 @@ __global__ __launch_bounds__(256) void dropout(const TX* x, const TX* res, TY* y
     const Words r = philox((uint64_t)block, offset, (uint32_t)seed, (uint32_t)(seed >> 32));
     float f[8], q[8];
     if (e0 + 8 <= n) {
-        load8(x + e0, f);
-        if constexpr (RES) load8(res + e0, q);
+        load_v<TX, 8>(x + e0, f);
+        if constexpr (RES) load_v<TX, 8>(res + e0, q);
     } else {
         for (int i = 0; i < 8; ++i) {
             f[i] = e0 + i < n ? load_f(x, e0 + i) : 0.0f;
@@ -80,7 +63,7 @@ __global__ __launch_bounds__(256) void dropout(const TX* x, const TX* res, TY* y
         if constexpr (RES) f[i] += q[i];
     }
     if (e0 + 8 <= n) {
-        store8(y + e0, f);
+        store_v<TY, 8>(y + e0, f);
     } else {
         for (int i = 0; i < 8; ++i)
             if (e0 + i < n) store_f(y, e0 + i, f[i]);

@@ -15,32 +15,15 @@
 #include <algorithm>
 
 #include "disco_internal.h"
-#include "kernels_common.h"
+#include "vector_io.h"
 
 namespace disco {
 
 namespace {
 
+#define QV 8
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 1024;    // workgroups of the gradient, and rows of partial sums
-
-// V consecutive elements, at any element alignment (gfx950 global memory takes
-// wide accesses at any)
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float* f) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[V]; };
-    const U u = *reinterpret_cast<const U*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = load_f(u.e, i);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float* f) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U { T e[V]; };
-    U u;
-#pragma unroll
-    for (int i = 0; i < V; ++i) store_f(u.e, i, f[i]);
-    *reinterpret_cast<U*>(p) = u;
-}
 
 // Where a lane's V pairs of slot p lie: elements a .. a + V - 1 and b .. b + V - 1.
 // Pairs of the half layout are (i, i + R/2); side by side they are 2 V elements
@@ -91,11 +74,27 @@ __device__ __forceinline__ void turn(float* f, const float* cs, const float* sn)
     }
 }
 
+// Sum over groups of L lanes: neighbours, pairs, fours and eights by the lane
+// crossings of vector instructions
+template <int CTRL>
+__device__ __forceinline__ float crossed(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d, 64);
+    v += crossed<0xB1>(v);                            // lane ^ 1
+    if constexpr (L >= 4) v += crossed<0x4E>(v);      // lane ^ 2
+    if constexpr (L >= 8) v += crossed<0x141>(v);     // the other four of eight
+    if constexpr (L >= 16) v += crossed<0x140>(v);    // the other eight of sixteen
+    if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+    if constexpr (L >= 64) v += __shfl_xor(v, 32, 64);
     return v;
+}
+
+// 1/sqrt(v) to one unit in the last place
+__device__ __forceinline__ float inverse_root(float v) {
+    if (v < 1e-30f) return 1.0f / sqrtf(v);   // the instruction takes no subnormal numbers
+    return __builtin_amdgcn_rsqf(v);
 }
 
 template <int V>
@@ -117,116 +116,154 @@ __device__ __forceinline__ void angles(const QkCall& c, int64_t tok, int p, bool
     }
 }
 
-// V pairs a lane and slot, L lanes a token, N slots a lane
+// The rows of one tensor that a token's lanes walk over
+template <typename T>
+struct HeadsOf {
+    const T* x;
+    const T* g;      // gradient of the result, or NULL
+    T* y;
+    int64_t xs, gs, ys;   // from head to head
+    const float* weight;
+};
+
+template <typename T>
+__device__ __forceinline__ HeadsOf<T> heads_of(const QkCall& c, bool isq, int64_t tok, int h0) {
+    if (isq)
+        return {(const T*)c.q + tok * c.q_ts + (int64_t)h0 * c.q_hs, c.gq ? (const T*)c.gq + tok * c.gq_ts + (int64_t)h0 * c.gq_hs : nullptr,
+                (T*)c.q_out + tok * c.qo_ts + (int64_t)h0 * c.qo_hs, c.q_hs, c.gq_hs, c.qo_hs, c.q_weight};
+    return {(const T*)c.k + tok * c.k_ts + (int64_t)h0 * c.k_hs, c.gk ? (const T*)c.gk + tok * c.gk_ts + (int64_t)h0 * c.gk_hs : nullptr,
+            (T*)c.k_out + tok * c.ko_ts + (int64_t)h0 * c.ko_hs, c.k_hs, c.gk_hs, c.ko_hs, c.k_weight};
+}
+
+template <int V>
+__device__ __forceinline__ void load_weight(const float* w, const Place& s, float* f) {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) f[i] = 1.0f;
+    if (w) load_pairs<float, V>(w, s, f);
+}
+
+// V pairs a lane and slot, L lanes a token, N slots a lane; U heads are in flight
 template <typename T, int V, int L, int N, bool INTER>
 __global__ __launch_bounds__(kThreads) void qk_fwd(QkCall c) {
+    constexpr int U = V * N >= 8 ? 2 : 4;
     const int lane = threadIdx.x % L;
     const int64_t tok = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     if (tok >= c.tokens) return;
-    const int heads = c.hq + c.hkv;
-    const int h0 = blockIdx.y * c.heads_each, h1 = min(h0 + c.heads_each, heads);
+    const int h0 = blockIdx.y * c.heads_each, h1 = min(h0 + c.heads_each, c.hq + c.hkv);
     Place s[N];
-    float cs[N][V], sn[N][V], wq[N][2 * V], wk[N][2 * V];
+    float cs[N][V], sn[N][V];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const int p = lane + n * L;
-        s[n] = place<V, INTER>(p, c.d, c.rot);
-        angles<V>(c, tok, p, s[n].turns, 1.0f, cs[n], sn[n]);
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) wq[n][i] = wk[n][i] = 1.0f;
-        if (c.q_weight) load_pairs<float, V>(c.q_weight, s[n], wq[n]);
-        if (c.k_weight) load_pairs<float, V>(c.k_weight, s[n], wk[n]);
+        s[n] = place<V, INTER>(lane + n * L, c.d, c.rot);
+        angles<V>(c, tok, lane + n * L, s[n].turns, 1.0f, cs[n], sn[n]);
     }
     const float inv_d = 1.0f / (float)c.d;
-    for (int hd = h0; hd < h1; ++hd) {
-        const bool isq = hd < c.hq;
-        const int64_t hh = isq ? hd : hd - c.hq;
-        const T* x = isq ? (const T*)c.q + tok * c.q_ts + hh * c.q_hs : (const T*)c.k + tok * c.k_ts + hh * c.k_hs;
-        T* y = isq ? (T*)c.q_out + tok * c.qo_ts + hh * c.qo_hs : (T*)c.k_out + tok * c.ko_ts + hh * c.ko_hs;
-        float f[N][2 * V], sq = 0.0f;
+    auto walk = [&](const HeadsOf<T>& t, int heads) {
+        float w[N][2 * V];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            load_pairs<T, V>(x, s[n], f[n]);
+        for (int n = 0; n < N; ++n) load_weight<V>(t.weight, s[n], w[n]);
+        for (int h = 0; h < heads; h += U) {
+            float f[U][N][2 * V], sq[U];
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) sq = fmaf(f[n][i], f[n][i], sq);
+            for (int u = 0; u < U; ++u)   // the last heads again where they are fewer
+#pragma unroll
+                for (int n = 0; n < N; ++n) load_pairs<T, V>(t.x + min(h + u, heads - 1) * t.xs, s[n], f[u][n]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                sq[u] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2 * V; ++i) sq[u] = fmaf(f[u][n][i], f[u][n][i], sq[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) sq[u] = group_sum<L>(sq[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float r = inverse_root(sq[u] * inv_d + c.eps);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 2 * V; ++i) f[u][n][i] *= r * w[n][i];
+                    if (s[n].turns) turn<V, INTER>(f[u][n], cs[n], sn[n]);
+                    if (h + u < heads) store_pairs<T, V>(t.y + (h + u) * t.ys, s[n], f[u][n]);
+                }
+            }
         }
-        const float r = 1.0f / sqrtf(group_sum<L>(sq) * inv_d + c.eps);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2 * V; ++i) f[n][i] *= r * (isq ? wq[n][i] : wk[n][i]);
-            if (s[n].turns) turn<V, INTER>(f[n], cs[n], sn[n]);
-            store_pairs<T, V>(y, s[n], f[n]);
-        }
-    }
+    };
+    if (h0 < c.hq) walk(heads_of<T>(c, true, tok, h0), min(h1, c.hq) - h0);
+    if (h1 > c.hq) walk(heads_of<T>(c, false, tok, max(h0 - c.hq, 0)), h1 - max(h0, c.hq));
 }
 
 template <typename T, int V, int L, int N, bool INTER>
 __global__ __launch_bounds__(kThreads) void qk_bwd(QkCall c) {
-    constexpr int TOK = kThreads / L;
+    constexpr int TOK = kThreads / L, U = V * N >= 8 ? 1 : 2;
     const int lane = threadIdx.x % L;
     const int heads = c.hq + c.hkv;
     Place s[N];
-    float wq[N][2 * V], wk[N][2 * V], gwq[N][2 * V], gwk[N][2 * V];
+    float gwq[N][2 * V], gwk[N][2 * V];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         s[n] = place<V, INTER>(lane + n * L, c.d, c.rot);
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-            wq[n][i] = wk[n][i] = 1.0f;
-            gwq[n][i] = gwk[n][i] = 0.0f;
-        }
-        if (c.q_weight) load_pairs<float, V>(c.q_weight, s[n], wq[n]);
-        if (c.k_weight) load_pairs<float, V>(c.k_weight, s[n], wk[n]);
+        for (int i = 0; i < 2 * V; ++i) gwq[n][i] = gwk[n][i] = 0.0f;
     }
     const float inv_d = 1.0f / (float)c.d;
     // a unit is a token and a share of its heads
     const int64_t units = c.tokens * c.head_parts;
     for (int64_t u0 = (int64_t)blockIdx.x * TOK; u0 < units; u0 += (int64_t)gridDim.x * TOK) {
-        const int64_t u = u0 + threadIdx.x / L;
-        if (u >= units) continue;
-        const int64_t tok = c.head_parts == 1 ? u : u / c.head_parts;
-        const int h0 = (int)(u - tok * c.head_parts) * c.heads_each, h1 = min(h0 + c.heads_each, heads);
+        const int64_t unit = u0 + threadIdx.x / L;
+        if (unit >= units) continue;
+        const int64_t tok = c.head_parts == 1 ? unit : unit / c.head_parts;
+        const int h0 = (int)(unit - tok * c.head_parts) * c.heads_each, h1 = min(h0 + c.heads_each, heads);
         float cs[N][V], sn[N][V];
 #pragma unroll
         for (int n = 0; n < N; ++n) angles<V>(c, tok, lane + n * L, s[n].turns, -1.0f, cs[n], sn[n]);
-        for (int hd = h0; hd < h1; ++hd) {
-            const bool isq = hd < c.hq;
-            const int64_t hh = isq ? hd : hd - c.hq;
-            const T* x = isq ? (const T*)c.q + tok * c.q_ts + hh * c.q_hs : (const T*)c.k + tok * c.k_ts + hh * c.k_hs;
-            const T* g = isq ? (const T*)c.gq + tok * c.gq_ts + hh * c.gq_hs : (const T*)c.gk + tok * c.gk_ts + hh * c.gk_hs;
-            T* y = isq ? (T*)c.q_out : (T*)c.k_out;
-            float f[N][2 * V], t[N][2 * V], sq = 0.0f, dot = 0.0f;
+        auto walk = [&](const HeadsOf<T>& t, int nh, float (*gw)[2 * V]) {
+            float w[N][2 * V];
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                load_pairs<T, V>(x, s[n], f[n]);
-                load_pairs<T, V>(g, s[n], t[n]);
-                if (s[n].turns) turn<V, INTER>(t[n], cs[n], sn[n]);
+            for (int n = 0; n < N; ++n) load_weight<V>(t.weight, s[n], w[n]);
+            for (int h = 0; h < nh; h += U) {
+                float f[U][N][2 * V], g[U][N][2 * V];
 #pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    sq = fmaf(f[n][i], f[n][i], sq);
-                    dot = fmaf(f[n][i], t[n][i] * (isq ? wq[n][i] : wk[n][i]), dot);
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        load_pairs<T, V>(t.x + min(h + u, nh - 1) * t.xs, s[n], f[u][n]);
+                        load_pairs<T, V>(t.g + min(h + u, nh - 1) * t.gs, s[n], g[u][n]);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (h + u >= nh) break;
+                    float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        if (s[n].turns) turn<V, INTER>(g[u][n], cs[n], sn[n]);
+#pragma unroll
+                        for (int i = 0; i < 2 * V; ++i) {
+                            sq = fmaf(f[u][n][i], f[u][n][i], sq);
+                            dot = fmaf(f[u][n][i], g[u][n][i] * w[n][i], dot);
+                        }
+                    }
+                    sq = group_sum<L>(sq);
+                    dot = group_sum<L>(dot);
+                    const float r = inverse_root(sq * inv_d + c.eps);
+                    const float back = r * r * inv_d * dot;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        float o[2 * V];
+#pragma unroll
+                        for (int i = 0; i < 2 * V; ++i) {
+                            o[i] = r * (g[u][n][i] * w[n][i] - f[u][n][i] * back);
+                            gw[n][i] += g[u][n][i] * (f[u][n][i] * r);
+                        }
+                        store_pairs<T, V>(t.y + (h + u) * t.ys, s[n], o);
+                    }
                 }
             }
-            sq = group_sum<L>(sq);
-            dot = group_sum<L>(dot);
-            const float r = 1.0f / sqrtf(sq * inv_d + c.eps);
-            const float back = r * r * inv_d * dot;
-            y += isq ? tok * c.qo_ts + hh * c.qo_hs : tok * c.ko_ts + hh * c.ko_hs;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                float o[2 * V];
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    const float gn = t[n][i];
-                    o[i] = r * (gn * (isq ? wq[n][i] : wk[n][i]) - f[n][i] * back);
-                    const float gw = gn * f[n][i] * r;
-                    gwq[n][i] += isq ? gw : 0.0f;
-                    gwk[n][i] += isq ? 0.0f : gw;
-                }
-                store_pairs<T, V>(y, s[n], o);
-            }
-        }
+        };
+        if (h0 < c.hq) walk(heads_of<T>(c, true, tok, h0), min(h1, c.hq) - h0, gwq);
+        if (h1 > c.hq) walk(heads_of<T>(c, false, tok, max(h0 - c.hq, 0)), h1 - max(h0, c.hq), gwk);
     }
     if (!c.partial) return;
     // sums of the workgroup's units: lanes of the same place meet in LDS
@@ -268,20 +305,23 @@ __global__ __launch_bounds__(kThreads) void qk_bwd(QkCall c) {
         }
 }
 
-// Column sums of the partial rows [rows][2 d]: sixteen columns and sixteen
-// shares of the rows a workgroup, in a fixed order
-__global__ __launch_bounds__(256) void qk_reduce(const float* __restrict__ partial, float* gqw, float* gkw, int rows, int d) {
-    __shared__ float red[16][17];
-    const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+// Column sums of the partial rows [rows][2 d]: sixteen columns and 64 shares of the
+// rows a workgroup, in a fixed order
+__global__ __launch_bounds__(1024) void qk_reduce(const float* __restrict__ partial, float* gqw, float* gkw, int rows, int d) {
+    __shared__ float red[64][17];
+    const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4, at = min(col, 2 * d - 1);
     float v = 0.0f;
-    if (col < 2 * d)
-        for (int r = part; r < rows; r += 16) v += partial[(int64_t)r * 2 * d + col];
+#pragma unroll 8
+    for (int r = part; r < rows; r += 64) v += partial[(int64_t)r * 2 * d + at];
     red[part][threadIdx.x & 15] = v;
     __syncthreads();
-    if (part != 0 || col >= 2 * d) return;
+    if (threadIdx.x >= 64) return;   // one wave: four lanes a column
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][threadIdx.x];
+    for (int i = 0; i < 16; ++i) v += red[16 * part + i][threadIdx.x & 15];
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+    if (part != 0 || col >= 2 * d) return;
     float* out = col < d ? gqw : gkw;
     if (out) out[col < d ? col : col - d] = v;
 }
@@ -290,8 +330,11 @@ int bwd_blocks(int64_t units, int L) {
     return (int)std::min<int64_t>((units * L + kThreads - 1) / kThreads, kMaxBlocks);
 }
 
-// pairs a lane holds: four where whole vectors fall on one side of every border
-int pairs_a_lane(int d, int rot) { return rot % 8 == 0 && d % 8 == 0 ? 4 : 1; }
+// pairs a lane holds: whole vectors fall on one side of every border
+int pairs_a_lane(int d, int rot, int dtype) {
+    if (dtype == DISCO_BF16 && rot % 16 == 0 && d % 16 == 0) return QV;
+    return rot % 8 == 0 && d % 8 == 0 ? 4 : 1;
+}
 
 // Shares of a token's heads: all in one where the tokens alone fill the chip.
 // 33024 tokens of 16 heads go in one share each; 8 tokens of 18 heads in 18.
@@ -328,7 +371,7 @@ int go(QkCall c, hipStream_t st) {
         }
         if (c.partial) {
             KernelTimer timer("qk_reduce", st);
-            qk_reduce<<<(2 * c.d + 15) / 16, 256, 0, st>>>(c.partial, c.gq_weight, c.gk_weight, blocks, c.d);
+            qk_reduce<<<(2 * c.d + 15) / 16, 1024, 0, st>>>(c.partial, c.gq_weight, c.gk_weight, blocks, c.d);
         }
     }
     const hipError_t e = hipGetLastError();
@@ -338,7 +381,15 @@ int go(QkCall c, hipStream_t st) {
 
 template <typename T>
 int typed(const QkCall& c, hipStream_t st) {
-    if (pairs_a_lane(c.d, c.rot) == 4) {
+    const int V = pairs_a_lane(c.d, c.rot, c.dtype);
+    if constexpr (sizeof(T) == 2) {
+        if (V == 8) switch (lanes_of(c.d, 8)) {
+            case 4: return go<T, 8, 4, 1>(c, st);
+            case 8: return go<T, 8, 8, 1>(c, st);
+            default: return go<T, 8, 16, 1>(c, st);
+        }
+    }
+    if (V == 4) {
         switch (lanes_of(c.d, 4)) {
             case 4: return go<T, 4, 4, 1>(c, st);
             case 8: return go<T, 4, 8, 1>(c, st);
