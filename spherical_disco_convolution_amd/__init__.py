@@ -39,6 +39,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import numpy as np
 
@@ -84,6 +85,13 @@ class _QkDesc(ctypes.Structure):
         ("dtype", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
         ("positions_int32", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
     ] + [(n + "_stride", ctypes.c_int64 * 2) for n in ("q", "k", "q_out", "k_out", "gq", "gk")]
+
+
+# the same two, written in one go (a structure's fields take 0.3 us each)
+_pack_attention = struct.Struct("@2q7if16q").pack
+_pack_qk = struct.Struct("@q8if12q").pack
+assert struct.calcsize("@2q7if16q") == ctypes.sizeof(_AttentionDesc)
+assert struct.calcsize("@q8if12q") == ctypes.sizeof(_QkDesc)
 
 
 def _load():
@@ -136,14 +144,14 @@ def _load():
                                            ctypes.c_float, ctypes.c_int, ctypes.c_float,
                                            ctypes.c_float, I32, I32, I32, I32, P, ctypes.c_float, P,
                                            I64, P]),
-        "disco_attention_fwd_workspace": (I64, [ctypes.POINTER(_AttentionDesc)]),
-        "disco_attention_fwd": (ctypes.c_int, [ctypes.POINTER(_AttentionDesc), P, P, P, P, P, P, P, P, P, I64, P]),
-        "disco_attention_bwd_workspace": (I64, [ctypes.POINTER(_AttentionDesc)]),
-        "disco_attention_bwd": (ctypes.c_int, [ctypes.POINTER(_AttentionDesc), P, P, P, P, P, P, P, P, P, P, P, P, P,
+        "disco_attention_fwd_workspace": (I64, [P]),
+        "disco_attention_fwd": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P, I64, P]),
+        "disco_attention_bwd_workspace": (I64, [P]),
+        "disco_attention_bwd": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                                I64, P]),
-        "disco_qk_norm_rope_fwd": (ctypes.c_int, [ctypes.POINTER(_QkDesc), P, P, P, P, P, P, P, P, P]),
+        "disco_qk_norm_rope_fwd": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P]),
         "disco_qk_norm_rope_bwd_workspace": (I64, [I32]),
-        "disco_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(_QkDesc), P, P, P, P, P, P, P, P, P, P, P, P, P, I64,
+        "disco_qk_norm_rope_bwd": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, I64,
                                                   P]),
         "disco_dropout_fwd": (ctypes.c_int, [P, ctypes.c_int, P, P, ctypes.c_int, I64, D, ctypes.c_uint64,
                                              ctypes.c_uint64, P, P]),
@@ -809,37 +817,48 @@ def muon_step(w, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool =
 # attention
 # ----------------------------------------------------------------------------
 def _tokens(t, name):
-    """(tokens, heads, d, (token stride, head stride)) of [T, H, D] or of a batch
+    """(tokens, heads, d, token stride, head stride) of [T, H, D] or of a batch
     [B, T, H, D] whose sequences lie one after another."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
     size, st = t.shape, t.stride()
-    if size[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"the elements of {name}'s heads must lie together")
-    ts = st[-3]
-    if t.dim() == 4:
-        if size[1] == 1:
-            ts = st[0]
-        elif size[0] > 1 and st[0] != size[1] * ts and t.numel():
+    if len(size) == 3:
+        n, h, d = size
+        ts, hs, one = st
+    elif len(size) == 4:
+        b, n, h, d = size
+        bs, ts, hs, one = st
+        if n == 1:
+            ts = bs
+        elif b > 1 and bs != n * ts and n * h * d:
             raise ValueError(f"{name}'s sequences must lie one after another")
-    n = math.prod(size[:-2])
-    return n, size[-2], size[-1], (ts if n > 1 else size[-2] * size[-1], st[-2] if size[-2] > 1 else size[-1])
+        n *= b
+    else:
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
+    if one != 1 and d > 1:
+        raise ValueError(f"the elements of {name}'s heads must lie together")
+    return n, h, d, ts if n > 1 else h * d, hs if h > 1 else d
 
 
-def _set_stride(desc, name, stride):
-    s = getattr(desc, name + "_stride")
-    s[0], s[1] = stride
-
-
-def _like(t, name, shape, dtype, make):
-    """A result: `t` as given, or a new dense tensor of make's device."""
+def _result(t, name, shape, like):
+    """A result and its strides: `t` as given, or a new dense tensor, of like's type."""
     if t is None:
-        return make.new_empty(shape, dtype=dtype)
-    if tuple(t.shape) != tuple(shape):
+        h, d = shape[-2:]
+        return like.new_empty(shape), h * d, d
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    return t
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+    return (t,) + _tokens(t, name)[3:]
+
+
+def _floats(t, name, n):
+    """Pointer of an optional float32 vector of n values (of a batch's too)."""
+    if t is None:
+        return None
+    if t.dtype != _torch().float32:
+        raise ValueError(f"{name} must be float32")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} values without gaps")
+    return t.data_ptr()
 
 
 def _boundaries(cu, name, n_seq):
@@ -854,38 +873,38 @@ def _boundaries(cu, name, n_seq):
 
 
 def _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale):
-    """The description of a call, and the pointers of its options."""
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    """The beginning of a call's description, and the pointers of its options."""
+    dtype = q.dtype
+    if k.dtype != dtype or v.dtype != dtype:
         raise ValueError(f"q, k and v must have the same dtype (got {q.dtype}, {k.dtype}, {v.dtype})")
-    if not q.dim() == k.dim() == v.dim():
+    dims = q.dim()
+    if not dims == k.dim() == v.dim():
         raise ValueError("q, k and v must have the same number of dimensions")
-    d = _AttentionDesc()
-    tq, hq, dk, sq = _tokens(q, "q")
-    tk, hkv, dk2, sk = _tokens(k, "k")
-    tv, hv, dv, sv = _tokens(v, "v")
+    tq, hq, dk, qts, qhs = _tokens(q, "q")
+    tk, hkv, dk2, kts, khs = _tokens(k, "k")
+    tv, hv, dv, vts, vhs = _tokens(v, "v")
     if dk2 != dk:
         raise ValueError(f"heads of k have {dk2} elements, those of q {dk}")
-    if (tv, hv) != (tk, hkv) or v.shape[:-1] != k.shape[:-1]:
+    if tv != tk or hv != hkv or (dims == 4 and v.shape[0] != k.shape[0]):
         raise ValueError(f"v has shape {tuple(v.shape)}, k {tuple(k.shape)}: tokens and heads must agree")
     if hkv < 1 or hq % hkv:
         raise ValueError(f"the heads of k and v ({hkv}) must divide those of q ({hq})")
-    if q.dim() == 4:
+    n_seq = 1
+    if dims == 4:
         if cu_q is not None or cu_k is not None:
             raise ValueError("boundaries are for packed tensors [tokens, heads, d]")
+        n_seq = max(q.shape[0], 1)
         if k.shape[0] != q.shape[0]:
             raise ValueError(f"q has {q.shape[0]} sequences, k {k.shape[0]}")
-        n_seq = q.shape[0]
-    else:
-        n_seq = cu_q.shape[0] - 1 if cu_q is not None else cu_k.shape[0] - 1 if cu_k is not None else 1
-    n_seq = max(n_seq, 1)
+    elif cu_q is not None or cu_k is not None:
+        n_seq = max((cu_k if cu_q is None else cu_q).shape[0] - 1, 1)
     _int32(n_seq, hq, hkv, dk, dv)
-    d.total_q, d.total_k, d.n_seq, d.hq, d.hkv, d.dk, d.dv = tq, tk, n_seq, hq, hkv, dk, dv
-    d.dtype, d.causal = _dtype_code(q), int(bool(causal))
-    d.scale = dk ** -0.5 if scale is None and dk else 1.0 if scale is None else float(scale)
-    for name, s in (("q", sq), ("k", sk), ("v", sv)):
-        _set_stride(d, name, s)
-    return d, (_f32_ptr(key_bias, "key_bias", k.shape[:-2]) if key_bias is None or key_bias.dim() != 1 else
-               _f32_ptr(key_bias, "key_bias", (tk,)), _boundaries(cu_q, "cu_q", n_seq), _boundaries(cu_k, "cu_k", n_seq))
+    if scale is None:
+        scale = dk ** -0.5 if dk else 1.0
+    # what a float32 rounds to infinity is refused as infinity
+    scale = scale if abs(scale) < 3e38 else math.inf
+    return ((tq, tk, n_seq, hq, hkv, dk, dv, _dtype_code(q), 1 if causal else 0, scale, qts, qhs, kts, khs, vts, vhs),
+            _floats(key_bias, "key_bias", tk), _boundaries(cu_q, "cu_q", n_seq), _boundaries(cu_k, "cu_k", n_seq))
 
 
 def attention_fwd(q, k, v, key_bias=None, cu_q=None, cu_k=None, causal: bool = False, scale: float | None = None,
@@ -906,18 +925,17 @@ def attention_fwd(q, k, v, key_bias=None, cu_q=None, cu_k=None, causal: bool = F
     need_lse=False.  What belongs to no sequence is left as it was."""
     if stream is not None:
         return _on(stream, attention_fwd, q, k, v, key_bias, cu_q, cu_k, causal, scale, out, need_lse)
-    torch = _torch()
-    d, (bptr, cq, ck) = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
-    out = _like(out, "out", tuple(q.shape[:-1]) + (v.shape[-1],), q.dtype, q)
-    _set_stride(d, "o", _tokens(out, "out")[3])
-    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if need_lse else None
-    nws = _lib.disco_attention_fwd_workspace(ctypes.byref(d))
+    head, bptr, cq, ck = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
+    out, ots, ohs = _result(out, "out", q.shape[:-1] + v.shape[-1:], q)
+    lse = q.new_empty(q.shape[:-1], dtype=_torch().float32) if need_lse else None
+    d = _pack_attention(*head, ots, ohs, 0, 0, 0, 0, 0, 0, 0, 0)
+    nws = _lib.disco_attention_fwd_workspace(d)
     if nws < 0:
         _check(nws, "attention_fwd")
     ws = _workspace(nws, q)
-    _check(_lib.disco_attention_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck,
-                                    out.data_ptr(), lse.data_ptr() if need_lse else None,
-                                    ws.data_ptr() if ws is not None else None, nws, _stream()), "attention_fwd")
+    _check(_lib.disco_attention_fwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck, out.data_ptr(),
+                                    lse.data_ptr() if need_lse else None, ws.data_ptr() if nws else None, nws,
+                                    _raw_current_stream()), "attention_fwd")
     return out, lse
 
 
@@ -931,64 +949,69 @@ def attention_bwd(q, k, v, o, lse, go, key_bias=None, cu_q=None, cu_k=None, caus
     if stream is not None:
         return _on(stream, attention_bwd, q, k, v, o, lse, go, key_bias, cu_q, cu_k, causal, scale, need_gq, need_gkv,
                    gq, gk, gv)
-    d, (bptr, cq, ck) = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
-    oshape = tuple(q.shape[:-1]) + (v.shape[-1],)
-    for t, name in ((o, "o"), (go, "go")):
-        _like(t, name, oshape, q.dtype, q)
-        _set_stride(d, name, _tokens(t, name)[3])
-    if lse is None:
-        raise ValueError("lse of the forward pass is needed")
-    lptr = _f32_ptr(lse, "lse", q.shape[:-1])
-    gq = _like(gq, "gq", q.shape, q.dtype, q) if need_gq else None
-    gk = _like(gk, "gk", k.shape, q.dtype, q) if need_gkv else None
-    gv = _like(gv, "gv", v.shape, q.dtype, q) if need_gkv else None
-    for t, name in ((gq, "gq"), (gk, "gk"), (gv, "gv")):
-        if t is not None:
-            _set_stride(d, name, _tokens(t, name)[3])
-    nws = _lib.disco_attention_bwd_workspace(ctypes.byref(d))
+    head, bptr, cq, ck = _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale)
+    oshape = q.shape[:-1] + v.shape[-1:]
+    if o is None or go is None or lse is None:
+        raise ValueError("o and lse of the forward pass and go are needed")
+    o, ots, ohs = _result(o, "o", oshape, q)
+    go, gots, gohs = _result(go, "go", oshape, q)
+    if lse.shape != q.shape[:-1]:
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {tuple(q.shape[:-1])}")
+    lptr = _floats(lse, "lse", lse.numel())
+    qs = ks = vs = (0, 0)
+    if need_gq:
+        gq, *qs = _result(gq, "gq", q.shape, q)
+    if need_gkv:
+        gk, *ks = _result(gk, "gk", k.shape, q)
+        gv, *vs = _result(gv, "gv", v.shape, q)
+    d = _pack_attention(*head, ots, ohs, gots, gohs, *qs, *ks, *vs)
+    nws = _lib.disco_attention_bwd_workspace(d)
     if nws < 0:
         _check(nws, "attention_bwd")
     ws = _workspace(nws, q)
     _check(_lib.disco_attention_bwd(
-        ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck, o.data_ptr(), lptr, go.data_ptr(),
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), bptr, cq, ck, o.data_ptr(), lptr, go.data_ptr(),
         gq.data_ptr() if need_gq else None, gk.data_ptr() if need_gkv else None, gv.data_ptr() if need_gkv else None,
-        ws.data_ptr() if ws is not None else None, nws, _stream()), "attention_bwd")
-    return gq, gk, gv
+        ws.data_ptr() if nws else None, nws, _raw_current_stream()), "attention_bwd")
+    return gq if need_gq else None, gk if need_gkv else None, gv if need_gkv else None
 
 
 # ----------------------------------------------------------------------------
 # norm and rotation of queries and keys
 # ----------------------------------------------------------------------------
 def _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps):
-    torch = _torch()
+    """The beginning of a call's description, and the pointers of its vectors."""
     if k.dtype != q.dtype:
         raise ValueError(f"q and k must have the same dtype (got {q.dtype}, {k.dtype})")
-    tokens, hq, dim, sq = _tokens(q, "q")
-    tk, hkv, dim2, sk = _tokens(k, "k")
-    if k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or dim2 != dim:
+    tokens, hq, dim, qts, qhs = _tokens(q, "q")
+    _, hkv, dim2, kts, khs = _tokens(k, "k")
+    lead = q.shape[:-2]
+    if lead != k.shape[:-2] or dim2 != dim:
         raise ValueError(f"q has shape {tuple(q.shape)}, k {tuple(k.shape)}: only the heads may differ")
     _int32(hq, hkv, dim)
-    d = _QkDesc()
-    d.tokens, d.hq, d.hkv, d.d, d.dtype = tokens, hq, hkv, dim, _dtype_code(q)
-    d.rot, d.axes, d.interleaved, d.eps = 0, 1, int(bool(interleaved)), float(eps)
-    _set_stride(d, "q", sq)
-    _set_stride(d, "k", sk)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq must both be given or both be None")
     pptr = fptr = None
+    pairs, axes, ints = 0, 1, 0
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must have one dimension")
-        fptr = _f32_ptr(inv_freq, "inv_freq", inv_freq.shape)
-        d.rot = 2 * inv_freq.shape[0]
-        lead = tuple(q.shape[:-2])
-        d.axes = positions.shape[-1] if positions.dim() == len(lead) + 1 else 1
-        _need(positions, "positions", lead + ((d.axes,) if positions.dim() == len(lead) + 1 else ()))
-        if positions.dtype not in (torch.int32, torch.float32):
+        torch = _torch()
+        pairs = inv_freq.numel()
+        fptr = _floats(inv_freq, "inv_freq", pairs)
+        shape = positions.shape
+        if len(shape) == len(lead) + 1:
+            axes = shape[-1]
+            shape = shape[:-1]
+        if shape != lead or not positions.is_contiguous():
+            raise ValueError(f"positions have shape {tuple(positions.shape)}, expected {tuple(lead)}, or axes behind, "
+                             "without gaps")
+        ints = int(positions.dtype == torch.int32)
+        if not ints and positions.dtype != torch.float32:
             raise ValueError(f"positions must be int32 or float32 (got {positions.dtype})")
-        d.positions_int32 = int(positions.dtype == torch.int32)
         pptr = positions.data_ptr()
-    return d, (_f32_ptr(q_weight, "q_weight", (dim,)), _f32_ptr(k_weight, "k_weight", (dim,)), pptr, fptr)
+        _int32(2 * pairs, axes)
+    eps = eps if abs(eps) < 3e38 else math.inf
+    return ((tokens, hq, hkv, dim, _dtype_code(q), 2 * pairs, axes, ints, 1 if interleaved else 0, eps, qts, qhs, kts, khs),
+            (_floats(q_weight, "q_weight", dim), _floats(k_weight, "k_weight", dim), pptr, fptr))
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, interleaved: bool = False,
@@ -1002,13 +1025,12 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     if stream is not None:
         return _on(stream, qk_norm_rope_fwd, q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps, q_out,
                    k_out)
-    d, (qw, kw, pptr, fptr) = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
-    q_out = _like(q_out, "q_out", q.shape, q.dtype, q)
-    k_out = _like(k_out, "k_out", k.shape, q.dtype, k)
-    _set_stride(d, "q_out", _tokens(q_out, "q_out")[3])
-    _set_stride(d, "k_out", _tokens(k_out, "k_out")[3])
-    _check(_lib.disco_qk_norm_rope_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), qw, kw, pptr, fptr,
-                                       q_out.data_ptr(), k_out.data_ptr(), _stream()), "qk_norm_rope_fwd")
+    head, ptrs = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
+    q_out, qts, qhs = _result(q_out, "q_out", q.shape, q)
+    k_out, kts, khs = _result(k_out, "k_out", k.shape, k)
+    d = _pack_qk(*head, qts, qhs, kts, khs, 0, 0, 0, 0)
+    _check(_lib.disco_qk_norm_rope_fwd(d, q.data_ptr(), k.data_ptr(), *ptrs, q_out.data_ptr(), k_out.data_ptr(),
+                                       _raw_current_stream()), "qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -1022,28 +1044,27 @@ def qk_norm_rope_bwd(q, k, gq_out, gk_out, q_weight=None, k_weight=None, positio
     if stream is not None:
         return _on(stream, qk_norm_rope_bwd, q, k, gq_out, gk_out, q_weight, k_weight, positions, inv_freq, interleaved,
                    eps, need_gweights, gq, gk)
-    torch = _torch()
-    d, (qw, kw, pptr, fptr) = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
-    _like(gq_out, "gq_out", q.shape, q.dtype, q)
-    _like(gk_out, "gk_out", k.shape, q.dtype, k)
-    gq = _like(gq, "gq", q.shape, q.dtype, q)
-    gk = _like(gk, "gk", k.shape, q.dtype, k)
-    for t, field, name in ((gq_out, "gq", "gq_out"), (gk_out, "gk", "gk_out"), (gq, "q_out", "gq"), (gk, "k_out", "gk")):
-        _set_stride(d, field, _tokens(t, name)[3])
+    head, ptrs = _qk(q, k, q_weight, k_weight, positions, inv_freq, interleaved, eps)
+    if gq_out is None or gk_out is None:
+        raise ValueError("the gradients of both results are needed")
+    gq_out, gqts, gqhs = _result(gq_out, "gq_out", q.shape, q)
+    gk_out, gkts, gkhs = _result(gk_out, "gk_out", k.shape, k)
+    gq, qts, qhs = _result(gq, "gq", q.shape, q)
+    gk, kts, khs = _result(gk, "gk", k.shape, k)
+    d = _pack_qk(*head, qts, qhs, kts, khs, gqts, gqhs, gkts, gkhs)
     gqw = gkw = ws = None
     nws = 0
     if need_gweights:
-        gqw = q.new_empty((d.d,), dtype=torch.float32)
-        gkw = torch.empty_like(gqw)
-        nws = _lib.disco_qk_norm_rope_bwd_workspace(d.d)
+        gqw = q.new_empty((head[3],), dtype=_torch().float32)
+        gkw = gqw.new_empty((head[3],))
+        nws = _lib.disco_qk_norm_rope_bwd_workspace(head[3])
         if nws < 0:
             _check(nws, "qk_norm_rope_bwd")
         ws = _workspace(nws, q)
     _check(_lib.disco_qk_norm_rope_bwd(
-        ctypes.byref(d), q.data_ptr(), k.data_ptr(), gq_out.data_ptr(), gk_out.data_ptr(), qw, kw, pptr, fptr,
-        gq.data_ptr(), gk.data_ptr(), gqw.data_ptr() if need_gweights else None,
-        gkw.data_ptr() if need_gweights else None, ws.data_ptr() if ws is not None else None, nws, _stream()),
-        "qk_norm_rope_bwd")
+        d, q.data_ptr(), k.data_ptr(), gq_out.data_ptr(), gk_out.data_ptr(), *ptrs, gq.data_ptr(), gk.data_ptr(),
+        gqw.data_ptr() if need_gweights else None, gkw.data_ptr() if need_gweights else None,
+        ws.data_ptr() if nws else None, nws, _raw_current_stream()), "qk_norm_rope_bwd")
     return gq, gk, gqw, gkw
 
 

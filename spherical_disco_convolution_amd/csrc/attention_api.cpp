@@ -45,7 +45,7 @@ bool wide(const AttnArgs& a) {
 int parts(int64_t n_seq, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 256; ++s) {
+    for (int s = 1; s <= 256; s += s < 8 ? 1 : s / 4) {
         if (s > 1 && steps / s < 4.0) break;
         const double rounds = (double)ceil_div(tiles * s, at_once);
         double t = rounds * (steps / s + 4.0);
@@ -233,22 +233,14 @@ int check_boundaries(const AttnArgs& a) {
 }
 
 int64_t fwd_bytes(const AttnArgs& a) {
-    // the plan of wide accesses has the most splits
-    AttnArgs b = a;
-    int64_t most = 0;
-    for (int odd = 0; odd < 2; ++odd) {
-        if (odd) b.q_ts |= 1;
-        const int splits = attn_plan_fwd(b).splits;
-        if (splits > 1) most = std::max(most, splits * b.total_q * b.hq * (b.dv + 1) * 4);
-    }
-    return ceil_div(most, 16) * 16;
+    const int64_t splits = a.plan.splits;
+    return splits > 1 ? ceil_div(splits * a.total_q * a.hq * (a.dv + 1) * 4, 16) * 16 : 0;
 }
 
 int64_t bwd_part_bytes(const AttnArgs& a) {
     int64_t n = 0;
-    const int sq = attn_plan_bwd_q(a).splits, sk = attn_plan_bwd_kv(a).splits;
-    if (sq > 1) n = sq * a.total_q * a.hq * a.dk * 4;
-    if (sk > 1) n = std::max(n, sk * a.total_k * a.hkv * (a.dk + a.dv) * 4);
+    if (a.plan.splits > 1) n = a.plan.splits * a.total_q * a.hq * a.dk * 4;
+    if (a.plan_kv.splits > 1) n = std::max(n, a.plan_kv.splits * a.total_k * a.hkv * (a.dk + a.dv) * 4);
     return n;
 }
 
@@ -272,7 +264,13 @@ int64_t disco_attention_fwd_workspace(const disco_attention_desc* desc) {
     clear_error();
     AttnArgs a;
     const int rc = check_desc(desc, &a);
-    return rc != DISCO_OK ? rc : fwd_bytes(a);
+    if (rc != DISCO_OK) return rc;
+    a.plan = attn_plan_fwd(a);
+    const int64_t wide = fwd_bytes(a);
+    if (!a.plan.fast) return wide;
+    a.q_ts |= 1;   // addresses that are not multiples of 16 bytes are cut up like this
+    a.plan = attn_plan_fwd(a);
+    return std::max(wide, fwd_bytes(a));
 }
 
 int disco_attention_fwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -292,6 +290,7 @@ int disco_attention_fwd(const disco_attention_desc* desc, const void* q, const v
     for (const Rows& r : rows)
         if ((rc = check_rows(r)) != DISCO_OK) return rc;
     if (a.total_q == 0) return DISCO_OK;
+    a.plan = attn_plan_fwd(a);
     const int64_t need = fwd_bytes(a), cu = (int64_t)(a.n_seq + 1) * 4;
     if ((rc = need_workspace(workspace, workspace_bytes, need)) != DISCO_OK) return rc;
     const Arg args[] = {{"key_bias", key_bias, a.total_k * 4, 4, false},
@@ -302,8 +301,7 @@ int disco_attention_fwd(const disco_attention_desc* desc, const void* q, const v
     const bool outs[] = {false, false, false, true, true};
     if ((rc = check_tensors(rows, 4, args, 5, outs)) != DISCO_OK) return rc;
     a.part = static_cast<float*>(workspace);
-    const int splits = attn_plan_fwd(a).splits;
-    a.part_lse = a.part + (splits > 1 ? splits * a.total_q * a.hq * a.dv : 0);
+    a.part_lse = a.part + (need ? a.plan.splits * a.total_q * a.hq * a.dv : 0);
     return launch_attention_fwd(a, stream);
 }
 
@@ -311,7 +309,10 @@ int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc) {
     clear_error();
     AttnArgs a;
     const int rc = check_desc(desc, &a);
-    return rc != DISCO_OK ? rc : bwd_delta_bytes(a) + bwd_part_bytes(a);
+    if (rc != DISCO_OK) return rc;
+    a.plan = attn_plan_bwd_q(a);
+    a.plan_kv = attn_plan_bwd_kv(a);
+    return bwd_delta_bytes(a) + bwd_part_bytes(a);
 }
 
 int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -348,6 +349,8 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
     for (const Rows& r : rows)
         if ((rc = check_rows(r)) != DISCO_OK) return rc;
     if (nq == 0 && nk == 0) return DISCO_OK;
+    a.plan = attn_plan_bwd_q(a);
+    a.plan_kv = attn_plan_bwd_kv(a);
     const int64_t delta = bwd_delta_bytes(a), need = delta + bwd_part_bytes(a), cu = (int64_t)(a.n_seq + 1) * 4;
     if ((rc = need_workspace(workspace, workspace_bytes, need)) != DISCO_OK) return rc;
     const Arg args[] = {{"key_bias", key_bias, a.total_k * 4, 4, false},

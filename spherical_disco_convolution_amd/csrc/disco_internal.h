@@ -231,6 +231,12 @@ struct OrthoCall {
 size_t orthogonalize_workspace(int batch, int rows, int cols);
 int launch_orthogonalize(const OrthoCall& c, void* stream);
 
+// How a call is cut up: by its sizes, types and alignment alone.
+struct AttnPlan {
+    int waves;        // of a workgroup, 32 rows (or keys) each
+    int splits;       // parts of the axis that a workgroup walks over
+    bool fast;        // 16-byte accesses
+};
 // Attention (kernels_attention.hip, kernels_attention_bwd.hip).  Strides are in
 // elements, ts from token to token and hs from head to head.
 struct AttnArgs {
@@ -248,13 +254,8 @@ struct AttnArgs {
     int n_seq, hq, hkv, G, dk, dv, causal;
     int each_q, each_k;          // tokens of a sequence where there are no boundaries
     float scale;
+    AttnPlan plan, plan_kv;      // of the call, and of its gradient of k and v
     int slots, splits;           // of one launch
-};
-// How a call is cut up: by its sizes, types and alignment alone.
-struct AttnPlan {
-    int waves;        // of a workgroup, 32 rows (or keys) each
-    int splits;       // parts of the axis that a workgroup walks over
-    bool fast;        // 16-byte accesses
 };
 AttnPlan attn_plan_fwd(const AttnArgs& a);
 AttnPlan attn_plan_bwd_q(const AttnArgs& a);

@@ -386,7 +386,7 @@ int fwd_waves(const AttnArgs& a, int waves, hipStream_t st) {
 
 template <typename T>
 int fwd_typed(AttnArgs a, hipStream_t st) {
-    const AttnPlan p = attn_plan_fwd(a);
+    const AttnPlan p = a.plan;
     a.splits = p.splits;
     // keys of a tile: 64 where two waves of a SIMD still hold their scores
     constexpr int KT = sizeof(T) == 2 ? 64 : 32;

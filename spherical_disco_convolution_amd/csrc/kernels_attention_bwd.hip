@@ -543,10 +543,10 @@ void sum_parts(const Parts& x, const Parts& y, int64_t total, int heads, int spl
 }
 
 template <typename T, int DP, bool FAST>
-int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
+int bwd_go(AttnArgs a, hipStream_t st) {
     constexpr int NW = 4;
     a.slots = (int)tile_slots(a.cu_q != nullptr, a.total_q, a.n_seq, a.G, 32 * NW);
-    a.splits = a.gq ? pq.splits : 1;
+    a.splits = a.gq ? a.plan.splits : 1;
     if (a.total_q > 0) {   // delta, which gk and gv need too
         KernelTimer timer("attn_bwd_q", st);
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
@@ -557,7 +557,7 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
         sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);
     if (a.gk && a.total_k > 0) {
         a.slots = (int)tile_slots(a.cu_k != nullptr, a.total_k, a.n_seq, 1, 32 * NW);
-        a.splits = pk.splits;
+        a.splits = a.plan_kv.splits;
         a.part2 = a.part + (size_t)a.splits * a.total_k * a.hkv * a.dk;
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
         {
@@ -573,12 +573,11 @@ int bwd_go(AttnArgs a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t st) {
 
 template <typename T>
 int bwd_typed(const AttnArgs& a, hipStream_t st) {
-    const AttnPlan pq = attn_plan_bwd_q(a), pk = attn_plan_bwd_kv(a);
-    if (!pq.fast) return bwd_go<T, 128, false>(a, pq, pk, st);
+    if (!a.plan.fast) return bwd_go<T, 128, false>(a, st);
     const int d = std::max(a.dk, a.dv);
-    if (d <= 32) return bwd_go<T, 32, true>(a, pq, pk, st);
-    if (d <= 64) return bwd_go<T, 64, true>(a, pq, pk, st);
-    return bwd_go<T, 128, true>(a, pq, pk, st);
+    if (d <= 32) return bwd_go<T, 32, true>(a, st);
+    if (d <= 64) return bwd_go<T, 64, true>(a, st);
+    return bwd_go<T, 128, true>(a, st);
 }
 
 }  // namespace
