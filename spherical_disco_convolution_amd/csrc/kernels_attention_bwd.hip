@@ -7,6 +7,7 @@
 // of keys (gk, gv): seven products where one kernel would do with five, but no
 // sum is taken in an order that changes from run to run, and no atomics.
 #include "attention_device.h"
+#include "vector_io.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -507,8 +508,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         }
 }
 
-// Sums of the parts of one or two tensors [tokens, heads, d], a wave a row; tokens
-// of no sequence stay as they are.
+// Sums of the parts of one or two tensors [tokens, heads, d], V elements a thread;
+// tokens of no sequence stay as they are.
 struct Parts {
     const float* part;
     void* out;
@@ -516,30 +517,35 @@ struct Parts {
     int d;
 };
 
-template <typename T>
+template <typename T, int V>
 __global__ __launch_bounds__(256) void attn_sum(Parts a, Parts b, int64_t total, int heads, int splits, const int32_t* cu,
                                                 int n_seq) {
-    const int lane = threadIdx.x & 63;
-    const int64_t cell = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tok = cell / heads;
-    const int head = (int)(cell - tok * heads);
+    const Parts p = blockIdx.y == 0 ? a : b;
+    const int groups = (p.d + V - 1) / V;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, cell = id / groups, tok = cell / heads;
+    const int d0 = (int)(id - cell * groups) * V, head = (int)(cell - tok * heads);
     if (tok >= total || (cu && (tok < cu[0] || tok >= cu[n_seq]))) return;
-    for (int k = 0; k < 2; ++k) {
-        const Parts& p = k == 0 ? a : b;
-        T* out = (T*)p.out + tok * p.ts + (int64_t)head * p.hs;
-        for (int i = lane; i < p.d; i += 64) {
-            float v = 0.0f;
+    const int64_t stride = total * heads * p.d;
+    const float* q = p.part + cell * p.d + d0;
+    float v[V] = {};
 #pragma unroll 4
-            for (int s = 0; s < splits; ++s) v += p.part[(s * total * heads + cell) * p.d + i];
-            store_f(out, i, v);
-        }
+    for (int s = 0; s < splits; ++s) {
+        float f[V];
+        load_v<float, V>(q + s * stride, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += f[i];
     }
+    store_v<T, V>((T*)p.out + tok * p.ts + (int64_t)head * p.hs + d0, v);
 }
 
 template <typename T>
 void sum_parts(const Parts& x, const Parts& y, int64_t total, int heads, int splits, const int32_t* cu, int n_seq,
                hipStream_t st) {
     KernelTimer timer("attn_sum", st);
-    attn_sum<T><<<(unsigned)((total * heads + 3) / 4), 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
+    const int v = x.d % 4 || y.d % 4 ? 1 : 4;
+    const dim3 grid((unsigned)((total * heads * (std::max(x.d, y.d) / v) + 255) / 256), y.out ? 2 : 1);
+    if (v == 4) attn_sum<T, 4><<<grid, 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
+    else attn_sum<T, 1><<<grid, 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
 }
 
 template <typename T, int DP, bool FAST>
