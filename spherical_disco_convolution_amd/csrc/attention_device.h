@@ -119,81 +119,81 @@ struct Tile {
     static constexpr int NCH = USED <= 4 ? 4 : USED <= 8 ? 8 : USED <= 16 ? 16 : 32;
     static constexpr int RB = 16 * NCH;
     static __device__ __forceinline__ int turn(int row) {
+        // float32 products are too slow for banks to matter: whole groups of eight
+        // chunks change places, so that few addresses need registers
+        if constexpr (sizeof(T) == 4) return NCH == 8 ? 0 : ((((row & 3) ^ ((row >> 2) & 1)) << 3) & (NCH - 1));
         if constexpr (NCH == 4) return (row >> 2) & 3;
         if constexpr (NCH == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-        if constexpr (NCH == 16) return ((row & 3) << 2) | ((row >> 2) & 3);
-        return (((row >> 2) & 1) << 3) | ((row & 3) << 1) | ((row >> 3) & 1);
+        return ((row & 3) << 2) | ((row >> 2) & 3);
     }
     static __device__ __forceinline__ uint32_t at(int row, int chunk) {
         return (uint32_t)(row * RB + ((chunk ^ turn(row)) << 4));
-    }
-    // rows row0 .. row0 + 31 as an operand, summed elements of chunks 2 c, 2 c + 1
-    static __device__ __forceinline__ typename Op<T>::Frag rows(uint32_t base, int row0, int c, int lane) {
-        const uint32_t p = base + at(row0 + (lane & 31), 2 * c + (lane >> 5));
-        return __builtin_bit_cast(typename Op<T>::Frag, *(const lds_u32x4*)(uintptr_t)p);
-    }
-    // columns 32 dt .. + 31 as an operand, summed over rows row0 .. row0 + KE - 1 in
-    // the order of a product's result
-    static __device__ __forceinline__ typename Op<T>::Frag columns(uint32_t base, int row0, int dt, int lane) {
-        const int h = lane >> 5;
-        if constexpr (sizeof(T) == 2) {
-            const int s = lane & 15, g = (lane >> 4) & 1;
-            const int d = 32 * dt + 16 * g + 4 * (s & 3);
-            const uint32_t sub = (d & 7) * 2;
-            const int r = row0 + 4 * h + (s >> 2);
-            const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(base + at(r, d >> 3) + sub));
-            const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(base + at(r + 8, d >> 3) + sub));
-            return __builtin_bit_cast(typename Op<T>::Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            const int d = 32 * dt + (lane & 31);
-            floatx4 f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = *(const lds_f32*)(uintptr_t)(base + at(row0 + 4 * h + i, d >> 2) + (d & 3) * 4);
-            return f;
-        }
     }
 };
 
 // Where a lane reads the operands of a tile whose place in LDS is known when
 // compiled: addresses are taken once, what changes goes into the instructions.
+// rows(): rows 32 k .. + 31 of the tile `off` bytes from base, summed elements of
+// chunks 2 c and 2 c + 1.  columns(): columns 32 d .. + 31, summed over rows KE b ..
+// in the order of a product's result.
 template <typename T, int DP>
-struct Reader {
-    typedef Tile<T, DP> L;
-    typedef typename Op<T>::Frag Frag;
-    static constexpr int KE = Op<T>::KE, NT = DP / 32;
-    uint32_t base, row[DP / KE], col[NT][2];
-    int lane;
-    __device__ __forceinline__ void init(uint32_t b, int ln) {
-        base = b;
-        lane = ln;
+struct Reader;
+
+template <int DP>
+struct Reader<bf16_t, DP> {
+    typedef Tile<bf16_t, DP> L;
+    typedef bf16x8_t Frag;
+    static constexpr int NT = DP / 32;
+    uint32_t row[DP / 16], col[NT][2];
+    __device__ __forceinline__ void init(uint32_t base, int lane) {
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) row[c] = b + L::at(ln & 31, 2 * c + (ln >> 5));
-        if constexpr (sizeof(T) == 2) {
-            const int s = ln & 15, r = 4 * (ln >> 5) + (s >> 2);
+        for (int c = 0; c < DP / 16; ++c) row[c] = base + L::at(lane & 31, 2 * c + (lane >> 5));
+        const int s = lane & 15, r = 4 * (lane >> 5) + (s >> 2);
 #pragma unroll
-            for (int d = 0; d < NT; ++d)
+        for (int d = 0; d < NT; ++d)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int e = 32 * d + 16 * ((ln >> 4) & 1) + 4 * (s & 3);
-                    col[d][j] = b + L::at(r + 8 * j, e >> 3) + (e & 7) * 2;
-                }
-        }
+            for (int j = 0; j < 2; ++j) {
+                const int e = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (s & 3);
+                col[d][j] = base + L::at(r + 8 * j, e >> 3) + (e & 7) * 2;
+            }
     }
-    // the tile `off` bytes from base; rows 32 k .. + 31, chunks 2 c and 2 c + 1
     __device__ __forceinline__ Frag rows(uint32_t off, int k, int c) const {
         return __builtin_bit_cast(Frag, *(const lds_u32x4*)(uintptr_t)(row[c] + (off + k * 32 * L::RB)));
     }
-    // columns 32 d .. + 31, summed over rows KE b .. in a result's order
     __device__ __forceinline__ Frag columns(uint32_t off, int b, int d) const {
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t o = off + b * KE * L::RB;
-            const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][0] + o));
-            const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][1] + o));
-            return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            return L::columns(base + off, b * KE, d, lane);
+        const uint32_t o = off + b * 16 * L::RB;
+        const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][0] + o));
+        const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(col[d][1] + o));
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+template <int DP>
+struct Reader<float, DP> {
+    typedef Tile<float, DP> L;
+    typedef floatx4 Frag;
+    static constexpr int NT = DP / 32;
+    uint32_t row[NT];   // of eight chunks each
+    uint32_t col[2];    // where the lane's half of the rows moves a group of chunks up, or down
+    __device__ __forceinline__ void init(uint32_t base, int lane) {
+        const int h = lane >> 5;
+#pragma unroll
+        for (int g = 0; g < NT; ++g) row[g] = base + L::at(lane & 31, 8 * g + h);
+        const uint32_t at = base + 4 * h * L::RB + (lane & 31) * 4;
+        col[0] = at + (NT > 1 ? 128 * h : 0);
+        col[1] = at - (NT > 1 ? 128 * h : 0);
+    }
+    __device__ __forceinline__ Frag rows(uint32_t off, int k, int c) const {
+        return *(const lds_f32x4*)(uintptr_t)(row[c / 4] + (off + k * 32 * L::RB + (c % 4) * 32));
+    }
+    __device__ __forceinline__ Frag columns(uint32_t off, int b, int d) const {
+        Frag f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // row 8 b + 4 h + i has group d at d ^ i ^ h
+            const int g = (d ^ i) & (NT - 1);
+            f[i] = *(const lds_f32*)(uintptr_t)(col[g & 1] + (off + (8 * b + i) * L::RB + 128 * g));
         }
+        return f;
     }
 };
 

@@ -17,15 +17,17 @@ constexpr float kMostSum = 1.152921504606846976e18f;
 
 // A workgroup of NW waves has 32 rows a wave and walks over the keys of its
 // part in tiles of KT: one pass with a reference close to the running maximum, and
-// the running sum.  Three tiles are under way in a wave: while tile i's scores
-// become weights on the vector units, the matrix cores take the scores of i + 1
-// and the values of i - 1, which depend on none of it.
+// the running sum.  bfloat16: three tiles are under way in a wave: while tile i's
+// scores become weights on the vector units, the matrix cores take the scores of
+// i + 1 and the values of i - 1, which depend on none of it.  float32 products take
+// most of the time, so a tile goes through at once and leaves registers for the heads.
 template <typename T, int DP, int NW, int KT, bool BIAS, bool FAST>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1) void attn_fwd(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
     typedef typename Addend<T>::Word Word;
     constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, NK = KT / 32, TB = KT * L::RB;
+    constexpr bool PIPE = sizeof(T) == 2;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TB];   // two stages of keys, then of values
     // biases, and zeros for the upper half of the lanes
     __shared__ __attribute__((aligned(16))) Word bias_s[BIAS ? 2 : 1][2][KT];
@@ -120,8 +122,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     const int head = hk * a.G + g;
     const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
     float m = -kInf, l = 0.0f;
-    Frag qf[DP / KE], pf[2][KT / KE];
-    floatx16 o[NT], s[2][NK];
+    Frag qf[DP / KE], pf[PIPE ? 2 : 1][KT / KE];
+    floatx16 o[NT], s[PIPE ? 2 : 1][NK];
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
         constexpr int st = decltype(stage_c)::value;
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
-            floatx16& x = s[st][kt];
+            floatx16& x = s[PIPE ? st : 0][kt];
             x = floatx16{};
             if constexpr (BIAS) x = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * st * KT + 32 * kt)));
 #pragma unroll
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 #pragma unroll
         for (int b = 0; b < KT / KE; ++b)
 #pragma unroll
-            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[st][b], o[d]);
+            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[PIPE ? st : 0][b], o[d]);
     };
     // scores to weights, and this lane's part of their sum
     auto soften = [&](const floatx16* x, Frag* w) -> float {
@@ -170,37 +172,45 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     auto step = [&](auto stage_c, int i) {
         constexpr int st = decltype(stage_c)::value;
         const int k0 = (t0 + i) * KT;
-        all_arrived();   // keys i + 1 and values i - 1; all waves have left keys i and values i - 2
-        start_values(st);
-        if constexpr (BIAS && !FAST) raw = bias_of(i + 2);
-        start_keys(i + 2, st, raw);
+        constexpr int at = PIPE ? st : 0, next = PIPE ? st : st ^ 1;   // of the scores, of the tile asked for
+        constexpr int more = PIPE ? 2 : 1;
+        // Here are keys i + 1 and values i - 1, and all waves have left keys i and values
+        // i - 2 (float32: tile i is here, and all waves have left tile i - 1).
+        all_arrived();
+        if constexpr (PIPE) start_values(st);
+        if constexpr (BIAS && !FAST) raw = bias_of(i + more);
+        start_keys(i + more, next, raw);
+        if constexpr (!PIPE) start_values(next);
         if constexpr (BIAS && FAST) {
-            if (wave == 0) start_bias(i + 4, st);
-            raw = raw_s[st ^ 1][lane];   // of tile i + 3
+            if (wave == 0) start_bias(i + more + 2, next);
+            raw = raw_s[next ^ 1][lane];   // of tile i + more + 1
         }
+        if constexpr (!PIPE) score(std::integral_constant<int, st>());
         if (k0 + KT > least) {   // some row does not see all of the tile
             const int room = lim - k0 - 4 * h;
 #pragma unroll
             for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (32 * kt + 8 * (e / 4) + e % 4 >= room) s[st][kt][e] = -kInf;
+                    if (32 * kt + 8 * (e / 4) + e % 4 >= room) s[at][kt][e] = -kInf;
         }
-        score(std::integral_constant<int, st ^ 1>());   // behind the last tile: not used
-        weigh(std::integral_constant<int, st ^ 1>());
-        float sum = soften(s[st], pf[st]);
+        if constexpr (PIPE) {
+            score(std::integral_constant<int, st ^ 1>());   // behind the last tile: not used
+            weigh(std::integral_constant<int, st ^ 1>());
+        }
+        float sum = soften(s[at], pf[at]);
         // NK DP / KE products for the scores and as many for the values (2 percent
         // faster than in the compiler's order)
-        if constexpr (sizeof(T) == 2) mix<NK * DP / 8, 6, 2, 320 / DP, 128 / DP>();
+        if constexpr (PIPE) mix<NK * DP / 8, 6, 2, 320 / DP, 128 / DP>();
         // rows whose reference is taken anew; the others keep their bits
         bool late = m == -kInf;
         if (__any(late || sum > kMostSum)) {
             late = late || half_max(sum) > kMostSum;
-            float mx = s[st][0][0];
+            float mx = s[at][0][0];
 #pragma unroll
             for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[st][kt][e]);
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[at][kt][e]);
             mx = half_max(mx) * scale2;
             const float mnew = late ? fmaxf(m, mx) : m;
             const float shrink = exp2_fast(m - (mnew == -kInf ? 0.0f : mnew));
@@ -210,9 +220,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             for (int d = 0; d < NT; ++d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
-            sum = soften(s[st], pf[st]);
+            sum = soften(s[at], pf[at]);
         }
         l += sum;
+        if constexpr (!PIPE) weigh(std::integral_constant<int, st>());
     };
 
     if constexpr (FAST) {
@@ -222,25 +233,28 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     }
     if (n_tiles > 0) {
         float b[2] = {0.0f, 0.0f};
+        constexpr int first = PIPE ? 2 : 1;   // tiles asked for beforehand
         if constexpr (BIAS) {
-            b[0] = bias_of(0);
-            b[1] = bias_of(1);
-            raw = bias_of(2);
+            for (int i = 0; i < first; ++i) b[i] = bias_of(i);
+            raw = bias_of(first);
         }
-        start_keys(0, 0, b[0]);
-        start_keys(1, 1, b[1]);
+        for (int i = 0; i < first; ++i) start_keys(i, i, b[i]);
+        if constexpr (!PIPE) start_values(0);
         if constexpr (BIAS) {
-            if (FAST && wave == 0) start_bias(3, 1);
+            if (FAST && wave == 0) start_bias(first + 1, (first + 1) & 1);
             for (int i = tid; i < 2 * KT; i += 64 * NW) bias_s[i / KT][1][i % KT] = Word{};
         }
-        // no values before the first: zeros, with weights of zero
-        for (int i = tid; i < TB / 16; i += 64 * NW)
-            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+        if constexpr (PIPE) {   // no values before the first: zeros, with weights of zero
+            for (int i = tid; i < TB / 16; i += 64 * NW)
+                *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < KT / KE; ++i) pf[1][i] = Frag{};
+            for (int i = 0; i < KT / KE; ++i) pf[1][i] = Frag{};
+        }
         load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, r < rows, lane);
-        all_arrived();
-        score(std::integral_constant<int, 0>());
+        if constexpr (PIPE) {
+            all_arrived();
+            score(std::integral_constant<int, 0>());
+        }
         int i = 0;
         for (;;) {
             step(std::integral_constant<int, 0>(), i);
@@ -248,9 +262,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             step(std::integral_constant<int, 1>(), i);
             if (++i == n_tiles) break;
         }
-        all_arrived();
-        if (n_tiles & 1) weigh(std::integral_constant<int, 0>());
-        else weigh(std::integral_constant<int, 1>());
+        all_arrived();   // no copy outlives its workgroup
+        if constexpr (PIPE) {
+            if (n_tiles & 1) weigh(std::integral_constant<int, 0>());
+            else weigh(std::integral_constant<int, 1>());
+        }
     }
 
     const float total = half_sum(l);

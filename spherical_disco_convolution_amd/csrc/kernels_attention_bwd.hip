@@ -21,16 +21,19 @@ namespace {
 constexpr int kStep = 32;   // keys (gq) or rows (gk, gv) of a step
 
 // A workgroup of NW waves has 32 rows a wave and walks over the keys of its part.
-// Three steps are under way in a wave: while the scores of step i become ds on the
-// vector units, the matrix cores take the scores and dp of step i + 1 and the
-// gradient's part of step i - 1.
+// bfloat16: three steps are under way in a wave: while the scores of step i become ds
+// on the vector units, the matrix cores take the scores and dp of step i + 1 and the
+// gradient's part of step i - 1.  float32 products take most of the time, so a step
+// goes through at once and leaves registers for the heads.
 template <typename T, int DP, int NW, bool BIAS, bool FAST>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_bwd_q(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
     typedef typename Addend<T>::Word Word;
     constexpr int KE = Op<T>::KE, NT = DP / 32, TR = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[6 * TB];   // four stages of keys, two of values
+    constexpr bool PIPE = sizeof(T) == 2;
+    constexpr int SK = PIPE ? 4 : 2;      // stages of keys; of values two
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[(SK + 2) * TB];
     __shared__ __attribute__((aligned(16))) Word bias_s[BIAS ? 2 : 1][2][kStep];
     __shared__ __attribute__((aligned(16))) float raw_s[BIAS && FAST ? 2 : 1][64];
     const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
             out |= __ballot(b == -kInf);
             if (wave == 0 && lane < kStep) bias_s[stage & 1][0][lane] = Addend<T>::pack(b);
         }
-        const uint32_t kat = base + (uint32_t)stage * TB, vat = base + (uint32_t)(4 + (stage & 1)) * TB;
+        const uint32_t kat = base + (uint32_t)(stage & (SK - 1)) * TB, vat = base + (uint32_t)(SK + (stage & 1)) * TB;
         if constexpr (FAST) {
             copy.start(knext, koff, kat, out, wave);
             copy.start(vnext, voff, vat, out, wave);
@@ -139,53 +142,60 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     rd.init(base, lane);
     typedef __attribute__((address_space(3))) Word lds_word;
     const uint32_t bbase = (uint32_t)(uintptr_t)(lds_word*)&bias_s[0][h][lane & 31];
-    floatx16 gq[NT], s[2], dp[2];
-    Frag sf[2][KB];
+    floatx16 gq[NT], s[PIPE ? 2 : 1], dp[PIPE ? 2 : 1];
+    Frag sf[PIPE ? 2 : 1][KB];
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) gq[d][e] = 0.0f;
 
     auto score = [&](auto stage_c) {
-        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        constexpr int st = decltype(stage_c)::value, sl = st & 1, p = PIPE ? sl : 0;
         s[p] = dp[p] = floatx16{};
-        if constexpr (BIAS) s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * p * kStep)));
+        if constexpr (BIAS) s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * sl * kStep)));
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), qf[c], s[p]);
+        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows((st & (SK - 1)) * TB, 0, c), qf[c], s[p]);
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((4 + p) * TB, 0, c), gf[c], dp[p]);
+        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((SK + sl) * TB, 0, c), gf[c], dp[p]);
     };
     auto collect = [&](auto stage_c) {
         constexpr int st = decltype(stage_c)::value;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int d = 0; d < NT; ++d) gq[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[st & 1][b], gq[d]);
+            for (int d = 0; d < NT; ++d) gq[d] = Op<T>::mma(rd.columns((st & (SK - 1)) * TB, b, d), sf[PIPE ? st & 1 : 0][b], gq[d]);
     };
     float raw = 0.0f;
     auto step = [&](auto stage_c, int i) {
-        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        constexpr int st = decltype(stage_c)::value, sl = st & 1, p = PIPE ? sl : 0;
+        constexpr int more = PIPE ? 2 : 1, nsl = PIPE ? sl : sl ^ 1;   // steps ahead, and the parity of that one
         const int k0 = (t0 + i) * kStep;
-        all_arrived();   // step i + 1; all waves have left the keys of i - 2 and the values of i
-        if constexpr (BIAS && !FAST) raw = bias_of(i + 2);
-        start(i + 2, (st + 2) & 3, raw);
+        // Here is step i + 1, and all waves have left the keys of i - 2 and the values of i
+        // (float32: step i is here, and all waves have left step i - 1).
+        all_arrived();
+        if constexpr (BIAS && !FAST) raw = bias_of(i + more);
+        start(i + more, (st + more) & 3, raw);
         if constexpr (BIAS && FAST) {
-            if (wave == 0) start_bias(i + 4, p);
-            raw = raw_s[p ^ 1][lane];   // of step i + 3
+            if (wave == 0) start_bias(i + more + 2, nsl);
+            raw = raw_s[nsl ^ 1][lane];   // of step i + more + 1
         }
+        if constexpr (!PIPE) score(std::integral_constant<int, st>());
         if (k0 + kStep > least) {   // some row does not see all of it
             const int room = lim - k0 - 4 * h;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 if (8 * (e / 4) + e % 4 >= room) s[p][e] = -kInf;
         }
-        score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
-        collect(std::integral_constant<int, (st + 3) & 3>());
+        if constexpr (PIPE) {
+            score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
+            collect(std::integral_constant<int, (st + 3) & 3>());
+        }
         floatx16 ds;
 #pragma unroll
         for (int e = 0; e < 16; ++e) ds[e] = exp2_fast(fmaf(s[p][e], scale2, -lse2)) * (dp[p][e] - delta);
 #pragma unroll
         for (int b = 0; b < KB; ++b) sf[p][b] = Op<T>::from(ds, b * KE / 2);
+        if constexpr (!PIPE) collect(std::integral_constant<int, st>());
     };
 
     if constexpr (FAST) {
@@ -195,37 +205,39 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     }
     if (n_steps > 0) {
         float b[2] = {0.0f, 0.0f};
+        constexpr int first = PIPE ? 2 : 1;   // steps asked for beforehand
         if constexpr (BIAS) {
-            b[0] = bias_of(0);
-            b[1] = bias_of(1);
-            raw = bias_of(2);
+            for (int i = 0; i < first; ++i) b[i] = bias_of(i);
+            raw = bias_of(first);
         }
-        start(0, 0, b[0]);
-        start(1, 1, b[1]);
+        for (int i = 0; i < first; ++i) start(i, i, b[i]);
         if constexpr (BIAS) {
-            if (FAST && wave == 0) start_bias(3, 1);
+            if (FAST && wave == 0) start_bias(first + 1, (first + 1) & 1);
             if (tid < 2 * kStep) bias_s[tid / kStep][1][tid % kStep] = Word{};
         }
-        // no step before the first: zeros
-        for (int i = tid; i < TB / 16; i += 64 * NW)
-            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+        if constexpr (PIPE) {   // no step before the first: zeros
+            for (int i = tid; i < TB / 16; i += 64 * NW)
+                *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < KB; ++i) sf[1][i] = Frag{};
-        all_arrived();
-        score(std::integral_constant<int, 0>());
+            for (int i = 0; i < KB; ++i) sf[1][i] = Frag{};
+            all_arrived();
+            score(std::integral_constant<int, 0>());
+        }
         int i = 0;
         for (;;) {
             step(std::integral_constant<int, 0>(), i);
             if (++i == n_steps) break;
             step(std::integral_constant<int, 1>(), i);
             if (++i == n_steps) break;
-            step(std::integral_constant<int, 2>(), i);
-            if (++i == n_steps) break;
-            step(std::integral_constant<int, 3>(), i);
-            if (++i == n_steps) break;
+            if constexpr (PIPE) {
+                step(std::integral_constant<int, 2>(), i);
+                if (++i == n_steps) break;
+                step(std::integral_constant<int, 3>(), i);
+                if (++i == n_steps) break;
+            }
         }
-        all_arrived();
-        switch (n_steps & 3) {
+        all_arrived();   // no copy outlives its workgroup
+        if constexpr (PIPE) switch (n_steps & 3) {
             case 0: collect(std::integral_constant<int, 3>()); break;
             case 1: collect(std::integral_constant<int, 0>()); break;
             case 2: collect(std::integral_constant<int, 1>()); break;
@@ -251,14 +263,17 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
 // A workgroup has 32 keys a wave and walks over the rows of all heads that read
 // its key head, in steps of 32.  Three steps are under way in a wave, as above: the
 // scores and dp of step i + 1, the weights of step i, the gradients' parts of
-// step i - 1.  -l and -delta of a row are the first summands of its scores and dp.
+// step i - 1.  -l and -delta of a row are the first summands of its scores and dp
+// (float32: they are added afterwards, where the sums are exact to their own size).
 template <typename T, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1) void attn_bwd_kv(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
     typedef typename Addend<T>::Word Word;
     constexpr int KE = Op<T>::KE, NT = DP / 32, TK = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * TB];   // four stages of queries, of gradients
+    constexpr bool PIPE = sizeof(T) == 2;
+    constexpr int SR = PIPE ? 4 : 2;   // stages
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SR * TB];   // of queries, of gradients
     // [stage][-l, -delta][values, zeros for the upper half of the lanes][row]
     __shared__ __attribute__((aligned(16))) Word add_s[2][2][2][kStep];
     __shared__ __attribute__((aligned(16))) float raw_s[2][2][64];
@@ -322,7 +337,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         int token;
         const int x0 = first_of(i, &token), r0 = (t0 + i) * kStep;
         const T *q = Q + (int64_t)token * a.q_ts, *o = O + (int64_t)token * a.go_ts;
-        const uint32_t qat = base + (uint32_t)stage * TB, oat = base + (uint32_t)(4 + stage) * TB;
+        const uint32_t qat = base + (uint32_t)stage * TB, oat = base + (uint32_t)(SR + stage) * TB;
         if constexpr (FAST) {
             if (!C::shares(wave)) return;
             const u32x4 qb = buffer_of(q), ob = buffer_of(o);
@@ -372,7 +387,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
     };
     auto put = [&](int i, int stage, float v) {   // by the first wave
         const bool ok = (t0 + i) * kStep + row < rows;
-        if (h == 0) v = !ok || v == -kInf ? -kInf : -v * per_scale;   // rows that see nothing weigh nothing
+        // rows that see nothing weigh nothing
+        if (h == 0) v = !ok || v == -kInf ? -kInf : -v * (PIPE ? per_scale : kLog2e);
         else v = ok ? -v : 0.0f;
         add_s[stage][h][0][row] = Addend<T>::pack(v);
     };
@@ -382,99 +398,125 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
     typedef __attribute__((address_space(3))) Word lds_word;
     const uint32_t abase = (uint32_t)(uintptr_t)(lds_word*)&add_s[0][0][h][row];
     constexpr uint32_t kAdd = (uint32_t)sizeof(Word) * 2 * kStep;
-    floatx16 gk[NT], gv[NT], s[2], dp[2];
-    Frag pf[2][KB], sf[2][KB];
+    floatx16 gk[NT], gv[NT], s[PIPE ? 2 : 1], dp[PIPE ? 2 : 1];
+    Frag pf[PIPE ? 2 : 1][KB], sf[PIPE ? 2 : 1][KB];
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) gk[d][e] = gv[d][e] = 0.0f;
 
     auto score = [&](auto stage_c) {
-        constexpr int st = decltype(stage_c)::value, p = st & 1;
-        s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p)));
-        dp[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p + 1)));
+        constexpr int st = decltype(stage_c)::value, p = PIPE ? st & 1 : 0;
+        if constexpr (PIPE) {
+            s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p)));
+            dp[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(abase + kAdd * (2 * p + 1)));
+        } else {
+            s[p] = dp[p] = floatx16{};
+        }
 #pragma unroll
         for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), kf[c], s[p]);
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((4 + st) * TB, 0, c), vf[c], dp[p]);
+        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((SR + st) * TB, 0, c), vf[c], dp[p]);
     };
     auto collect = [&](auto stage_c) {
-        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        constexpr int st = decltype(stage_c)::value, p = PIPE ? st & 1 : 0;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int d = 0; d < NT; ++d) {
-                gv[d] = Op<T>::mma(rd.columns((4 + st) * TB, b, d), pf[p][b], gv[d]);
+                gv[d] = Op<T>::mma(rd.columns((SR + st) * TB, b, d), pf[p][b], gv[d]);
                 gk[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[p][b], gk[d]);
             }
     };
     float raw = 0.0f;
     auto step = [&](auto stage_c, int i) {
-        constexpr int st = decltype(stage_c)::value, p = st & 1;
+        constexpr int st = decltype(stage_c)::value, sl = st & 1, p = PIPE ? sl : 0;
+        constexpr int more = PIPE ? 2 : 1, nsl = PIPE ? sl : sl ^ 1;   // steps ahead, and the parity of that one
         const int r0 = (t0 + i) * kStep;
-        all_arrived();   // step i + 1; all waves have left step i - 2
-        start(i + 2, (st + 2) & 3);
-        if constexpr (!FAST) raw = raw_of(i + 2);
-        if (wave == 0) put(i + 2, p, raw);
+        // Here is step i + 1, and all waves have left step i - 2 (float32: step i is here,
+        // and all waves have left step i - 1).
+        all_arrived();
+        start(i + more, (st + more) & (SR - 1));
+        if constexpr (!FAST) raw = raw_of(i + more);
+        if (wave == 0) put(i + more, nsl, raw);
         if constexpr (FAST) {
-            if (wave < 2) start_raw(i + 4, p);
-            raw = raw_s[p ^ 1][h][row];   // of step i + 3
+            if (wave < 2) start_raw(i + more + 2, nsl);
+            raw = raw_s[nsl ^ 1][h][row];   // of step i + more + 1
         }
+        if constexpr (!PIPE) score(std::integral_constant<int, st>());
         if (r0 < r_all) {   // some row does not see all keys of this wave
             const int hidden = r_mine - r0 - 4 * h;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 if (8 * (e / 4) + e % 4 < hidden) s[p][e] = -kInf;
         }
-        score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
-        collect(std::integral_constant<int, (st + 3) & 3>());
         floatx16 w, ds;
+        if constexpr (PIPE) {
+            score(std::integral_constant<int, (st + 1) & 3>());   // behind the last step: not used
+            collect(std::integral_constant<int, (st + 3) & 3>());
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            w[e] = exp2_fast(fmaf(s[p][e], scale2, bias));
-            ds[e] = w[e] * dp[p][e];
+            for (int e = 0; e < 16; ++e) {
+                w[e] = exp2_fast(fmaf(s[p][e], scale2, bias));
+                ds[e] = w[e] * dp[p][e];
+            }
+        } else {
+            const uint32_t at = (uint32_t)(uintptr_t)(lds_f32*)&add_s[sl][0][0][4 * h];
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+                const floatx4 l4 = *(const lds_f32x4*)(uintptr_t)(at + 32 * e4);
+                const floatx4 d4 = *(const lds_f32x4*)(uintptr_t)(at + kAdd + 32 * e4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[4 * e4 + e] = exp2_fast(fmaf(s[p][4 * e4 + e], scale2, bias + l4[e]));
+                    ds[4 * e4 + e] = w[4 * e4 + e] * (dp[p][4 * e4 + e] + d4[e]);
+                }
+            }
         }
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             pf[p][b] = Op<T>::from(w, b * KE / 2);
             sf[p][b] = Op<T>::from(ds, b * KE / 2);
         }
+        if constexpr (!PIPE) collect(std::integral_constant<int, st>());
     };
 
     if (n_steps > 0) {
-        const float a0 = raw_of(0), a1 = raw_of(1);
-        raw = raw_of(2);
-        start(0, 0);
-        start(1, 1);
-        if (wave == 0) {
-            put(0, 0, a0);
-            put(1, 1, a1);
+        constexpr int first = PIPE ? 2 : 1;   // steps asked for beforehand
+        float r[2] = {0.0f, 0.0f};
+        for (int i = 0; i < first; ++i) r[i] = raw_of(i);
+        raw = raw_of(first);
+        for (int i = 0; i < first; ++i) {
+            start(i, i);
+            if (wave == 0) put(i, i, r[i]);
         }
         if constexpr (FAST)
-            if (wave < 2) start_raw(3, 1);
+            if (wave < 2) start_raw(first + 1, (first + 1) & 1);
         if (tid < 4 * kStep) add_s[tid >> 6][(tid >> 5) & 1][1][tid & 31] = Word{};
-        // no step before the first: zeros
-        for (int i = tid; i < TB / 16; i += 64 * NW) {
-            *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
-            *(lds_u32x4*)(uintptr_t)(base + 7 * TB + 16 * i) = u32x4{0, 0, 0, 0};
-        }
+        if constexpr (PIPE) {   // no step before the first: zeros
+            for (int i = tid; i < TB / 16; i += 64 * NW) {
+                *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+                *(lds_u32x4*)(uintptr_t)(base + 7 * TB + 16 * i) = u32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-        for (int i = 0; i < KB; ++i) pf[1][i] = sf[1][i] = Frag{};
-        all_arrived();
-        score(std::integral_constant<int, 0>());
+            for (int i = 0; i < KB; ++i) pf[1][i] = sf[1][i] = Frag{};
+            all_arrived();
+            score(std::integral_constant<int, 0>());
+        }
         int i = 0;
         for (;;) {
             step(std::integral_constant<int, 0>(), i);
             if (++i == n_steps) break;
             step(std::integral_constant<int, 1>(), i);
             if (++i == n_steps) break;
-            step(std::integral_constant<int, 2>(), i);
-            if (++i == n_steps) break;
-            step(std::integral_constant<int, 3>(), i);
-            if (++i == n_steps) break;
+            if constexpr (PIPE) {
+                step(std::integral_constant<int, 2>(), i);
+                if (++i == n_steps) break;
+                step(std::integral_constant<int, 3>(), i);
+                if (++i == n_steps) break;
+            }
         }
-        all_arrived();
-        switch (n_steps & 3) {
+        all_arrived();   // no copy outlives its workgroup
+        if constexpr (PIPE) switch (n_steps & 3) {
             case 0: collect(std::integral_constant<int, 3>()); break;
             case 1: collect(std::integral_constant<int, 0>()); break;
             case 2: collect(std::integral_constant<int, 1>()); break;
