@@ -36,21 +36,21 @@ bool wide(const AttnArgs& a) {
 }
 
 // Parts of the axis that a workgroup walks over.  `tiles` workgroups of `steps`
-// steps of `us` each run `at_once` at a time; parts cost the writing and reading of
-// their float32 results, `bytes` a part, and a launch.  Sequences of a packed call
-// may be of any lengths: one of up to four times the mean is counted on, and its
-// last workgroup ends the call.
+// steps of `us` each run `at_once` at a time, with 3 us before and after; parts cost
+// the writing and reading of their float32 results, `bytes` a part, and a launch.
+// Sequences of a packed call may be of any lengths: one of several times the mean is
+// counted on, the more the more there are, and its last workgroup ends the call.
 // Gradient of 65 x 128 points, 8 heads of 64: 520 workgroups, 512 at once: one part
-// 447 us (gk, gv) and 324 us (gq), four 345 and 262, joined in 18 us.
+// 447 us (gk, gv) and 324 us (gq), four 345 and 262, joined in 16 us each.
 int parts(int64_t n_seq, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
+    const double longest = std::min((double)n_seq, 2.0 + 0.25 * n_seq);
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 256; s += s < 8 ? 1 : s / 4) {
-        if (s > 1 && steps / s < 4.0) break;
-        const double rounds = (double)ceil_div(tiles * s, at_once);
-        double t = rounds * (steps / s + 4.0);
-        if (n_seq > 1) t = std::max(t, 4.0 * steps / s + 4.0);
-        t = t * us + (s > 1 ? 8.0 + s * bytes / 2.5e6 : 0.0);
+        if (s > 1 && (steps / s * us < 1.5 || steps / s < 1.5)) break;
+        double t = (double)ceil_div(tiles * s, at_once) * (steps / s * us + 3.0);
+        if (n_seq > 1) t = std::max(t, longest * steps / s * us + 3.0);
+        if (s > 1) t += 8.0 + s * bytes / 2.5e6;
         if (s == 1 || t < 0.95 * least) {
             best = s;
             least = t;
@@ -63,8 +63,15 @@ struct Mean {   // of a sequence
     int64_t rows, keys;
 };
 Mean mean_of(const AttnArgs& a) { return {ceil_div(a.total_q, a.n_seq) * a.G, ceil_div(a.total_k, a.n_seq)}; }
-// float32 products take up to sixteen times as long, at a quarter of the waves' number
-double slower(const AttnArgs& a) { return (a.dtype == DISCO_F32 ? 3.0 : 1.0) * (std::max(a.dk, a.dv) > 64 ? 1.5 : 1.0); }
+
+// Microseconds of a step of 32 with `products` matrix products: float32 by the rate
+// of its products, bfloat16 as measured for two (forward), three (gq) and four (gk, gv)
+double step_us(const AttnArgs& a, int products) {
+    if (a.dtype == DISCO_F32) return 0.3 + 0.0073 * products * (a.dk + a.dv);
+    return (products == 2 ? 0.4 : products == 3 ? 0.6 : 0.86) * (std::max(a.dk, a.dv) > 64 ? 1.5 : 1.0);
+}
+
+double steps_of(const AttnArgs& a, int64_t n) { return (double)ceil_div(n, 32) * (a.causal ? 0.5 : 1.0); }
 
 }  // namespace
 
@@ -75,11 +82,7 @@ AttnPlan attn_plan_fwd(const AttnArgs& a) {
     p.waves = !p.fast || m.rows > 64 ? 4 : m.rows > 32 ? 2 : 1;
     const int64_t tiles = a.n_seq * ceil_div(m.rows, 32 * p.waves) * a.hkv;
     // more rows than that fill the chip: 129 x 256 points in two parts were no faster
-    if (tiles < 256)
-        p.splits = parts(a.n_seq, tiles, (double)ceil_div(m.keys, 32) * (a.causal ? 0.5 : 1.0), 0.4 * slower(a), 512,
-                         4.0 * a.total_q * a.hq * a.dv);
-    else
-        p.splits = 1;
+    p.splits = tiles >= 256 ? 1 : parts(a.n_seq, tiles, steps_of(a, m.keys), step_us(a, 2), 512, 4.0 * a.total_q * a.hq * a.dv);
     return p;
 }
 
@@ -88,8 +91,8 @@ AttnPlan attn_plan_bwd_q(const AttnArgs& a) {
     p.fast = wide(a);
     p.waves = 4;
     const Mean m = mean_of(a);
-    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.rows, 128) * a.hkv, (double)ceil_div(m.keys, 32) * (a.causal ? 0.5 : 1.0),
-                     0.6 * slower(a), a.dtype == DISCO_F32 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
+    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.rows, 128) * a.hkv, steps_of(a, m.keys), step_us(a, 3),
+                     a.dtype == DISCO_F32 && std::max(a.dk, a.dv) > 64 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
     return p;
 }
 
@@ -98,9 +101,11 @@ AttnPlan attn_plan_bwd_kv(const AttnArgs& a) {
     p.fast = wide(a);
     p.waves = 4;
     const Mean m = mean_of(a);
-    const bool one = a.dtype == DISCO_F32 || std::max(a.dk, a.dv) > 64;   // workgroup of a compute unit
-    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.keys, 128) * a.hkv, (double)ceil_div(m.rows, 32) * (a.causal ? 0.5 : 1.0),
-                     0.86 * slower(a) / (one ? 1.5 : 1.0), one ? 256 : 512, 4.0 * a.total_k * a.hkv * (a.dk + a.dv));
+    const int d = std::max(a.dk, a.dv);
+    const bool one = d > 64 || (d > 32 && a.dtype == DISCO_F32);   // workgroup of a compute unit
+    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.keys, 128) * a.hkv, steps_of(a, m.rows),
+                     step_us(a, 4) / (one && a.dtype != DISCO_F32 ? 1.5 : 1.0), one ? 256 : 512,
+                     4.0 * a.total_k * a.hkv * (a.dk + a.dv));
     return p;
 }
 

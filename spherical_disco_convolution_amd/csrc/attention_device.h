@@ -364,6 +364,13 @@ struct Copy {
     }
 };
 
+// Whether elements from e on of a head of d take part.  float32 products are worth
+// skipping; bfloat16 ones are not worth a branch between them.
+template <typename T>
+__device__ __forceinline__ bool worth(int e, int d) {
+    return sizeof(T) == 2 || e < d;
+}
+
 // bits n .. 63
 __device__ __forceinline__ uint64_t from_bit(int n) { return n >= 64 ? 0 : ~(uint64_t)0 << max(n, 0); }
 

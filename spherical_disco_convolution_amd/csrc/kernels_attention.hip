@@ -141,7 +141,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             x = floatx16{};
             if constexpr (BIAS) x = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * st * KT + 32 * kt)));
 #pragma unroll
-            for (int c = 0; c < DP / KE; ++c) x = Op<T>::mma(rd.rows(st * TB, kt, c), qf[c], x);
+            for (int c = 0; c < DP / KE; ++c)
+                if (worth<T>(c * KE, a.dk)) x = Op<T>::mma(rd.rows(st * TB, kt, c), qf[c], x);
         }
     };
     auto weigh = [&](auto stage_c) {
@@ -149,7 +150,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 #pragma unroll
         for (int b = 0; b < KT / KE; ++b)
 #pragma unroll
-            for (int d = 0; d < NT; ++d) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[PIPE ? st : 0][b], o[d]);
+            for (int d = 0; d < NT; ++d)
+                if (worth<T>(32 * d, a.dv)) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[PIPE ? st : 0][b], o[d]);
     };
     // scores to weights, and this lane's part of their sum
     auto soften = [&](const floatx16* x, Frag* w) -> float {

@@ -154,16 +154,19 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
         s[p] = dp[p] = floatx16{};
         if constexpr (BIAS) s[p] = Addend<T>::spread(*(const lds_word*)(uintptr_t)(bbase + (uint32_t)sizeof(Word) * (2 * sl * kStep)));
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows((st & (SK - 1)) * TB, 0, c), qf[c], s[p]);
+        for (int c = 0; c < DP / KE; ++c)
+            if (worth<T>(c * KE, a.dk)) s[p] = Op<T>::mma(rd.rows((st & (SK - 1)) * TB, 0, c), qf[c], s[p]);
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((SK + sl) * TB, 0, c), gf[c], dp[p]);
+        for (int c = 0; c < DP / KE; ++c)
+            if (worth<T>(c * KE, a.dv)) dp[p] = Op<T>::mma(rd.rows((SK + sl) * TB, 0, c), gf[c], dp[p]);
     };
     auto collect = [&](auto stage_c) {
         constexpr int st = decltype(stage_c)::value;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int d = 0; d < NT; ++d) gq[d] = Op<T>::mma(rd.columns((st & (SK - 1)) * TB, b, d), sf[PIPE ? st & 1 : 0][b], gq[d]);
+            for (int d = 0; d < NT; ++d)
+                if (worth<T>(32 * d, a.dk)) gq[d] = Op<T>::mma(rd.columns((st & (SK - 1)) * TB, b, d), sf[PIPE ? st & 1 : 0][b], gq[d]);
     };
     float raw = 0.0f;
     auto step = [&](auto stage_c, int i) {
@@ -414,9 +417,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
             s[p] = dp[p] = floatx16{};
         }
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), kf[c], s[p]);
+        for (int c = 0; c < DP / KE; ++c)
+            if (worth<T>(c * KE, a.dk)) s[p] = Op<T>::mma(rd.rows(st * TB, 0, c), kf[c], s[p]);
 #pragma unroll
-        for (int c = 0; c < DP / KE; ++c) dp[p] = Op<T>::mma(rd.rows((SR + st) * TB, 0, c), vf[c], dp[p]);
+        for (int c = 0; c < DP / KE; ++c)
+            if (worth<T>(c * KE, a.dv)) dp[p] = Op<T>::mma(rd.rows((SR + st) * TB, 0, c), vf[c], dp[p]);
     };
     auto collect = [&](auto stage_c) {
         constexpr int st = decltype(stage_c)::value, p = PIPE ? st & 1 : 0;
@@ -424,8 +429,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int d = 0; d < NT; ++d) {
-                gv[d] = Op<T>::mma(rd.columns((SR + st) * TB, b, d), pf[p][b], gv[d]);
-                gk[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[p][b], gk[d]);
+                if (worth<T>(32 * d, a.dv)) gv[d] = Op<T>::mma(rd.columns((SR + st) * TB, b, d), pf[p][b], gv[d]);
+                if (worth<T>(32 * d, a.dk)) gk[d] = Op<T>::mma(rd.columns(st * TB, b, d), sf[p][b], gk[d]);
             }
     };
     float raw = 0.0f;
