@@ -380,9 +380,11 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
  * left as they were.
  *  - causal != 0: query i of a sequence of Lq queries and Lk keys sees keys
  *    j <= i + Lk - Lq (the last query sees all keys).
- *  - key_bias [total_k] float32 or NULL; -inf, or anything below -1e30, leaves
- *    a key out, whatever k and v hold there.  It is a constant: no gradient.
+ *  - key_bias [total_k] float32 or NULL, at most 1e30; -inf, or anything below
+ *    -1e30, leaves a key out, whatever k and v hold there.  It is a constant: no
+ *    gradient.
  *  - a query that sees no key gets o = 0, lse = -inf and gradients of zero.
+ *  - values of v are at most 1e25: sums may be that much larger for a while.
  *  - what a causal query does not see has to be finite all the same: a NaN or an
  *    infinity there may reach queries up to 63 keys earlier.
  * float32 tensors are computed in float32; for bfloat16 ones products are of
@@ -391,9 +393,9 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
  * results are reproducible.  Any alignment and strides are taken; head sizes,
  * strides and addresses that are multiples of 16 bytes are much faster. */
 typedef struct disco_attention_desc {
-    int64_t total_q, total_k;       /* tokens of all sequences; tokens * heads < 2^31 - 4096 */
+    int64_t total_q, total_k;       /* tokens of all sequences; tokens * heads < 2^30 - 4096 */
     int32_t n_seq;                  /* >= 1 */
-    int32_t hq, hkv;                /* heads of q and o, of k and v; hkv divides hq */
+    int32_t hq, hkv;                /* heads of q and o (at most 65535), of k and v; hkv divides hq */
     int32_t dk, dv;                 /* sizes of a head of q and k, of v and o: 1..128 */
     int32_t dtype;                  /* of every tensor but lse and key_bias */
     int32_t causal;

@@ -850,14 +850,15 @@ def _result(t, name, shape, like):
     return (t,) + _tokens(t, name)[3:]
 
 
-def _floats(t, name, n):
-    """Pointer of an optional float32 vector of n values (of a batch's too)."""
+def _floats(t, name, n, lead=None):
+    """Pointer of an optional float32 vector of n values, or of a batch's [B, S]."""
     if t is None:
         return None
     if t.dtype != _torch().float32:
         raise ValueError(f"{name} must be float32")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} values without gaps")
+    shape = t.shape
+    if not ((len(shape) == 1 and shape[0] == n) or shape == lead) or not t.is_contiguous():
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {n} values without gaps")
     return t.data_ptr()
 
 
@@ -904,7 +905,7 @@ def _attention(q, k, v, key_bias, cu_q, cu_k, causal, scale):
     # what a float32 rounds to infinity is refused as infinity
     scale = scale if abs(scale) < 3e38 else math.inf
     return ((tq, tk, n_seq, hq, hkv, dk, dv, _dtype_code(q), 1 if causal else 0, scale, qts, qhs, kts, khs, vts, vhs),
-            _floats(key_bias, "key_bias", tk), _boundaries(cu_q, "cu_q", n_seq), _boundaries(cu_k, "cu_k", n_seq))
+            _floats(key_bias, "key_bias", tk, k.shape[:-2]), _boundaries(cu_q, "cu_q", n_seq), _boundaries(cu_k, "cu_k", n_seq))
 
 
 def attention_fwd(q, k, v, key_bias=None, cu_q=None, cu_k=None, causal: bool = False, scale: float | None = None,
@@ -957,7 +958,7 @@ def attention_bwd(q, k, v, o, lse, go, key_bias=None, cu_q=None, cu_k=None, caus
     go, gots, gohs = _result(go, "go", oshape, q)
     if lse.shape != q.shape[:-1]:
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {tuple(q.shape[:-1])}")
-    lptr = _floats(lse, "lse", lse.numel())
+    lptr = _floats(lse, "lse", -1, lse.shape)
     qs = ks = vs = (0, 0)
     if need_gq:
         gq, *qs = _result(gq, "gq", q.shape, q)

@@ -26,30 +26,30 @@ bool wide(const AttnArgs& a) {
     for (const void* p : {a.q, a.k, a.v, a.o, a.go, (const void*)a.out, (const void*)a.gq, (const void*)a.gk,
                           (const void*)a.gv})
         if (reinterpret_cast<uintptr_t>(p) % 16) return false;
-    const int64_t size = 16 / epc, reach = ((int64_t)1 << 31) / (64 * size);
+    const int64_t size = 16 / epc, far = ((int64_t)1 << 31) / size;   // elements
     for (int64_t s : {a.k_ts, a.v_ts})
-        if (s >= reach) return false;
+        if (s >= far / 64) return false;
     if (a.go)   // a step's rows of the gradient of k and v: up to 33 tokens of G heads
         for (const auto& s : {std::make_pair(a.q_ts, a.q_hs), std::make_pair(a.go_ts, a.go_hs)})
-            if (s.first >= reach || s.second >= reach / a.G) return false;
+            if (s.first >= far / 64 || s.second >= far || 33 * s.first + a.G * s.second + 128 >= far) return false;
     return true;
 }
 
 // Parts of the axis that a workgroup walks over.  `tiles` workgroups of `steps`
 // steps of `us` each run `at_once` at a time, with 3 us before and after; parts cost
 // the writing and reading of their float32 results, `bytes` a part, and a launch.
-// Sequences of a packed call may be of any lengths: one of several times the mean is
-// counted on, the more the more there are, and its last workgroup ends the call.
+// Sequences between boundaries may be of any lengths: one of several times the mean
+// is counted on, the more the more there are, and its last workgroup ends the call.
 // Gradient of 65 x 128 points, 8 heads of 64: 520 workgroups, 512 at once: one part
 // 447 us (gk, gv) and 324 us (gq), four 345 and 262, joined in 16 us each.
-int parts(int64_t n_seq, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
-    const double longest = std::min((double)n_seq, 2.0 + 0.25 * n_seq);
+int parts(const AttnArgs& a, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
+    const double longest = a.ragged ? std::min({(double)a.n_seq, 2.0 + 0.25 * a.n_seq, 8.0}) : 1.0;
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 256; s += s < 8 ? 1 : s / 4) {
         if (s > 1 && (steps / s * us < 1.5 || steps / s < 1.5)) break;
         double t = (double)ceil_div(tiles * s, at_once) * (steps / s * us + 3.0);
-        if (n_seq > 1) t = std::max(t, longest * steps / s * us + 3.0);
+        t = std::max(t, longest * steps / s * us + 3.0);
         if (s > 1) t += 8.0 + s * bytes / 2.5e6;
         if (s == 1 || t < 0.95 * least) {
             best = s;
@@ -82,7 +82,7 @@ AttnPlan attn_plan_fwd(const AttnArgs& a) {
     p.waves = !p.fast || m.rows > 64 ? 4 : m.rows > 32 ? 2 : 1;
     const int64_t tiles = a.n_seq * ceil_div(m.rows, 32 * p.waves) * a.hkv;
     // more rows than that fill the chip: 129 x 256 points in two parts were no faster
-    p.splits = tiles >= 256 ? 1 : parts(a.n_seq, tiles, steps_of(a, m.keys), step_us(a, 2), 512, 4.0 * a.total_q * a.hq * a.dv);
+    p.splits = tiles >= 256 ? 1 : parts(a, tiles, steps_of(a, m.keys), step_us(a, 2), 512, 4.0 * a.total_q * a.hq * a.dv);
     return p;
 }
 
@@ -91,7 +91,7 @@ AttnPlan attn_plan_bwd_q(const AttnArgs& a) {
     p.fast = wide(a);
     p.waves = 4;
     const Mean m = mean_of(a);
-    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.rows, 128) * a.hkv, steps_of(a, m.keys), step_us(a, 3),
+    p.splits = parts(a, a.n_seq * ceil_div(m.rows, 128) * a.hkv, steps_of(a, m.keys), step_us(a, 3),
                      a.dtype == DISCO_F32 && std::max(a.dk, a.dv) > 64 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
     return p;
 }
@@ -103,7 +103,7 @@ AttnPlan attn_plan_bwd_kv(const AttnArgs& a) {
     const Mean m = mean_of(a);
     const int d = std::max(a.dk, a.dv);
     const bool one = d > 64 || (d > 32 && a.dtype == DISCO_F32);   // workgroup of a compute unit
-    p.splits = parts(a.n_seq, a.n_seq * ceil_div(m.keys, 128) * a.hkv, steps_of(a, m.rows),
+    p.splits = parts(a, a.n_seq * ceil_div(m.keys, 128) * a.hkv, steps_of(a, m.rows),
                      step_us(a, 4) / (one && a.dtype != DISCO_F32 ? 1.5 : 1.0), one ? 256 : 512,
                      4.0 * a.total_k * a.hkv * (a.dk + a.dv));
     return p;
@@ -201,10 +201,11 @@ int check_desc(const disco_attention_desc* d, AttnArgs* a) {
     // a bias is taken in units of the raw score
     if (!(d->scale >= 1e-6f && d->scale <= 1e6f))
         return set_error(DISCO_EINVAL, "scale must lie in [1e-6, 1e6] (got %g)", (double)d->scale);
-    // rows of a tile are counted in 32 bits, tiles of a launch too
-    constexpr int64_t kMost = INT32_MAX - 4096;
+    if (d->hq > 65535) return set_error(DISCO_EUNSUPPORTED, "at most 65535 heads (got %d)", d->hq);
+    // rows of a tile are counted in 32 bits, the threads of a launch too
+    constexpr int64_t kMost = ((int64_t)1 << 30) - 4096;
     if (d->total_k > kMost || d->total_q > kMost || d->total_q * d->hq > kMost || d->total_k * d->hkv > kMost)
-        return set_error(DISCO_EUNSUPPORTED, "tokens times heads must stay below 2^31 - 4096");
+        return set_error(DISCO_EUNSUPPORTED, "tokens times heads must stay below 2^30 - 4096");
     *a = AttnArgs{};
     a->dtype = d->dtype;
     a->total_q = d->total_q;
@@ -229,7 +230,8 @@ int check_desc(const disco_attention_desc* d, AttnArgs* a) {
     return DISCO_OK;
 }
 
-int check_boundaries(const AttnArgs& a) {
+int check_boundaries(AttnArgs& a) {
+    a.ragged = a.n_seq > 1 && (a.cu_q || a.cu_k);
     if (a.cu_q == nullptr && a.total_q % a.n_seq)
         return set_error(DISCO_EINVAL, "without boundaries n_seq (%d) must divide total_q (%lld)", a.n_seq, (long long)a.total_q);
     if (a.cu_k == nullptr && a.total_k % a.n_seq)
@@ -270,12 +272,14 @@ int64_t disco_attention_fwd_workspace(const disco_attention_desc* desc) {
     AttnArgs a;
     const int rc = check_desc(desc, &a);
     if (rc != DISCO_OK) return rc;
-    a.plan = attn_plan_fwd(a);
-    const int64_t wide = fwd_bytes(a);
-    if (!a.plan.fast) return wide;
-    a.q_ts |= 1;   // addresses that are not multiples of 16 bytes are cut up like this
-    a.plan = attn_plan_fwd(a);
-    return std::max(wide, fwd_bytes(a));
+    int64_t most = 0;   // with boundaries or without; addresses that are not multiples of 16 bytes
+    for (int way = 0; way < 4; ++way) {
+        a.ragged = way & 1;
+        if (way & 2) a.q_ts |= 1;
+        a.plan = attn_plan_fwd(a);
+        most = std::max(most, fwd_bytes(a));
+    }
+    return most;
 }
 
 int disco_attention_fwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -315,9 +319,14 @@ int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc) {
     AttnArgs a;
     const int rc = check_desc(desc, &a);
     if (rc != DISCO_OK) return rc;
-    a.plan = attn_plan_bwd_q(a);
-    a.plan_kv = attn_plan_bwd_kv(a);
-    return bwd_delta_bytes(a) + bwd_part_bytes(a);
+    int64_t most = 0;
+    for (int way = 0; way < 2; ++way) {
+        a.ragged = way;
+        a.plan = attn_plan_bwd_q(a);
+        a.plan_kv = attn_plan_bwd_kv(a);
+        most = std::max(most, bwd_part_bytes(a));
+    }
+    return bwd_delta_bytes(a) + most;
 }
 
 int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,

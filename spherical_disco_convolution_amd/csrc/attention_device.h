@@ -83,7 +83,7 @@ struct Op<bf16_t> {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
     // elements e0 .. e0 + 7 of a product's result, rounded to bfloat16: the
-    // weights are at most 1 (2^8 while a maximum lags), so this costs each 2^-9
+    // weights are at most 1 (2^24 while a maximum lags); this costs each at most 2^-8 of itself
     static __device__ __forceinline__ Frag from(const floatx16& s, int e0) {
         u32x4 w;
 #pragma unroll
@@ -394,7 +394,7 @@ __device__ __forceinline__ Span span_of(const int32_t* cu, int s, int each, int 
 // sequences have equal counts.  With them tile `slot` belongs to the last
 // sequence s with first(s) per / T + s <= slot, which leaves every sequence the
 // tiles it needs and at most one that it does not: no list has to be built
-// beforehand.  Tokens times heads stay below 2^31 - 4096.
+// beforehand.  Tokens times heads stay below 2^30 - 4096.
 inline int64_t tile_slots(bool packed, int64_t total, int n_seq, int per, int T) {
     if (!packed) return n_seq * ((total / n_seq * per + T - 1) / T);
     return total * per / T + n_seq;

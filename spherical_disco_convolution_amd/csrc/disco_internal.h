@@ -251,7 +251,7 @@ struct AttnArgs {
     float *part, *part2, *part_lse;   // results of each split, workspace
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, go_ts, go_hs, gq_ts, gq_hs, gk_ts, gk_hs, gv_ts, gv_hs;
     int64_t total_q, total_k;
-    int n_seq, hq, hkv, G, dk, dv, causal;
+    int n_seq, hq, hkv, G, dk, dv, causal, ragged;   // ragged: sequences of lengths of their own
     int each_q, each_k;          // tokens of a sequence where there are no boundaries
     float scale;
     AttnPlan plan, plan_kv;      // of the call, and of its gradient of k and v

@@ -10,10 +10,10 @@ using namespace attn;
 
 namespace {
 
-// The running maximum may lag: weights of 2^60 keep as many digits as weights of
+// The running maximum may lag: weights of 2^24 keep as many digits as weights of
 // 1, in bfloat16 too.  So a tile's maximum is taken only where the sum of its
 // weights passes this bound, or where the row has seen no key yet.
-constexpr float kMostSum = 1.152921504606846976e18f;
+constexpr float kMostSum = 16777216.0f;
 
 // A workgroup of NW waves has 32 rows a wave and walks over the keys of its
 // part in tiles of KT: one pass with a reference close to the running maximum, and

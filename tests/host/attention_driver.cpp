@@ -131,6 +131,7 @@ int main() {
     expect(with([](auto& x) { x.scale = -1.0f; }), EI, "scale < 0");
     expect(with([](auto& x) { x.scale = INFINITY; }), EI, "scale infinite");
     expect(with([](auto& x) { x.total_q = INT32_MAX / 4; }), EU, "too many rows");
+    expect(with([](auto& x) { x.hq = x.hkv = 65536; }), EU, "too many heads");
     expect(with([](auto& x) { x.total_q = INT64_MAX; }), EU, "far too many rows");
     expect(with([](auto& x) { x.n_seq = 1 << 28; x.total_q = x.total_k = 0; }), EU, "too many sequences");
     expect(with([](auto& x) { x.q_stride[0] = -64; }), EI, "negative stride");

@@ -95,6 +95,8 @@ Q, K = (10, 4, 16), (12, 2, 16)
     "batch of views": lambda: sdc.attention_fwd(z(2, 12, 4, 16)[:, :10], z(2, *K), z(2, *K)),
     "strided elements": lambda: sdc.attention_fwd(z(10, 4, 32)[..., ::2], z(*K), z(*K)),
     "bias size": lambda: sdc.attention_fwd(z(*Q), z(*K), z(*K), key_bias=z(10)),
+    "bias of a batch turned": lambda: sdc.attention_fwd(z(2, 5, 4, 16), z(2, 6, 2, 16), z(2, 6, 2, 16), key_bias=z(6, 2)),
+    "weight of two dimensions": lambda: sdc.qk_norm_rope_fwd(z(*Q), z(10, 2, 16), q_weight=z(4, 4)),
     "bias type": lambda: sdc.attention_fwd(z(*Q), z(*K), z(*K), key_bias=z(12, dtype=BF16)),
     "boundary type": lambda: sdc.attention_fwd(z(*Q), z(*K), z(*K), cu_q=torch.tensor([0, 10])),
     "boundary counts": lambda: sdc.attention_fwd(z(*Q), z(*K), z(*K), cu_q=torch.tensor([0, 10], dtype=torch.int32),

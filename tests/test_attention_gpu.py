@@ -202,6 +202,19 @@ def test_scores_of_every_size(sdc, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_large_values_under_growing_scores(sdc, dtype):
+    # each tile's scores are larger than the last one's, by 2^9 a tile in the weights
+    q, k, v, go = inputs(25, 70, 900, 2, 2, 32, 32, dtype)
+    bias = torch.linspace(0, 100, 900, device="cuda")
+    v = (1e25 * v.float()).to(dtype)
+    opt = dict(key_bias=bias)
+    o, lse = sdc.attention_fwd(q, k, v, **opt)
+    want = attention(q, k, v, bias, [0, 70], [0, 900], False, 32 ** -0.5, dtype=dtype)
+    check("o", o, *want["o"])
+    check("lse", lse, *want["lse"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("off", [0, 1, 3])
 def test_columns_of_one_buffer(sdc, off, dtype):
     # q, k, v side by side in a projection's output, gradients side by side too; odd starts
@@ -235,16 +248,20 @@ def test_heads_first(sdc, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
-def test_a_batch_is_its_sequences(sdc, dtype):
-    b, t, s = 3, 77, 131
+@pytest.mark.parametrize("b,t,s", [(3, 77, 131), (40, 130, 130)])
+def test_a_batch_is_its_sequences(sdc, b, t, s, dtype):
+    # with boundaries the sums may be cut up for sequences of other lengths, so that each
+    # of the two is held against the formula, not against the other's bits
     q, k, v, go = inputs(16, b * t, b * s, 4, 2, 64, 64, dtype)
     bias = torch.rand(b * s, generator=gen(17), device="cuda")
-    a = run(sdc, q, k, v, go, bias=bias, cu_q=[0, t, 2 * t, 3 * t], cu_k=[0, s, 2 * s, 3 * s])
+    cu_q, cu_k = list(range(0, b * t + 1, t)), list(range(0, b * s + 1, s))
+    run(sdc, q, k, v, go, bias=bias, cu_q=cu_q, cu_k=cu_k)
     q4, k4, v4, go4 = (x.unflatten(0, (b, -1)) for x in (q, k, v, go))
     o, lse = sdc.attention_fwd(q4, k4, v4, key_bias=bias.view(b, s))
     got = (o, lse) + sdc.attention_bwd(q4, k4, v4, o, lse, go4, key_bias=bias)
-    for x, y in zip(got, a):
-        assert torch.equal(x.flatten(0, 1), y)
+    want = attention(q, k, v, bias, cu_q, cu_k, False, 64 ** -0.5, go, o.flatten(0, 1), lse.flatten(0, 1), dtype=dtype)
+    for n, x in zip(("o", "lse", "gq", "gk", "gv"), got):
+        check(n, x.flatten(0, 1), *want[n])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
