@@ -391,17 +391,22 @@ __device__ __forceinline__ Span span_of(const int32_t* cu, int s, int each, int 
 }
 
 // Tiles of T rows (a power of two), `per` rows a token.  Without boundaries the
-// sequences have equal counts.  With them tile `slot` belongs to the last
-// sequence s with first(s) per / T + s <= slot, which leaves every sequence the
-// tiles it needs and at most one that it does not: no list has to be built
-// beforehand.  Tokens times heads stay below 2^30 - 4096.
+// sequences have equal counts.  With them first(s) per / T + s tiles lie before
+// sequence s, which leaves every sequence the tiles it needs and at most one that
+// it does not: the launch needs no list and no lengths.  Tokens times heads stay
+// below 2^30 - 4096.
 inline int64_t tile_slots(bool packed, int64_t total, int n_seq, int per, int T) {
     if (!packed) return n_seq * ((total / n_seq * per + T - 1) / T);
     return total * per / T + n_seq;
 }
 
-__device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int total, int each, int per, int T, int slot, int* seq,
-                                       int* tile, int* tiles) {
+// Up to 64 sequences each workgroup counts the tiles before its own, a sequence a
+// lane, and those too many stand behind the last.  More are searched with the tiles
+// too many between the others, in groups of eight that are turned: at even distances
+// they would all meet the same compute units (256 sequences of 128 tokens, 8 heads
+// of 64: not turned 63 us, turned 41, counted 48, a dense batch 35).
+__device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int total, int each, int per, int T, int slot, int slots,
+                                       int* seq, int* tile, int* tiles) {
     if (cu == nullptr) {
         const int nt = (each * per + T - 1) / T;
         *seq = n_seq == 1 ? 0 : slot / nt;
@@ -409,16 +414,42 @@ __device__ __forceinline__ bool locate(const int32_t* cu, int n_seq, int total, 
         *tiles = nt;
         return *seq < n_seq;
     }
-    auto first = [&](int s) { return min(max(uniform(cu[s]), 0), total) * per / T + s; };
-    int lo = 0, hi = n_seq;      // first(lo) <= slot < first(hi), if the boundaries are in order
+    const int lane = threadIdx.x & 63;
+    if (n_seq <= 64) {
+        int n = 0;
+        if (lane < n_seq) {
+            const int a = min(max(cu[lane], 0), total), b = min(max(cu[lane + 1], a), total);
+            n = ((b - a) * per + T - 1) / T;
+        }
+        int sum = n;   // of the lanes up to this one
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int below = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += below;
+        }
+        const uint64_t here = __ballot(slot < sum);
+        if (!here) return false;
+        const int w = __builtin_ctzll(here);
+        *seq = w;
+        *tiles = __builtin_amdgcn_readlane(n, w);
+        *tile = slot - (__builtin_amdgcn_readlane(sum, w) - *tiles);
+        return *tile >= 0 && *tile < *tiles;   // boundaries out of order
+    }
+    if (slot < (slots & ~7)) slot = (slot & ~7) | ((slot + (((uint32_t)slot >> 3) * 0x9E3779B1u >> 29)) & 7);
+    // the lanes look at 64 sequences at a time: first(lo) <= slot < first(hi), if the
+    // boundaries are in order
+    auto first = [&](int at) { return min(max(at, 0), total) * per / T; };
+    int lo = 0, hi = n_seq;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first(mid) <= slot) lo = mid;
-        else hi = mid;
+        const int each_lane = (hi - lo + 63) >> 6, s = min(lo + lane * each_lane, hi - 1);
+        const uint64_t before = __ballot(lane == 0 || (lo + lane * each_lane < hi && first(cu[s]) + s <= slot));
+        const int n = before == ~(uint64_t)0 ? 64 : __builtin_ctzll(~before);
+        lo += (n - 1) * each_lane;
+        hi = min(hi, lo + each_lane);
     }
     const Span sp = span_of(cu, lo, 0, total);
     *seq = lo;
-    *tile = slot - first(lo);
+    *tile = slot - first(uniform(cu[lo])) - lo;
     *tiles = (sp.len * per + T - 1) / T;
     return *tile >= 0 && *tile < *tiles;
 }
@@ -443,7 +474,8 @@ __device__ __forceinline__ bool head_of(int id, int per_head, int hkv, int* head
     if (8 % hkv == 0) {
         const int share = 8 / hkv, x = id & 7;
         *head = x % hkv;
-        *idx = (id >> 3) * share + x / hkv;
+        const int j = id >> 3, y = x / hkv;   // there and back: tiles of falling sizes are shared evenly
+        *idx = j * share + (j & 1 ? share - 1 - y : y);
         return *idx < per_head;
     }
     *head = id % hkv;

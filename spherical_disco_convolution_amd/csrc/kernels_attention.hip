@@ -38,7 +38,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
     const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, &seq, &tile, &tiles)) return;
+    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
     if (a.causal) tile = tiles - 1 - tile;   // the longest rows first
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
     const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, &seq, &tile, &tiles)) return;
+    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
     if (a.causal) tile = tiles - 1 - tile;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
     int hk, idx, seq, tile, tiles;
     if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
     const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, slot, &seq, &tile, &tiles)) return;
+    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, slot, a.slots, &seq, &tile, &tiles)) return;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
