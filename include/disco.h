@@ -435,10 +435,10 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
  * from rot on do not turn.  positions [tokens, axes], int32 or float32 (times of a
  * series; colatitude and longitude of a point, where whole frequencies are
  * periodic in longitude); scaled tables for long series are the caller's
- * inv_freq.  Angles are taken in float64.  Heads are independent: a NaN stays in
- * its own. */
+ * inv_freq.  Angles are taken in float64, squares are summed in float32 (elements of at
+ * most 1e18).  Heads are independent: a NaN stays in its own. */
 typedef struct disco_qk_desc {
-    int64_t tokens;                 /* < 2^31 */
+    int64_t tokens;                 /* at most 2^26 - 64 */
     int32_t hq, hkv, d;             /* hkv may be 0; d in 1..256 */
     int32_t dtype;                  /* of every tensor but weights, positions and inv_freq */
     int32_t rot;                    /* elements that turn: even, 0..d */

@@ -392,8 +392,9 @@ static int qk_call(const disco_qk_desc* d, QkCall* c) {
         return set_error(DISCO_EINVAL, "sizes must be tokens >= 0, hq >= 1, hkv >= 0, d >= 1 (got %lld, %d, %d, %d)",
                          (long long)d->tokens, d->hq, d->hkv, d->d);
     if (d->d > 256) return set_error(DISCO_EUNSUPPORTED, "head sizes of at most 256 (got %d)", d->d);
-    if (d->tokens > INT32_MAX || (int64_t)d->hq + d->hkv > 65535)
-        return set_error(DISCO_EUNSUPPORTED, "at most 2^31 - 1 tokens and 65535 heads");
+    // up to 64 threads a token, and fewer than 2^32 of a launch
+    if (d->tokens > ((int64_t)1 << 26) - 64 || (int64_t)d->hq + d->hkv > 65535)
+        return set_error(DISCO_EUNSUPPORTED, "at most 2^26 - 64 tokens and 65535 heads");
     if (d->rot < 0 || d->rot % 2 || d->rot > d->d)
         return set_error(DISCO_EINVAL, "rot must be even and lie in 0..%d (got %d)", d->d, d->rot);
     if (d->axes < 1 || d->axes > 4) return set_error(DISCO_EINVAL, "positions have 1 to 4 axes (got %d)", d->axes);

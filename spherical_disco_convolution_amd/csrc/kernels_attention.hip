@@ -1,4 +1,16 @@
 // Attention over points or tokens, forward.
+//
+// 4 D operations a score against 2 / rows of a key's bytes: the matrix cores bound it
+// where there are more than a few hundred rows, with an exponential, two products
+// and a sum a score on the vector units beside them.  129 x 256 points, 8 heads of 64,
+// bf16: 2.9 ms, 0.76 PFLOP/s; the matrix cores take 39 percent of the cycles, the
+// vector units 60, and power holds the clock at 1.8 to 2.0 GHz.  Packed causal series
+// of 12001 tokens, 12 heads of 128 over 4: 0.15 ms, 0.74 PFLOP/s.  Few rows over many
+// keys are bound by the reading of the keys (8 points over 33024 keys, 34 MB: 20 us).
+//
+// Tried and not kept: 64 rows a wave (a third fewer reads of LDS, half the waves: 3.6
+// ms of the 2.9), registers for four waves a SIMD (spills: 5.4), four stages of tiles
+// instead of two (no gain), tiles of 64 keys at heads of 128 (spills).
 #include "attention_device.h"
 
 #include <algorithm>

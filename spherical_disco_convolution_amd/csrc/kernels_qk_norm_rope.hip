@@ -9,7 +9,10 @@
 // HBM bounds both: each element is read and written once.  A group of lanes
 // takes a token and walks over its heads, so that an angle is taken once for all
 // heads (in float64: a float32 product has lost the angle of position 10^6).  A
-// lane holds V pairs of a head in registers, between the sum and the output.
+// lane holds V pairs of a head in registers, between the sum and the output, and
+// the next heads are on their way meanwhile (without: 73 and 148 us).  33024 tokens of
+// 16 heads of 128, bf16: forward 66 us, 4.1 TB/s; gradient 99 us, 4.1 TB/s, and 4 us
+// for the weights' sums.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

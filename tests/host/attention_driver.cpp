@@ -244,7 +244,7 @@ int main() {
     expect(qk([](auto& x) { x.axes = 5; }), EI, "axes");
     expect(qk([](auto& x) { x.d = 257; }), EU, "large heads");
     expect(qk([](auto& x) { x.eps = NAN; }), EI, "eps");
-    expect(qk([](auto& x) { x.tokens = (int64_t)1 << 31; }), EU, "tokens");
+    expect(qk([](auto& x) { x.tokens = (int64_t)1 << 26; }), EU, "tokens");
     expect(qk([](auto& x) { x.hkv = 0; }), OK, "queries alone");
     expect(qk([](auto& x) { x.tokens = 0; }, nullptr, nullptr, nullptr), OK, "no tokens");
     qk(same);

@@ -106,10 +106,10 @@ def test_a_step_counter_in_a_graph(sdc):
         assert torch.equal(y, sdc.dropout_fwd(x, 0.5, 7, 100 + i))
 
 
-def test_past_2_31_elements(sdc):
-    n = (1 << 31) + 4099
+@pytest.mark.parametrize("n", [(1 << 31) + 4099, (1 << 34) + 4099])   # the last takes two launches
+def test_past_2_31_elements(sdc, n):
     x = torch.ones(n, dtype=BF16, device="cuda")
-    y = sdc.dropout_fwd(x, 0.5, 5, 6)
+    y = sdc.dropout_fwd(x, 0.5, 5, 6, y=x)
     # blocks at the far end, by a call whose counters the definition gives
     import numpy as np
     from attention_reference import philox
@@ -119,3 +119,5 @@ def test_past_2_31_elements(sdc):
     first = int(blocks[0]) * 8
     want = torch.from_numpy(h[:n - first].astype(np.int64) >= 32768)
     assert torch.equal(y[first:].cpu() != 0, want)
+    del x, y
+    torch.cuda.empty_cache()
