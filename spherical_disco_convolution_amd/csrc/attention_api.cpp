@@ -35,21 +35,16 @@ bool wide(const AttnArgs& a) {
     return true;
 }
 
-// Parts of the axis that a workgroup walks over.  `tiles` workgroups of `steps`
-// steps of `us` each run `at_once` at a time, with 3 us before and after; parts cost
-// the writing and reading of their float32 results, `bytes` a part, and a launch.
-// Sequences between boundaries may be of any lengths: one of several times the mean
-// is counted on, the more the more there are, and its last workgroup ends the call.
-// Gradient of 65 x 128 points, 8 heads of 64: 520 workgroups, 512 at once: one part
-// 447 us (gk, gv) and 324 us (gq), four 345 and 262, joined in 16 us each.
-int parts(const AttnArgs& a, int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
-    const double longest = a.ragged ? std::min({(double)a.n_seq, 2.0 + 0.25 * a.n_seq, 8.0}) : 1.0;
+// Parts of the keys in a forward call whose `tiles` workgroups of `steps` steps of `us`
+// do not fill the chip; `at_once` of them run together, with 3 us before and after.
+// Parts cost the writing and reading of their float32 results, `bytes` a part, and a
+// launch.
+int parts(int64_t tiles, double steps, double us, int64_t at_once, double bytes) {
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 256; s += s < 8 ? 1 : s / 4) {
         if (s > 1 && (steps / s * us < 1.5 || steps / s < 1.5)) break;
         double t = (double)ceil_div(tiles * s, at_once) * (steps / s * us + 3.0);
-        t = std::max(t, longest * steps / s * us + 3.0);
         if (s > 1) t += 8.0 + s * bytes / 2.5e6;
         if (s == 1 || t < 0.95 * least) {
             best = s;
@@ -57,6 +52,40 @@ int parts(const AttnArgs& a, int64_t tiles, double steps, double us, int64_t at_
         }
     }
     return best;
+}
+
+// The same for a gradient, whose tiles have up to `full` steps.  Equal ones are cut
+// alike (65 x 128 points, 8 heads of 64: 520 workgroups, 512 at once: one part 447 us
+// (gk, gv) and 324 us (gq), four 345 and 262, joined in 16 us each).  Where tiles have
+// steps of different number, causal ones or of packed sequences, a part has `chunk`
+// steps, and only tiles of more are cut: else one with all steps of a sequence of
+// several times the mean, which is counted on, ends the call (gk and gv of 7 causal
+// series of 6007 tokens, 12 heads of 128 over 4: one part 319 us, four 129).
+void cut(const AttnArgs& a, AttnPlan* p, int64_t tiles, int64_t full, double us, int64_t at_once, double bytes) {
+    p->splits = 1;
+    p->chunk = (int)std::max<int64_t>(full, 1);
+    if (!a.ragged && !a.causal) {
+        p->splits = parts(tiles, (double)full, us, at_once, bytes);
+        p->chunk = (int)std::max<int64_t>(ceil_div(full, p->splits), 1);
+        return;
+    }
+    // the longest sequence and the sum of squares of all, over the mean's
+    const double n = a.n_seq, far = a.ragged ? std::min({n, 1.5 + 0.15 * n, 4.0}) : 1.0;
+    const double skew = a.ragged ? (far * far + (n - far) * (n - far) / (n - 1.0)) / n : 1.0;
+    const double around = at_once > 256 ? 5.0 : 10.0;   // us before and after a workgroup's steps
+    const double even = tiles * (full * (a.causal ? 0.5 : 1.0) * us * skew + around) / at_once;
+    double least = 0.0;
+    for (int s = 1; s <= 8; ++s) {
+        const double chunk = std::ceil(full * far / s);
+        if (s > 1 && (chunk * us < 6.0 || s * bytes > 1e9)) break;
+        const double t = std::max(even + 0.35 * chunk * us, chunk * us + around) +
+                         (s > 1 ? 5.0 + s * bytes / 11e6 + (1.0 - 1.0 / s) * bytes / 2.5e6 + 2.0 * (s - 1) * tiles / at_once : 0.0);
+        if (s == 1 || t < 0.92 * least) {
+            p->splits = s;
+            p->chunk = (int)chunk;
+            least = t;
+        }
+    }
 }
 
 struct Mean {   // of a sequence
@@ -68,7 +97,8 @@ Mean mean_of(const AttnArgs& a) { return {ceil_div(a.total_q, a.n_seq) * a.G, ce
 // of its products, bfloat16 as measured for two (forward), three (gq) and four (gk, gv)
 double step_us(const AttnArgs& a, int products) {
     if (a.dtype == DISCO_F32) return 0.3 + 0.0073 * products * (a.dk + a.dv);
-    return (products == 2 ? 0.4 : products == 3 ? 0.6 : 0.86) * (std::max(a.dk, a.dv) > 64 ? 1.5 : 1.0);
+    const bool wide = std::max(a.dk, a.dv) > 64;
+    return products == 2 ? (wide ? 0.6 : 0.4) : products == 3 ? (wide ? 0.9 : 0.6) : wide ? 1.6 : 0.86;
 }
 
 double steps_of(const AttnArgs& a, int64_t n) { return (double)ceil_div(n, 32) * (a.causal ? 0.5 : 1.0); }
@@ -82,7 +112,7 @@ AttnPlan attn_plan_fwd(const AttnArgs& a) {
     p.waves = !p.fast || m.rows > 64 ? 4 : m.rows > 32 ? 2 : 1;
     const int64_t tiles = a.n_seq * ceil_div(m.rows, 32 * p.waves) * a.hkv;
     // more rows than that fill the chip: 129 x 256 points in two parts were no faster
-    p.splits = tiles >= 256 ? 1 : parts(a, tiles, steps_of(a, m.keys), step_us(a, 2), 512, 4.0 * a.total_q * a.hq * a.dv);
+    p.splits = tiles >= 256 ? 1 : parts(tiles, steps_of(a, m.keys), step_us(a, 2), 512, 4.0 * a.total_q * a.hq * a.dv);
     return p;
 }
 
@@ -91,8 +121,8 @@ AttnPlan attn_plan_bwd_q(const AttnArgs& a) {
     p.fast = wide(a);
     p.waves = 4;
     const Mean m = mean_of(a);
-    p.splits = parts(a, a.n_seq * ceil_div(m.rows, 128) * a.hkv, steps_of(a, m.keys), step_us(a, 3),
-                     a.dtype == DISCO_F32 && std::max(a.dk, a.dv) > 64 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
+    cut(a, &p, a.n_seq * ceil_div(m.rows, 128) * a.hkv, ceil_div(m.keys, 32), step_us(a, 3),
+        a.dtype == DISCO_F32 && std::max(a.dk, a.dv) > 64 ? 256 : 512, 4.0 * a.total_q * a.hq * a.dk);
     return p;
 }
 
@@ -103,9 +133,8 @@ AttnPlan attn_plan_bwd_kv(const AttnArgs& a) {
     const Mean m = mean_of(a);
     const int d = std::max(a.dk, a.dv);
     const bool one = d > 64 || (d > 32 && a.dtype == DISCO_F32);   // workgroup of a compute unit
-    p.splits = parts(a, a.n_seq * ceil_div(m.keys, 128) * a.hkv, steps_of(a, m.rows),
-                     step_us(a, 4) / (one && a.dtype != DISCO_F32 ? 1.5 : 1.0), one ? 256 : 512,
-                     4.0 * a.total_k * a.hkv * (a.dk + a.dv));
+    cut(a, &p, a.n_seq * ceil_div(m.keys, 128) * a.hkv, ceil_div(m.rows, 32),
+        step_us(a, 4), one ? 256 : 512, 4.0 * a.total_k * a.hkv * (a.dk + a.dv));
     return p;
 }
 
@@ -251,6 +280,9 @@ int64_t bwd_part_bytes(const AttnArgs& a) {
     return n;
 }
 
+// how many parts each row of gq, or of gk and gv, came in
+int64_t bwd_count_bytes(const AttnArgs& a) { return ceil_div(std::max(a.total_q * a.hq, a.total_k * a.hkv) * 4, 256) * 256; }
+
 int64_t bwd_delta_bytes(const AttnArgs& a) { return ceil_div(a.total_q * a.hq * 4, 256) * 256; }
 
 int need_workspace(const void* ws, int64_t have, int64_t need) {
@@ -326,7 +358,7 @@ int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc) {
         a.plan_kv = attn_plan_bwd_kv(a);
         most = std::max(most, bwd_part_bytes(a));
     }
-    return bwd_delta_bytes(a) + most;
+    return bwd_delta_bytes(a) + bwd_count_bytes(a) + most;
 }
 
 int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -365,7 +397,8 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
     if (nq == 0 && nk == 0) return DISCO_OK;
     a.plan = attn_plan_bwd_q(a);
     a.plan_kv = attn_plan_bwd_kv(a);
-    const int64_t delta = bwd_delta_bytes(a), need = delta + bwd_part_bytes(a), cu = (int64_t)(a.n_seq + 1) * 4;
+    const int64_t delta = bwd_delta_bytes(a), count = bwd_count_bytes(a), need = delta + count + bwd_part_bytes(a);
+    const int64_t cu = (int64_t)(a.n_seq + 1) * 4;
     if ((rc = need_workspace(workspace, workspace_bytes, need)) != DISCO_OK) return rc;
     const Arg args[] = {{"key_bias", key_bias, a.total_k * 4, 4, false},
                         {"cu_q", cu_q, cu, 4, false},
@@ -375,7 +408,8 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
     const bool outs[] = {false, false, false, false, true};
     if ((rc = check_tensors(rows, 8, args, 5, outs)) != DISCO_OK) return rc;
     a.delta = static_cast<float*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta);
+    a.count = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + delta);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta + count);
     return launch_attention_bwd(a, stream);
 }
 

@@ -234,7 +234,8 @@ int launch_orthogonalize(const OrthoCall& c, void* stream);
 // How a call is cut up: by its sizes, types and alignment alone.
 struct AttnPlan {
     int waves;        // of a workgroup, 32 rows (or keys) each
-    int splits;       // parts of the axis that a workgroup walks over
+    int splits;       // parts of the axis that a workgroup walks over (gradients: at most)
+    int chunk;        // gradients: steps of a part
     bool fast;        // 16-byte accesses
 };
 // Attention (kernels_attention.hip, kernels_attention_bwd.hip).  Strides are in
@@ -249,13 +250,14 @@ struct AttnArgs {
     const int32_t *cu_q, *cu_k;  // boundaries in device memory, or NULL: equal counts
     float* delta;                // [total_q, hq], workspace
     float *part, *part2, *part_lse;   // results of each split, workspace
+    int32_t* count;              // gradients: parts of each row, workspace
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, go_ts, go_hs, gq_ts, gq_hs, gk_ts, gk_hs, gv_ts, gv_hs;
     int64_t total_q, total_k;
     int n_seq, hq, hkv, G, dk, dv, causal, ragged;   // ragged: sequences of lengths of their own
     int each_q, each_k;          // tokens of a sequence where there are no boundaries
     float scale;
     AttnPlan plan, plan_kv;      // of the call, and of its gradient of k and v
-    int slots, splits;           // of one launch
+    int slots, splits, chunk;    // of one launch
 };
 AttnPlan attn_plan_fwd(const AttnArgs& a);
 AttnPlan attn_plan_bwd_q(const AttnArgs& a);

@@ -5,7 +5,7 @@
 // and a sum a score on the vector units beside them.  129 x 256 points, 8 heads of 64,
 // bf16: 2.9 ms, 0.76 PFLOP/s; the matrix cores take 39 percent of the cycles, the
 // vector units 60, and power holds the clock at 1.8 to 2.0 GHz.  Packed causal series
-// of 12001 tokens, 12 heads of 128 over 4: 0.15 ms, 0.74 PFLOP/s.  Few rows over many
+// of 12001 tokens, 12 heads of 128 over 4: 0.13 ms, 0.82 PFLOP/s.  Few rows over many
 // keys are bound by the reading of the keys (8 points over 33024 keys, 34 MB: 20 us).
 //
 // Tried and not kept: 64 rows a wave (a third fewer reads of LDS, half the waves: 3.6
@@ -48,10 +48,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
-    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
+    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, a.causal, &hk, &idx)) return;
     const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
-    if (a.causal) tile = tiles - 1 - tile;   // the longest rows first
+    if (!locate<GROWS>(a.causal, a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;

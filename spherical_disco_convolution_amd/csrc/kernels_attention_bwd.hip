@@ -11,9 +11,9 @@
 // the reads of LDS (each operand of gq, gk and gv is read by columns, at half the
 // width) and the vector units.  65 x 128 points, 8 heads of 64, bf16, in four parts:
 // gq 258 us (0.82 PFLOP/s of its three products), gk and gv 345 us (0.82 of four).
-// Packed causal series of 6007 tokens, 12 heads of 128 over 4: 79 and 122 us; there
+// Packed causal series of 6007 tokens, 12 heads of 128 over 4: 62 and 127 us; there
 // gk and gv of 128 leave one workgroup a compute unit (two workgroups by spilling: 435
-// us).  float32, 2 x 33 x 64 points, 4 heads of 32: 80 and 108 us at 0.09 PFLOP/s of
+// us), and nothing covers the 10 us in which one begins and ends.  float32, 2 x 33 x 64 points, 4 heads of 32: 80 and 108 us at 0.09 PFLOP/s of
 // the 0.15 that float32 products reach.
 //
 // The order of instructions is the compiler's: laid out as in the forward kernel,
@@ -31,6 +31,11 @@ using namespace attn;
 namespace {
 
 constexpr int kStep = 32;   // keys (gq) or rows (gk, gv) of a step
+
+// Parts of a tile of so many steps: a causal or packed call's tiles have few or many
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int steps) {
+    return a.splits == 1 ? 1 : min(max((steps + a.chunk - 1) / a.chunk, 1), a.splits);
+}
 
 // A workgroup of NW waves has 32 rows a wave and walks over the keys of its part.
 // bfloat16: three steps are under way in a wave: while the scores of step i become ds
@@ -52,13 +57,27 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
-    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
-    const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
-    if (a.causal) tile = tiles - 1 - tile;
+    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, a.causal, &hk, &idx)) return;
+    // the parts that only the longest tiles have go first
+    const int turn = a.splits == 1 ? 0 : idx / a.slots, slot = idx - turn * a.slots, split = a.splits - 1 - turn;
+    if (!locate<GROWS>(a.causal, a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, slot, a.slots, &seq, &tile, &tiles)) return;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
+
+    int most = lk, least = lk;
+    if (a.causal) {
+        int t_first, t_last, unused;
+        row_of(tile * TR, a.G, &t_first, &unused);
+        row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
+        most = uniform(min(max(t_last + ahead + 1, 0), lk));
+        least = uniform(min(max(t_first + ahead + 1, 0), lk));
+    }
+    const int all = (most + kStep - 1) / kStep;
+    const int parts = parts_of(a, all);
+    if (split >= parts) return;
+    const int t0 = (int)((int64_t)all * split / parts), t1 = (int)((int64_t)all * (split + 1) / parts);
+    const int n_steps = t1 - t0;
 
     const int r = tile * TR + wave * 32 + (lane & 31);
     int token, g;
@@ -86,28 +105,15 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
         }
     }
     delta = half_sum(delta);
-    if (split == 0 && h == 0 && mine) a.delta[tok * a.hq + head] = delta;
+    if (split == 0 && h == 0 && mine) {
+        a.delta[tok * a.hq + head] = delta;
+        if (a.splits > 1) a.count[tok * a.hq + head] = parts;
+    }
     if (!a.gq) return;   // only delta is wanted
     load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, mine, lane);
     // rows that see nothing have no gradient: their l is -inf
     const float lse = mine ? a.lse_in[tok * a.hq + head] : -kInf;
     const float lse2 = lse == -kInf ? kInf : lse * kLog2e;
-
-    int most = lk, least = lk;
-    if (a.causal) {
-        int t_first, t_last, unused;
-        row_of(tile * TR, a.G, &t_first, &unused);
-        row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
-        most = uniform(min(max(t_last + ahead + 1, 0), lk));
-        least = uniform(min(max(t_first + ahead + 1, 0), lk));
-    }
-    const int all = (most + kStep - 1) / kStep;
-    int t0 = 0, t1 = all;
-    if (a.splits > 1) {
-        t0 = (int)((int64_t)all * split / a.splits);
-        t1 = (int)((int64_t)all * (split + 1) / a.splits);
-    }
-    const int n_steps = t1 - t0;
 
     const float* B = BIAS ? a.bias + sk.first : nullptr;
     const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
@@ -270,7 +276,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = gq[d][4 * e4 + e] * a.scale;
-            if (a.splits > 1) store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dk, v);
+            if (parts > 1) store4<float, FAST>(part, 32 * d + 8 * e4 + 4 * h, a.dk, v);
             else store4<T, FAST>(out, 32 * d + 8 * e4 + 4 * h, a.dk, v);
         }
 }
@@ -296,23 +302,15 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
 
     int hk, idx, seq, tile, tiles;
-    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, &hk, &idx)) return;
-    const int slot = a.splits == 1 ? idx : idx / a.splits, split = idx - slot * a.splits;
-    if (!locate(a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, slot, a.slots, &seq, &tile, &tiles)) return;
+    if (!head_of(blockIdx.x, a.slots * a.splits, a.hkv, a.causal, &hk, &idx)) return;
+    // the parts that only the longest tiles have go first
+    const int turn = a.splits == 1 ? 0 : idx / a.slots, slot = idx - turn * a.slots, split = a.splits - 1 - turn;
+    if (!locate<SHRINKS>(a.causal, a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, slot, a.slots, &seq, &tile, &tiles)) return;
     const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q);
     const Span sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
     const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
 
     const int key0 = tile * TK + wave * 32, key = key0 + (lane & 31);
-    const int64_t tok = sk.first + key;
-    Frag kf[DP / KE], vf[DP / KE];
-    bool seen = key < lk;
-    float bias = 0.0f;
-    if (a.bias && seen) bias = bias2(a.bias[tok]);
-    seen = seen && bias != -kInf;
-    if (!seen) bias = -kInf;
-    load_columns<T, DP, FAST>(kf, (const T*)a.k + tok * a.k_ts + (int64_t)hk * a.k_hs, a.dk, seen, lane);
-    load_columns<T, DP, FAST>(vf, (const T*)a.v + tok * a.v_ts + (int64_t)hk * a.v_hs, a.dv, seen, lane);
     // the first row that sees the tile's first key, the first that sees this lane's key,
     // and the row from which on all of this wave's are seen
     int r_first = 0, r_mine = 0, r_all = 0;
@@ -322,11 +320,19 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         r_all = uniform(min(max(min(key0 + 31, lk - 1) - ahead, 0), sq.len) * a.G);
     }
     const int b0 = r_first / kStep, all = (rows + kStep - 1) / kStep - b0;
-    int t0 = b0, t1 = b0 + all;
-    if (a.splits > 1) {
-        t0 = b0 + (int)((int64_t)all * split / a.splits);
-        t1 = b0 + (int)((int64_t)all * (split + 1) / a.splits);
-    }
+    const int parts = parts_of(a, all);
+    if (split >= parts) return;
+    const int t0 = b0 + (int)((int64_t)all * split / parts), t1 = b0 + (int)((int64_t)all * (split + 1) / parts);
+    const int64_t tok = sk.first + key;
+    Frag kf[DP / KE], vf[DP / KE];
+    bool seen = key < lk;
+    if (a.splits > 1 && split == 0 && h == 0 && seen) a.count[tok * a.hkv + hk] = parts;
+    float bias = 0.0f;
+    if (a.bias && seen) bias = bias2(a.bias[tok]);
+    seen = seen && bias != -kInf;
+    if (!seen) bias = -kInf;
+    load_columns<T, DP, FAST>(kf, (const T*)a.k + tok * a.k_ts + (int64_t)hk * a.k_hs, a.dk, seen, lane);
+    load_columns<T, DP, FAST>(vf, (const T*)a.v + tok * a.v_ts + (int64_t)hk * a.v_hs, a.dv, seen, lane);
     const int n_steps = t1 - t0;
     const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
 
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
                 x[e] = gk[d][4 * e4 + e] * a.scale;
                 y[e] = gv[d][4 * e4 + e];
             }
-            if (a.splits > 1) {
+            if (parts > 1) {
                 store4<float, FAST>(pk, d0, a.dk, x);
                 store4<float, FAST>(pv, d0, a.dv, y);
             } else {
@@ -567,8 +573,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         }
 }
 
-// Sums of the parts of one or two tensors [tokens, heads, d], V elements a thread;
-// tokens of no sequence stay as they are.
+// Sums of the parts of one or two tensors [tokens, heads, d], V elements a thread.
+// What came in one part is there already; tokens of no sequence stay as they are.
 struct Parts {
     const float* part;
     void* out;
@@ -577,13 +583,15 @@ struct Parts {
 };
 
 template <typename T, int V>
-__global__ __launch_bounds__(256) void attn_sum(Parts a, Parts b, int64_t total, int heads, int splits, const int32_t* cu,
-                                                int n_seq) {
+__global__ __launch_bounds__(256) void attn_sum(Parts a, Parts b, const int32_t* count, int64_t total, int heads, int splits,
+                                                const int32_t* cu, int n_seq) {
     const Parts p = blockIdx.y == 0 ? a : b;
     const int groups = (p.d + V - 1) / V;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, cell = id / groups, tok = cell / heads;
     const int d0 = (int)(id - cell * groups) * V, head = (int)(cell - tok * heads);
     if (tok >= total || (cu && (tok < cu[0] || tok >= cu[n_seq]))) return;
+    splits = min(count[cell], splits);   // boundaries out of order leave it undefined
+    if (splits <= 1) return;
     const int64_t stride = total * heads * p.d;
     const float* q = p.part + cell * p.d + d0;
     float v[V] = {};
@@ -598,13 +606,13 @@ __global__ __launch_bounds__(256) void attn_sum(Parts a, Parts b, int64_t total,
 }
 
 template <typename T>
-void sum_parts(const Parts& x, const Parts& y, int64_t total, int heads, int splits, const int32_t* cu, int n_seq,
+void sum_parts(const Parts& x, const Parts& y, const int32_t* count, int64_t total, int heads, int splits, const int32_t* cu, int n_seq,
                hipStream_t st) {
     KernelTimer timer("attn_sum", st);
     const int v = x.d % 4 || y.d % 4 ? 1 : 4;
     const dim3 grid((unsigned)((total * heads * (std::max(x.d, y.d) / v) + 255) / 256), y.out ? 2 : 1);
-    if (v == 4) attn_sum<T, 4><<<grid, 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
-    else attn_sum<T, 1><<<grid, 256, 0, st>>>(x, y, total, heads, splits, cu, n_seq);
+    if (v == 4) attn_sum<T, 4><<<grid, 256, 0, st>>>(x, y, count, total, heads, splits, cu, n_seq);
+    else attn_sum<T, 1><<<grid, 256, 0, st>>>(x, y, count, total, heads, splits, cu, n_seq);
 }
 
 template <typename T, int DP, bool FAST>
@@ -612,6 +620,7 @@ int bwd_go(AttnArgs a, hipStream_t st) {
     constexpr int NW = 4;
     a.slots = (int)tile_slots(a.cu_q != nullptr, a.total_q, a.n_seq, a.G, 32 * NW);
     a.splits = a.gq ? a.plan.splits : 1;
+    a.chunk = a.plan.chunk;
     if (a.total_q > 0) {   // delta, which gk and gv need too
         KernelTimer timer("attn_bwd_q", st);
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
@@ -619,10 +628,11 @@ int bwd_go(AttnArgs a, hipStream_t st) {
         else attn_bwd_q<T, DP, NW, false, FAST><<<grid, 64 * NW, 0, st>>>(a);
     }
     if (a.splits > 1)
-        sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);
+        sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.count, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);
     if (a.gk && a.total_k > 0) {
         a.slots = (int)tile_slots(a.cu_k != nullptr, a.total_k, a.n_seq, 1, 32 * NW);
         a.splits = a.plan_kv.splits;
+        a.chunk = a.plan_kv.chunk;
         a.part2 = a.part + (size_t)a.splits * a.total_k * a.hkv * a.dk;
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
         {
@@ -630,8 +640,8 @@ int bwd_go(AttnArgs a, hipStream_t st) {
             attn_bwd_kv<T, DP, NW, FAST><<<grid, 64 * NW, 0, st>>>(a);
         }
         if (a.splits > 1)
-            sum_parts<T>({a.part, a.gk, a.gk_ts, a.gk_hs, a.dk}, {a.part2, a.gv, a.gv_ts, a.gv_hs, a.dv}, a.total_k, a.hkv,
-                         a.splits, a.cu_k, a.n_seq, st);
+            sum_parts<T>({a.part, a.gk, a.gk_ts, a.gk_hs, a.dk}, {a.part2, a.gv, a.gv_ts, a.gv_hs, a.dv}, a.count, a.total_k,
+                         a.hkv, a.splits, a.cu_k, a.n_seq, st);
     }
     return attn_launched("attention_bwd");
 }

@@ -247,6 +247,18 @@ def test_heads_first(sdc, dtype):
     run(sdc, q, k1, v1, go)
 
 
+# 64 sequences are counted, more are searched; causal tiles go by their steps
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,causal", [(63, True), (64, True), (65, True), (64, False), (300, True), (300, False)])
+def test_many_sequences(sdc, n, causal, dtype):
+    r = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 60, (2, n), generator=r) * (torch.rand(2, n, generator=r) < 0.8)
+    lens[:, 2] = 300
+    cu_q, cu_k = ([0] + x.cumsum(0).tolist() for x in lens)
+    q, k, v, go = inputs(n, cu_q[-1], cu_k[-1], 3, 1, 32, 32, dtype)
+    run(sdc, q, k, v, go, cu_q=cu_q, cu_k=cu_k, causal=causal)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("b,t,s", [(3, 77, 131), (40, 130, 130)])
 def test_a_batch_is_its_sequences(sdc, b, t, s, dtype):
