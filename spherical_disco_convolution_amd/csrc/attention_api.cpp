@@ -75,7 +75,7 @@ void cut(const AttnArgs& a, AttnPlan* p, int64_t tiles, int64_t full, double us,
     const double around = at_once > 256 ? 5.0 : 10.0;   // us before and after a workgroup's steps
     const double even = tiles * (full * (a.causal ? 0.5 : 1.0) * us * skew + around) / at_once;
     double least = 0.0;
-    for (int s = 1; s <= 8; ++s) {
+    for (int s = 1; s <= 256; s += s < 8 ? 1 : s / 4) {
         const double chunk = std::ceil(full * far / s);
         if (s > 1 && (chunk * us < 6.0 || s * bytes > 1e9)) break;
         const double t = std::max(even + 0.35 * chunk * us, chunk * us + around) +
@@ -304,10 +304,9 @@ int64_t disco_attention_fwd_workspace(const disco_attention_desc* desc) {
     AttnArgs a;
     const int rc = check_desc(desc, &a);
     if (rc != DISCO_OK) return rc;
-    int64_t most = 0;   // with boundaries or without; addresses that are not multiples of 16 bytes
-    for (int way = 0; way < 4; ++way) {
-        a.ragged = way & 1;
-        if (way & 2) a.q_ts |= 1;
+    int64_t most = 0;   // addresses that are not multiples of 16 bytes are cut up like odd strides
+    for (int way = 0; way < 2; ++way) {
+        if (way) a.q_ts |= 1;
         a.plan = attn_plan_fwd(a);
         most = std::max(most, fwd_bytes(a));
     }
@@ -351,9 +350,9 @@ int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc) {
     AttnArgs a;
     const int rc = check_desc(desc, &a);
     if (rc != DISCO_OK) return rc;
-    int64_t most = 0;
+    int64_t most = 0;   // with boundaries or without
     for (int way = 0; way < 2; ++way) {
-        a.ragged = way;
+        a.ragged = way && a.n_seq > 1;
         a.plan = attn_plan_bwd_q(a);
         a.plan_kv = attn_plan_bwd_kv(a);
         most = std::max(most, bwd_part_bytes(a));

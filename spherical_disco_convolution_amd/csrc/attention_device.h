@@ -90,6 +90,15 @@ struct Op<bf16_t> {
         for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[e0 + 2 * i], s[e0 + 2 * i + 1]);
         return __builtin_bit_cast(Frag, w);
     }
+    // what that rounding left behind
+    static __device__ __forceinline__ Frag rest(const floatx16& s, int e0, Frag rounded) {
+        const u32x4 r = __builtin_bit_cast(u32x4, rounded);
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16(s[e0 + 2 * i] - __uint_as_float(r[i] << 16), s[e0 + 2 * i + 1] - __uint_as_float(r[i] & 0xffff0000u));
+        return __builtin_bit_cast(Frag, w);
+    }
 };
 
 template <>

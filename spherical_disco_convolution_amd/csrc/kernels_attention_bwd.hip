@@ -42,7 +42,13 @@ __device__ __forceinline__ int parts_of(const AttnArgs& a, int steps) {
 // on the vector units, the matrix cores take the scores and dp of step i + 1 and the
 // gradient's part of step i - 1.  float32 products take most of the time, so a step
 // goes through at once and leaves registers for the heads.
-template <typename T, int DP, int NW, bool BIAS, bool FAST>
+//
+// FINE, for queries of up to 32 elements in bfloat16: ds goes into its product in two
+// bfloat16 parts (16 bits).  The few keys that such a row weighs most point the same way,
+// and as the ds of a row add up to nothing their parts of gq cancel: with one part the
+// error was 1.5 to 1.8 times that of rounding the result alone, where heads of 64 have
+// 1.4 (65 x 128 points, 8 heads of 32: one part 168 us, two 224).
+template <typename T, int DP, int NW, bool BIAS, bool FAST, bool FINE>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_bwd_q(AttnArgs a) {
     typedef Tile<T, DP> L;
     typedef typename Op<T>::Frag Frag;
@@ -160,10 +166,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     rd.init(base, lane);
     typedef __attribute__((address_space(3))) Word lds_word;
     const uint32_t bbase = (uint32_t)(uintptr_t)(lds_word*)&bias_s[0][h][lane & 31];
-    floatx16 gq[NT], s[PIPE ? 2 : 1], dp[PIPE ? 2 : 1];
-    Frag sf[PIPE ? 2 : 1][KB];
+    constexpr int NQ = FINE ? 1 : NT;   // tiles of a query's elements
+    floatx16 gq[NQ], s[PIPE ? 2 : 1], dp[PIPE ? 2 : 1];
+    Frag sf[PIPE ? 2 : 1][KB], sr[FINE ? 2 : 1][FINE ? KB : 1];
 #pragma unroll
-    for (int d = 0; d < NT; ++d)
+    for (int d = 0; d < NQ; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) gq[d][e] = 0.0f;
 
@@ -183,8 +190,12 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int d = 0; d < NT; ++d)
-                if (worth<T>(32 * d, a.dk)) gq[d] = Op<T>::mma(rd.columns((st & (SK - 1)) * TB, b, d), sf[PIPE ? st & 1 : 0][b], gq[d]);
+            for (int d = 0; d < NQ; ++d)
+                if (worth<T>(32 * d, a.dk)) {
+                    const Frag k = rd.columns((st & (SK - 1)) * TB, b, d);
+                    gq[d] = Op<T>::mma(k, sf[PIPE ? st & 1 : 0][b], gq[d]);
+                    if constexpr (FINE) gq[d] = Op<T>::mma(k, sr[st & 1][b], gq[d]);
+                }
     };
     float raw = 0.0f;
     auto step = [&](auto stage_c, int i) {
@@ -215,7 +226,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
 #pragma unroll
         for (int e = 0; e < 16; ++e) ds[e] = exp2_fast(fmaf(s[p][e], scale2, -lse2)) * (dp[p][e] - delta);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) sf[p][b] = Op<T>::from(ds, b * KE / 2);
+        for (int b = 0; b < KB; ++b) {
+            sf[p][b] = Op<T>::from(ds, b * KE / 2);
+            if constexpr (FINE) sr[p][b] = Op<T>::rest(ds, b * KE / 2, sf[p][b]);
+        }
         if constexpr (!PIPE) collect(std::integral_constant<int, st>());
     };
 
@@ -240,7 +254,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
             for (int i = tid; i < TB / 16; i += 64 * NW)
                 *(lds_u32x4*)(uintptr_t)(base + 3 * TB + 16 * i) = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < KB; ++i) sf[1][i] = Frag{};
+            for (int i = 0; i < KB; ++i) {
+                sf[1][i] = Frag{};
+                if constexpr (FINE) sr[1][i] = Frag{};
+            }
             all_arrived();
             score(std::integral_constant<int, 0>());
         }
@@ -270,7 +287,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
     float* part = a.part + (((int64_t)split * a.total_q + tok) * a.hq + head) * a.dk;
     T* out = (T*)a.gq + tok * a.gq_ts + (int64_t)head * a.gq_hs;
 #pragma unroll
-    for (int d = 0; d < NT; ++d)
+    for (int d = 0; d < NQ; ++d)
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4) {
             float v[4];
@@ -624,8 +641,14 @@ int bwd_go(AttnArgs a, hipStream_t st) {
     if (a.total_q > 0) {   // delta, which gk and gv need too
         KernelTimer timer("attn_bwd_q", st);
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
-        if (a.bias) attn_bwd_q<T, DP, NW, true, FAST><<<grid, 64 * NW, 0, st>>>(a);
-        else attn_bwd_q<T, DP, NW, false, FAST><<<grid, 64 * NW, 0, st>>>(a);
+        constexpr bool TWO = sizeof(T) == 2;
+        if (DP == 32 || (TWO && a.dk <= 32)) {
+            if (a.bias) attn_bwd_q<T, DP, NW, true, FAST, TWO><<<grid, 64 * NW, 0, st>>>(a);
+            else attn_bwd_q<T, DP, NW, false, FAST, TWO><<<grid, 64 * NW, 0, st>>>(a);
+        } else if constexpr (DP > 32) {
+            if (a.bias) attn_bwd_q<T, DP, NW, true, FAST, false><<<grid, 64 * NW, 0, st>>>(a);
+            else attn_bwd_q<T, DP, NW, false, FAST, false><<<grid, 64 * NW, 0, st>>>(a);
+        }
     }
     if (a.splits > 1)
         sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.count, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);

@@ -247,6 +247,14 @@ def test_heads_first(sdc, dtype):
     run(sdc, q, k1, v1, go)
 
 
+# causal: tiles of few and of many steps, in parts
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("lq,lk", [(1, 1), (1, 3001), (5, 5000), (700, 2900), (1500, 1500), (2500, 5), (2500, 1)])
+def test_causal_lengths(sdc, lq, lk, dtype):
+    q, k, v, go = inputs(lq * 5 + lk, lq, lk, 4, 2, 64, 64, dtype)
+    run(sdc, q, k, v, go, causal=True)
+
+
 # 64 sequences are counted, more are searched; causal tiles go by their steps
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("n,causal", [(63, True), (64, True), (65, True), (64, False), (300, True), (300, False)])
