@@ -9,8 +9,8 @@
 //
 // HBM bounds it where the generator stays below the memory's time: ten rounds of
 // two 64-bit products serve eight elements, a thread's own.  128 x 721 x 1440 bf16
-// joined to a residual: 132 us, 6.0 TB/s; a float32 gradient of 16383 x 2047: 44 us,
-// 6.1 TB/s.
+// joined to a residual: 132 us, 6.0 TB/s; a float32 gradient of 16383 x 2047: 53 us,
+// 5.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
