@@ -408,3 +408,23 @@ def test_far_rows(sdc, dtype):
     o, lse = sdc.attention_fwd(*small[:3], causal=True)
     want = (o, lse) + sdc.attention_bwd(*small[:3], o, lse, small[3], causal=True)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_host_memory_is_refused(sdc):
+    q, k, v, go = inputs(3, 20, 30, 2, 2, 32, 32, F32)
+    cu_q, cu_k, bias = dev([0, 20]), dev([0, 30]), torch.zeros(30, device="cuda")
+    o, lse = sdc.attention_fwd(q, k, v, bias, cu_q, cu_k)
+    calls = [lambda: sdc.attention_fwd(q, k, v, bias, cu_q.cpu(), cu_k),
+             lambda: sdc.attention_fwd(q, k, v, bias, cu_q, cu_k.cpu()),
+             lambda: sdc.attention_fwd(q, k, v, bias.cpu(), cu_q, cu_k),
+             lambda: sdc.attention_fwd(q, k.cpu(), v, bias, cu_q, cu_k),
+             lambda: sdc.attention_bwd(q, k, v, o, lse.cpu(), go, bias, cu_q, cu_k),
+             lambda: sdc.attention_bwd(q, k, v, o, lse, go.cpu(), bias, cu_q, cu_k),
+             lambda: sdc.qk_norm_rope_fwd(q, q, positions=torch.zeros(20, dtype=torch.int32),
+                                          inv_freq=torch.ones(16, device="cuda")),
+             lambda: sdc.qk_norm_rope_fwd(q, q, torch.ones(32)),
+             lambda: sdc.dropout_fwd(q, 0.5, 1, step=torch.zeros(1, dtype=torch.int64))]
+    for call in calls:
+        with pytest.raises(ValueError, match="device"):
+            call()
+    torch.cuda.synchronize()
