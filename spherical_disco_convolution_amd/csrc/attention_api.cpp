@@ -270,7 +270,8 @@ int check_boundaries(AttnArgs& a) {
 
 int64_t fwd_bytes(const AttnArgs& a) {
     const int64_t splits = a.plan.splits;
-    return splits > 1 ? ceil_div(splits * a.total_q * a.hq * (a.dv + 1) * 4, 16) * 16 : 0;
+    // results, references and sums of each part
+    return splits > 1 ? ceil_div(splits * a.total_q * a.hq * (a.dv + 2) * 4, 16) * 16 : 0;
 }
 
 int64_t bwd_part_bytes(const AttnArgs& a) {

@@ -553,6 +553,28 @@ __device__ __forceinline__ void row_of(int r, int G, int* token, int* head) {
     *head = r - *token * G;
 }
 
+// What the exponents of a row are taken from, in units of log 2: weights are
+// exp2(fma(x - raw, scale2, -two)).  `two` is m * scale2 rounded, whose error all of a
+// row's weights share, 2^-4 at most below kFarTwo.  Above, where the error passes the
+// range of an exponential (2^9 at a bias of -1e10), m itself is subtracted: the
+// largest score's exponent is then exactly 0.
+constexpr float kFarTwo = 1048576.0f;
+struct Reference {
+    float raw, two;
+};
+__device__ __forceinline__ Reference reference_of(float m, float scale2, float far) {   // far: kFarTwo / scale2
+    if (fabsf(m) < far) return {0.0f, m * scale2};
+    return {m == -kInf ? 0.0f : m, 0.0f};
+}
+// what weights under `from` are multiplied with to stand under `to`
+__device__ __forceinline__ float change_of(Reference from, Reference to, float scale2) {
+    return exp2_fast(fmaf(from.raw - to.raw, scale2, from.two - to.two));
+}
+// the logarithm of a sum of weights
+__device__ __forceinline__ float log_of(Reference r, float scale, float sum) {
+    return sum == 0.0f ? -kInf : fmaf(r.raw, scale, r.two * kLn2 + logf(sum));
+}
+
 __device__ __forceinline__ float bias2(float b) {   // in units of log 2
     return b < kLowest ? -kInf : b * kLog2e;
 }

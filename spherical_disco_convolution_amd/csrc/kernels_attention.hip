@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     const T* K = (const T*)a.k + sk.first * a.k_ts + (int64_t)hk * a.k_hs;
     const T* V = (const T*)a.v + sk.first * a.v_ts + (int64_t)hk * a.v_hs;
     const float* B = BIAS ? a.bias + sk.first : nullptr;
-    const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
+    const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale, far = kFarTwo / scale2;
 
     // a key's bias in units of the raw score, which starts the score's sum; -inf
     // where the key is left out.  What lies there stays out of every product.
@@ -132,7 +132,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
     const int64_t tok = sq.first + token;
     const int head = hk * a.G + g;
     const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
-    float m = -kInf, l = 0.0f;
+    float m = -kInf, l = 0.0f;      // of raw scores
+    Reference ref = {0.0f, 0.0f};   // of m
     Frag qf[DP / KE], pf[PIPE ? 2 : 1][KT / KE];
     floatx16 o[NT], s[PIPE ? 2 : 1][NK];
 #pragma unroll
@@ -164,16 +165,15 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             for (int d = 0; d < NT; ++d)
                 if (worth<T>(32 * d, a.dv)) o[d] = Op<T>::mma(rd.columns((2 + st) * TB, b, d), pf[PIPE ? st : 0][b], o[d]);
     };
-    // scores to weights, and this lane's part of their sum
-    auto soften = [&](const floatx16* x, Frag* w) -> float {
-        const float use = m == -kInf ? 0.0f : m;
+    // scores to weights, and this lane's part of their sum.  ANY: of every reference
+    auto soften = [&](auto any_c, const floatx16* x, Frag* w) -> float {
         float part[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
             floatx16 p;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                p[e] = exp2_fast(fmaf(x[kt][e], scale2, -use));
+                p[e] = exp2_fast(fmaf(decltype(any_c)::value ? x[kt][e] - ref.raw : x[kt][e], scale2, -ref.two));
                 part[e % 4] += p[e];
             }
 #pragma unroll
@@ -211,12 +211,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             score(std::integral_constant<int, st ^ 1>());   // behind the last tile: not used
             weigh(std::integral_constant<int, st ^ 1>());
         }
-        float sum = soften(s[at], pf[at]);
+        float sum = soften(std::false_type(), s[at], pf[at]);
         // NK DP / KE products for the scores and as many for the values (2 percent
         // faster than in the compiler's order)
         if constexpr (PIPE) mix<NK * DP / 8, 6, 2, 320 / DP, 128 / DP>();
-        // rows whose reference is taken anew; the others keep their bits
-        bool late = m == -kInf;
+        // rows whose reference is taken anew; the others keep their bits.  Rows without one,
+        // or with a far one, go this way at every tile
+        bool late = !(fabsf(m) < far);
         if (__any(late || sum > kMostSum)) {
             late = late || half_max(sum) > kMostSum;
             float mx = s[at][0][0];
@@ -224,16 +225,18 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
             for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[at][kt][e]);
-            mx = half_max(mx) * scale2;
+            mx = half_max(mx);
             const float mnew = late ? fmaxf(m, mx) : m;
-            const float shrink = exp2_fast(m - (mnew == -kInf ? 0.0f : mnew));
+            const Reference to = reference_of(mnew, scale2, far);
+            const float shrink = m == -kInf ? 0.0f : change_of(ref, to, scale2);
             m = mnew;
+            ref = to;
             l *= shrink;
 #pragma unroll
             for (int d = 0; d < NT; ++d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
-            sum = soften(s[at], pf[at]);
+            sum = soften(std::true_type(), s[at], pf[at]);
         }
         l += sum;
         if constexpr (!PIPE) weigh(std::integral_constant<int, st>());
@@ -284,12 +287,15 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 
     const float total = half_sum(l);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const float lse = total == 0.0f ? -kInf : m * kLn2 + logf(total);
     if (r >= rows) return;
     const int64_t cell = ((int64_t)split * a.total_q + tok) * a.hq + head;
     if (h == 0) {
-        if (a.splits > 1) a.part_lse[cell] = lse;
-        else if (a.lse) a.lse[cell] = lse;
+        if (a.splits > 1) {
+            a.part_lse[cell] = m;
+            a.part_lse[a.splits * a.total_q * a.hq + cell] = total;
+        } else if (a.lse) {
+            a.lse[cell] = log_of(ref, a.scale, total);
+        }
     }
     float* part = a.part + cell * a.dv;
     T* orow = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
@@ -307,8 +313,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && NW == 4 && FAST ? 2 : 1)
 
 constexpr int kMostSplits = 256, kJoinWaves = 16;
 
-// Joins the parts of each row:
-//   l = log sum_s exp l_s,  o = sum_s exp(l_s - l) o_s
+// Joins the parts of each row, with weights w_s = sum_s exp(reference_s - reference):
+//   l = reference + log sum_s w_s,  o = sum_s w_s o_s / sum_s w_s
+// (of a part's l alone a large bias would leave no digit of its sum.)
+__device__ __forceinline__ float part_weight(float m, float sum, Reference top, float scale2, float far) {
+    return sum == 0.0f ? 0.0f : sum * change_of(reference_of(m, scale2, far), top, scale2);
+}
+
 // A wave a row, where the parts are few
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_few(AttnArgs a) {
@@ -318,20 +329,22 @@ __global__ __launch_bounds__(256) void attn_join_few(AttnArgs a) {
     // tokens before the first and behind the last sequence stay as they are
     if (tok >= a.total_q || (a.cu_q && (tok < a.cu_q[0] || tok >= a.cu_q[a.n_seq]))) return;
     const int64_t stride = a.total_q * a.hq;
+    const float scale2 = a.scale * kLog2e, far = kFarTwo / scale2;
+    const float *pm = a.part_lse + cell, *ps = pm + a.splits * stride;
     float mx = -kInf, sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, a.part_lse[s * stride + cell]);
-    const float use = mx == -kInf ? 0.0f : mx;
+    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, pm[s * stride]);
+    const Reference top = reference_of(mx, scale2, far);
     const int d0 = min(lane, a.dv - 1), d1 = min(lane + 64, a.dv - 1);
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
-        const float w = exp2_fast((a.part_lse[s * stride + cell] - use) * kLog2e);
+        const float w = part_weight(pm[s * stride], ps[s * stride], top, scale2, far);
         const float* q = a.part + (s * stride + cell) * a.dv;
         sum += w;
         v0 = fmaf(w, q[d0], v0);
         v1 = fmaf(w, q[d1], v1);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (a.lse && lane == 0) a.lse[cell] = sum == 0.0f ? -kInf : use + logf(sum);
+    if (a.lse && lane == 0) a.lse[cell] = log_of(top, a.scale, sum);
     T* out = (T*)a.out + tok * a.o_ts + (int64_t)head * a.o_hs;
     if (lane < a.dv) store_f(out, lane, v0 * inv);
     if (lane + 64 < a.dv) store_f(out, lane + 64, v1 * inv);
@@ -349,18 +362,22 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join(AttnArgs a) {
     // tokens before the first and behind the last sequence stay as they are
     if (a.cu_q && (tok < a.cu_q[0] || tok >= a.cu_q[a.n_seq])) return;
     const int64_t stride = a.total_q * a.hq;
-    float l[P], mx = -kInf, sum = 0.0f;
+    const float scale2 = a.scale * kLog2e, far = kFarTwo / scale2;
+    const float *pm = a.part_lse + cell, *ps = pm + a.splits * stride;
+    float m[P], l[P], mx = -kInf, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        l[i] = lane + 64 * i < a.splits ? a.part_lse[(lane + 64 * i) * stride + cell] : -kInf;
-        mx = fmaxf(mx, l[i]);
+        const bool ok = lane + 64 * i < a.splits;
+        m[i] = ok ? pm[(lane + 64 * i) * stride] : -kInf;
+        l[i] = ok ? ps[(lane + 64 * i) * stride] : 0.0f;
+        mx = fmaxf(mx, m[i]);
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
-    const float use = mx == -kInf ? 0.0f : mx;
+    const Reference top = reference_of(mx, scale2, far);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const float w = exp2_fast((l[i] - use) * kLog2e);
+        const float w = part_weight(m[i], l[i], top, scale2, far);
         if (wave == 0) w_s[lane + 64 * i] = w;
         sum += w;
     }
@@ -380,7 +397,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join(AttnArgs a) {
     red[wave][lane + 64] = v1;
     __syncthreads();
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (a.lse && threadIdx.x == 0) a.lse[cell] = sum == 0.0f ? -kInf : use + logf(sum);
+    if (a.lse && threadIdx.x == 0) a.lse[cell] = log_of(top, a.scale, sum);
     const int d = threadIdx.x;
     if (d >= a.dv) return;
     float v = 0.0f;
