@@ -306,10 +306,13 @@ __device__ __forceinline__ void store4(T* row, int d0, int D, const float* v) {
 constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer: the copy writes zeros
 
 // 16 bytes a lane from base + off (zeros for kNowhere) to LDS at + 16 lane; no
-// registers are written, and completion counts as a vector memory operation.
+// registers are written, and completion counts as a vector memory operation.  The
+// compiler does not see into the block: a scalar register written by a vector
+// instruction (readfirstlane of the descriptor, a spilled one read back) needs five
+// wait states before a memory instruction reads it, which the s_nop gives.
 // off reaches 2^31 bytes: the caller checks that a tile's rows lie that near.
 __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t off, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(at))
                  : "memory", "m0");
@@ -317,7 +320,7 @@ __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t off, uint32_t at) 
 
 // 4 bytes a lane in the same way
 __device__ __forceinline__ void copy4(u32x4 buffer, uint32_t off, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
                  :
                  : "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(at))
                  : "memory", "m0");
