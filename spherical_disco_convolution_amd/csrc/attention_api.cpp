@@ -284,7 +284,13 @@ int64_t bwd_part_bytes(const AttnArgs& a) {
 // how many parts each row of gq, or of gk and gv, came in
 int64_t bwd_count_bytes(const AttnArgs& a) { return ceil_div(std::max(a.total_q * a.hq, a.total_k * a.hkv) * 4, 256) * 256; }
 
+// of each of delta, top and inv
 int64_t bwd_delta_bytes(const AttnArgs& a) { return ceil_div(a.total_q * a.hq * 4, 256) * 256; }
+
+// of the flags of each wave of a tile of 128 rows, as many as a launch may have (tile_slots)
+int64_t bwd_flag_bytes(const AttnArgs& a) {
+    return ceil_div((a.total_q * a.G / 128 + a.n_seq) * a.hkv * 16, 256) * 256;
+}
 
 int need_workspace(const void* ws, int64_t have, int64_t need) {
     if (need > 0 && (ws == nullptr || have < need))
@@ -358,7 +364,7 @@ int64_t disco_attention_bwd_workspace(const disco_attention_desc* desc) {
         a.plan_kv = attn_plan_bwd_kv(a);
         most = std::max(most, bwd_part_bytes(a));
     }
-    return bwd_delta_bytes(a) + bwd_count_bytes(a) + most;
+    return 3 * bwd_delta_bytes(a) + bwd_count_bytes(a) + bwd_flag_bytes(a) + most;
 }
 
 int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -397,7 +403,8 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
     if (nq == 0 && nk == 0) return DISCO_OK;
     a.plan = attn_plan_bwd_q(a);
     a.plan_kv = attn_plan_bwd_kv(a);
-    const int64_t delta = bwd_delta_bytes(a), count = bwd_count_bytes(a), need = delta + count + bwd_part_bytes(a);
+    const int64_t delta = bwd_delta_bytes(a), count = bwd_count_bytes(a), flags = bwd_flag_bytes(a);
+    const int64_t need = 3 * delta + count + flags + bwd_part_bytes(a);
     const int64_t cu = (int64_t)(a.n_seq + 1) * 4;
     if ((rc = need_workspace(workspace, workspace_bytes, need)) != DISCO_OK) return rc;
     const Arg args[] = {{"key_bias", key_bias, a.total_k * 4, 4, false},
@@ -408,8 +415,11 @@ int disco_attention_bwd(const disco_attention_desc* desc, const void* q, const v
     const bool outs[] = {false, false, false, false, true};
     if ((rc = check_tensors(rows, 8, args, 5, outs)) != DISCO_OK) return rc;
     a.delta = static_cast<float*>(workspace);
-    a.count = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + delta);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta + count);
+    a.top = a.delta + delta / 4;
+    a.inv = a.top + delta / 4;
+    a.count = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + 3 * delta);
+    a.flags = a.count + count / 4;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 3 * delta + count + flags);
     return launch_attention_bwd(a, stream);
 }
 

@@ -578,6 +578,13 @@ __device__ __forceinline__ float log_of(Reference r, float scale, float sum) {
     return sum == 0.0f ? -kInf : fmaf(r.raw, scale, r.two * kLn2 + logf(sum));
 }
 
+// Rows whose l has lost what a gradient's weights exp(x - l) need: its rounding alone is
+// 2^-9 of each from here on, and at -1e9 (every key of the row behind such a mask) more
+// than the weights' range.  Gradients take the maximum and the sum of these rows' scores
+// anew.
+constexpr float kFarLse = 65536.0f * kLn2;
+__device__ __forceinline__ bool lse_is_far(float lse) { return fabsf(lse) >= kFarLse && fabsf(lse) < kInf; }
+
 __device__ __forceinline__ float bias2(float b) {   // in units of log 2
     return b < kLowest ? -kInf : b * kLog2e;
 }

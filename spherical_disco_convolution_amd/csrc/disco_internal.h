@@ -249,8 +249,11 @@ struct AttnArgs {
     const float* bias;           // of a key, or NULL
     const int32_t *cu_q, *cu_k;  // boundaries in device memory, or NULL: equal counts
     float* delta;                // [total_q, hq], workspace
+    float *top, *inv;            // the same, of far rows: largest raw score, 1 / sum of weights
     float *part, *part2, *part_lse;   // results of each split, workspace
     int32_t* count;              // gradients: parts of each row, workspace
+    int32_t* flags;              // gradients: waves of gq's tiles that have far rows, workspace
+    int n_flags;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, go_ts, go_hs, gq_ts, gq_hs, gk_ts, gk_hs, gv_ts, gv_hs;
     int64_t total_q, total_k;
     int n_seq, hq, hkv, G, dk, dv, causal, ragged;   // ragged: sequences of lengths of their own

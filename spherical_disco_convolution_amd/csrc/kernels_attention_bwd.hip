@@ -7,6 +7,12 @@
 // of keys (gk, gv): seven products where one kernel would do with five, but no
 // sum is taken in an order that changes from run to run, and no atomics.
 //
+// p comes from l, which is rounded: rows of |l| above 45426 (all keys behind a mask of
+// -1e9, say) have lost it there.  They weigh nothing in the two kernels, and each has a
+// slow one behind it that ends at once where there are no such rows (5 us for both).
+// Inside the kernels these steps cost the others their registers (gq and gk, gv of 6007
+// packed tokens 70 and 151 us instead of 61 and 127).
+//
 // The matrix cores bound both, 6 D and 8 D operations a score; what they wait for are
 // the reads of LDS (each operand of gq, gk and gv is read by columns, at half the
 // width) and the vector units.  65 x 128 points, 8 heads of 64, bf16, in four parts:
@@ -115,11 +121,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST ? 2 : 1) void attn_
         a.delta[tok * a.hq + head] = delta;
         if (a.splits > 1) a.count[tok * a.hq + head] = parts;
     }
+    // rows that see nothing have no gradient: their l is -inf.  Far rows weigh nothing here
+    const float lse = mine ? a.lse_in[tok * a.hq + head] : -kInf;
+    const bool far = lse_is_far(lse);
+    const float lse2 = lse == -kInf || far ? kInf : lse * kLog2e;
+    const int any_far = __any(far) ? 1 : 0;
+    if (split == 0 && lane == 0) a.flags[((int64_t)slot * a.hkv + hk) * NW + wave] = any_far;
     if (!a.gq) return;   // only delta is wanted
     load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, mine, lane);
-    // rows that see nothing have no gradient: their l is -inf
-    const float lse = mine ? a.lse_in[tok * a.hq + head] : -kInf;
-    const float lse2 = lse == -kInf ? kInf : lse * kLog2e;
 
     const float* B = BIAS ? a.bias + sk.first : nullptr;
     const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
@@ -425,8 +434,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
     };
     auto put = [&](int i, int stage, float v) {   // by the first wave
         const bool ok = (t0 + i) * kStep + row < rows;
-        // rows that see nothing weigh nothing
-        if (h == 0) v = !ok || v == -kInf ? -kInf : -v * (PIPE ? per_scale : kLog2e);
+        // rows that see nothing weigh nothing, nor do far ones here
+        if (h == 0) v = !ok || fabsf(v) >= kFarLse ? -kInf : -v * (PIPE ? per_scale : kLog2e);
         else v = ok ? -v : 0.0f;
         add_s[stage][h][0][row] = Addend<T>::pack(v);
     };
@@ -590,6 +599,272 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && FAST && DP <= 64 ? 2 : 1
         }
 }
 
+// A tile of kStep rows ts apart into LDS, past d and in rows of `out` zeros
+template <typename T, int DP, int NW, bool FAST>
+__device__ __forceinline__ void load_tile(const T* p, int64_t ts, int d, uint32_t at, uint64_t out) {
+    typedef Tile<T, DP> L;
+#pragma unroll 1
+    for (int id = threadIdx.x; id < kStep * L::NCH; id += 64 * NW) {
+        const int row = id / L::NCH, c = id % L::NCH;
+        *(lds_u32x4*)(uintptr_t)(at + L::at(row, c)) = load_chunk<T, FAST>(p + row * ts, c * L::EPC, d, !((out >> row) & 1));
+    }
+}
+
+// gq of far rows: the maximum and the sum of their scores over all keys, which the
+// kernel of gk and gv needs too, then their part of gq, a step at a time.
+template <typename T, int DP, int NW, bool FAST, bool FINE>
+__global__ __launch_bounds__(64 * NW) void attn_far_q(AttnArgs a) {
+    typedef Tile<T, DP> L;
+    typedef typename Op<T>::Frag Frag;
+    constexpr int KE = Op<T>::KE, NT = FINE ? 1 : DP / 32, TR = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * TB];
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+    int hk, idx, seq, tile, tiles;
+    if (!head_of(blockIdx.x, a.slots, a.hkv, a.causal, &hk, &idx)) return;
+    int* flags = a.flags + ((int64_t)idx * a.hkv + hk) * NW;
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) any |= flags[i];
+    if (!uniform(any)) return;
+    if (!locate<GROWS>(a.causal, a.cu_q, a.n_seq, (int)a.total_q, a.each_q, a.G, TR, idx, a.slots, &seq, &tile, &tiles)) {
+        if (threadIdx.x < NW) flags[threadIdx.x] = 0;   // no tile: what the workspace held
+        return;
+    }
+    const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q), sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
+    const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
+    int most = lk;
+    if (a.causal) {
+        int t_last, unused;
+        row_of(min(tile * TR + TR, rows) - 1, a.G, &t_last, &unused);
+        most = uniform(min(max(t_last + ahead + 1, 0), lk));
+    }
+    const int all = (most + kStep - 1) / kStep;
+    const int r = tile * TR + wave * 32 + (lane & 31);
+    int token, g;
+    row_of(r, a.G, &token, &g);
+    const int64_t tok = sq.first + token;
+    const int head = hk * a.G + g;
+    const bool far = r < rows && lse_is_far(a.lse_in[tok * a.hq + head]);
+    const float delta = far ? a.delta[tok * a.hq + head] : 0.0f;
+    const int lim = a.causal ? min(max(token + ahead + 1, 0), lk) : lk;
+    const float scale2 = a.scale * kLog2e, per_scale = 1.0f / a.scale;
+    Frag qf[DP / KE], gf[DP / KE];
+    load_columns<T, DP, FAST>(qf, (const T*)a.q + tok * a.q_ts + (int64_t)head * a.q_hs, a.dk, far, lane);
+    load_columns<T, DP, FAST>(gf, (const T*)a.go + tok * a.go_ts + (int64_t)head * a.go_hs, a.dv, far, lane);
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    floatx16 gq[NT], s, dp;
+#pragma unroll
+    for (int d = 0; d < NT; ++d) gq[d] = floatx16{};
+    float top = -kInf, sum = 0.0f, inv = 0.0f;
+    const bool gradient = a.gq != nullptr;
+    // once for the maximum and the sum, then for gq
+    for (int pass = 0; pass < (gradient ? 2 : 1); ++pass) {
+        for (int i = 0; i < all; ++i) {
+            const int k0 = i * kStep, key = k0 + (lane & 31);
+            float b = 0.0f;
+            if (a.bias) b = key < lk ? a.bias[sk.first + key] : 0.0f;
+            b = key >= lk || b < kLowest ? -kInf : b * per_scale;
+            const uint64_t out = __ballot(b == -kInf);
+            const int64_t first = sk.first + k0;
+            all_arrived();   // all have left the step before
+            load_tile<T, DP, NW, FAST>((const T*)a.k + first * a.k_ts + (int64_t)hk * a.k_hs, a.k_ts, a.dk, base, out);
+            load_tile<T, DP, NW, FAST>((const T*)a.v + first * a.v_ts + (int64_t)hk * a.v_hs, a.v_ts, a.dv, base + TB, out);
+            all_arrived();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[e] = __shfl(b, 8 * (e / 4) + 4 * h + e % 4, 64);
+                dp[e] = 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < DP / KE; ++c) s = Op<T>::mma(rd.rows(0, 0, c), qf[c], s);
+            const int room = lim - k0 - 4 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (8 * (e / 4) + e % 4 >= room) s[e] = -kInf;
+            if (pass == 0) {
+                float mx = s[0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
+                mx = fmaxf(top, half_max(mx));
+                if (mx != -kInf) {
+                    sum *= exp2_fast((top - mx) * scale2);
+                    top = mx;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum += exp2_fast((s[e] - top) * scale2);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int c = 0; c < DP / KE; ++c) dp = Op<T>::mma(rd.rows(TB, 0, c), gf[c], dp);
+            floatx16 ds;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ds[e] = far ? exp2_fast((s[e] - top) * scale2) * inv * (dp[e] - delta) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const Frag w = Op<T>::from(ds, k * KE / 2);
+#pragma unroll
+                for (int d = 0; d < NT; ++d) gq[d] = Op<T>::mma(rd.columns(0, k, d), w, gq[d]);
+                if constexpr (FINE) gq[0] = Op<T>::mma(rd.columns(0, k, 0), Op<T>::rest(ds, k * KE / 2, w), gq[0]);
+            }
+        }
+        if (pass) break;
+        sum = half_sum(sum);
+        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (top == -kInf) top = 0.0f;
+        if (h == 0 && far) {
+            a.top[tok * a.hq + head] = top;
+            a.inv[tok * a.hq + head] = inv;
+        }
+    }
+    if (!gradient || !far) return;
+    T* res = (T*)a.gq + tok * a.gq_ts + (int64_t)head * a.gq_hs;
+#pragma unroll
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = gq[d][4 * e4 + e] * a.scale;
+            store4<T, FAST>(res, 32 * d + 8 * e4 + 4 * h, a.dk, v);
+        }
+}
+
+// gk and gv of tiles that far rows see, once more and of all rows, a step at a time:
+//   p = exp2((x - top) scale2 - two) inv
+// with the maximum and the sum that attn_far_q left, or with l for other rows.
+template <typename T, int DP, int NW, bool FAST>
+__global__ __launch_bounds__(64 * NW) void attn_far_kv(AttnArgs a) {
+    typedef Tile<T, DP> L;
+    typedef typename Op<T>::Frag Frag;
+    constexpr int KE = Op<T>::KE, NT = DP / 32, TK = 32 * NW, KB = 32 / KE, TB = kStep * L::RB;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * TB];
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)&smem[0];
+    __shared__ int far_s[2][NW];   // which waves have met far rows
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5, row = lane & 31;
+    int hk, idx, seq, tile, tiles;
+    if (!head_of(blockIdx.x, a.slots, a.hkv, a.causal, &hk, &idx)) return;
+    auto none = [&](int which, bool met) -> bool {   // in the workgroup
+        if (lane == 0) far_s[which][wave] = 0;
+        if (met) far_s[which][wave] = 1;
+        all_arrived();
+        int any = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) any |= far_s[which][i];
+        return !uniform(any);
+    };
+    bool met = false;   // in the whole call, then among the rows that the tile meets
+#pragma unroll 8
+    for (int i = tid; i < a.n_flags; i += 64 * NW) met |= a.flags[i] != 0;
+    if (none(0, met)) return;
+    if (!locate<SHRINKS>(a.causal, a.cu_k, a.n_seq, (int)a.total_k, a.each_k, 1, TK, idx, a.slots, &seq, &tile, &tiles)) return;
+    const Span sq = span_of(a.cu_q, seq, a.each_q, (int)a.total_q), sk = span_of(a.cu_k, seq, a.each_k, (int)a.total_k);
+    const int rows = sq.len * a.G, lk = sk.len, ahead = sk.len - sq.len;
+    const int key = tile * TK + wave * 32 + row;
+    int r_first = 0, r_mine = 0;
+    if (a.causal) {
+        r_first = uniform(min(max(tile * TK - ahead, 0), sq.len) * a.G);
+        r_mine = min(max(key - ahead, 0), sq.len) * a.G;
+    }
+    const int t0 = r_first / kStep, t1 = (rows + kStep - 1) / kStep;
+    auto cell_of = [&](int r) -> int64_t {
+        int t, g;
+        row_of(r, a.G, &t, &g);
+        return (sq.first + t) * a.hq + hk * a.G + g;
+    };
+    met = false;
+    for (int r = r_first + tid; r < rows; r += 64 * NW) met |= lse_is_far(a.lse_in[cell_of(r)]);
+    if (none(1, met)) return;
+    const int64_t tok = sk.first + key;
+    const float scale2 = a.scale * kLog2e;
+    bool seen = key < lk;
+    float b = a.bias && seen ? a.bias[tok] : 0.0f;
+    seen = seen && !(b < kLowest);
+    b *= 1.0f / a.scale;
+    Frag kf[DP / KE], vf[DP / KE];
+    load_columns<T, DP, FAST>(kf, (const T*)a.k + tok * a.k_ts + (int64_t)hk * a.k_hs, a.dk, seen, lane);
+    load_columns<T, DP, FAST>(vf, (const T*)a.v + tok * a.v_ts + (int64_t)hk * a.v_hs, a.dv, seen, lane);
+    Reader<T, DP> rd;
+    rd.init(base, lane);
+    floatx16 gk[NT], gv[NT], s, dp;
+#pragma unroll
+    for (int d = 0; d < NT; ++d) gk[d] = gv[d] = floatx16{};
+    for (int i = t0; i < t1; ++i) {
+        const int r0 = i * kStep;
+        all_arrived();   // all have left the step before
+#pragma unroll 1
+        for (int n = tid; n < kStep * L::NCH; n += 64 * NW) {
+            const int at = n / L::NCH, c = n % L::NCH;
+            int t, g;
+            row_of(r0 + at, a.G, &t, &g);
+            const bool ok = r0 + at < rows;
+            const int64_t q = sq.first + t, head = hk * a.G + g;
+            *(lds_u32x4*)(uintptr_t)(base + L::at(at, c)) =
+                load_chunk<T, FAST>((const T*)a.q + q * a.q_ts + head * a.q_hs, c * L::EPC, a.dk, ok);
+            *(lds_u32x4*)(uintptr_t)(base + TB + L::at(at, c)) =
+                load_chunk<T, FAST>((const T*)a.go + q * a.go_ts + head * a.go_hs, c * L::EPC, a.dv, ok);
+        }
+        float top = 0.0f, two = kInf, inv = 0.0f, delta = 0.0f;   // of row r0 + row
+        if (r0 + row < rows) {
+            const int64_t cell = cell_of(r0 + row);
+            const float lse = a.lse_in[cell];
+            delta = a.delta[cell];
+            inv = 1.0f;
+            if (lse_is_far(lse)) {
+                top = a.top[cell];
+                inv = a.inv[cell];
+                two = 0.0f;
+            } else if (lse != -kInf) {
+                two = lse * kLog2e;
+            }
+        }
+        all_arrived();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = b, dp[e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < DP / KE; ++c) {
+            s = Op<T>::mma(rd.rows(0, 0, c), kf[c], s);
+            dp = Op<T>::mma(rd.rows(TB, 0, c), vf[c], dp);
+        }
+        floatx16 w, ds;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int at = 8 * (e / 4) + 4 * h + e % 4;   // of the step's rows
+            const float x = fmaf(s[e] - __shfl(top, at, 64), scale2, -__shfl(two, at, 64));
+            const float f = __shfl(inv, at, 64), di = __shfl(delta, at, 64);
+            w[e] = seen && r0 + at >= r_mine ? exp2_fast(x) * f : 0.0f;
+            ds[e] = w[e] * (dp[e] - di);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const Frag pf = Op<T>::from(w, k * KE / 2), sf = Op<T>::from(ds, k * KE / 2);
+#pragma unroll
+            for (int d = 0; d < NT; ++d) {
+                gv[d] = Op<T>::mma(rd.columns(TB, k, d), pf, gv[d]);
+                gk[d] = Op<T>::mma(rd.columns(0, k, d), sf, gk[d]);
+            }
+        }
+    }
+    if (key >= lk) return;
+    T* ok = (T*)a.gk + tok * a.gk_ts + (int64_t)hk * a.gk_hs;
+    T* ov = (T*)a.gv + tok * a.gv_ts + (int64_t)hk * a.gv_hs;
+#pragma unroll
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+            const int d0 = 32 * d + 8 * e4 + 4 * h;
+            float x[4], y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = gk[d][4 * e4 + e] * a.scale;
+                y[e] = gv[d][4 * e4 + e];
+            }
+            store4<T, FAST>(ok, d0, a.dk, x);
+            store4<T, FAST>(ov, d0, a.dv, y);
+        }
+}
+
 // Sums of the parts of one or two tensors [tokens, heads, d], V elements a thread.
 // What came in one part is there already; tokens of no sequence stay as they are.
 struct Parts {
@@ -638,6 +913,7 @@ int bwd_go(AttnArgs a, hipStream_t st) {
     a.slots = (int)tile_slots(a.cu_q != nullptr, a.total_q, a.n_seq, a.G, 32 * NW);
     a.splits = a.gq ? a.plan.splits : 1;
     a.chunk = a.plan.chunk;
+    a.n_flags = a.slots * a.hkv * NW;
     if (a.total_q > 0) {   // delta, which gk and gv need too
         KernelTimer timer("attn_bwd_q", st);
         const unsigned grid = (unsigned)grid_size((int64_t)a.slots * a.splits, a.hkv);
@@ -652,6 +928,13 @@ int bwd_go(AttnArgs a, hipStream_t st) {
     }
     if (a.splits > 1)
         sum_parts<T>({a.part, a.gq, a.gq_ts, a.gq_hs, a.dk}, {}, a.count, a.total_q, a.hq, a.splits, a.cu_q, a.n_seq, st);
+    if (a.total_q > 0 && a.total_k > 0) {
+        KernelTimer timer("attn_far_q", st);
+        const unsigned grid = (unsigned)grid_size(a.slots, a.hkv);
+        constexpr bool TWO = sizeof(T) == 2;
+        if (DP == 32 || (TWO && a.dk <= 32)) attn_far_q<T, DP, NW, FAST, TWO><<<grid, 64 * NW, 0, st>>>(a);
+        else if constexpr (DP > 32) attn_far_q<T, DP, NW, FAST, false><<<grid, 64 * NW, 0, st>>>(a);
+    }
     if (a.gk && a.total_k > 0) {
         a.slots = (int)tile_slots(a.cu_k != nullptr, a.total_k, a.n_seq, 1, 32 * NW);
         a.splits = a.plan_kv.splits;
@@ -665,6 +948,10 @@ int bwd_go(AttnArgs a, hipStream_t st) {
         if (a.splits > 1)
             sum_parts<T>({a.part, a.gk, a.gk_ts, a.gk_hs, a.dk}, {a.part2, a.gv, a.gv_ts, a.gv_hs, a.dv}, a.count, a.total_k,
                          a.hkv, a.splits, a.cu_k, a.n_seq, st);
+        if (a.total_q > 0) {
+            KernelTimer timer("attn_far_kv", st);
+            attn_far_kv<T, DP, NW, FAST><<<(unsigned)grid_size(a.slots, a.hkv), 64 * NW, 0, st>>>(a);
+        }
     }
     return attn_launched("attention_bwd");
 }
