@@ -382,11 +382,15 @@ int disco_muon_step(const void* grad, int grad_dtype, const float* momentum, flo
  *    j <= i + Lk - Lq (the last query sees all keys).
  *  - key_bias [total_k] float32 or NULL, at most 1e30; -inf, or anything below
  *    -1e30, leaves a key out, whatever k and v hold there.  It is a constant: no
- *    gradient.
+ *    gradient.  Any other value is a summand, so a query all of whose keys carry a
+ *    mask of -1e9 gets a mean of their values, as large as float32 scores let it be
+ *    told apart; beside ordinary keys such a mask weighs nothing.
  *  - a query that sees no key gets o = 0, lse = -inf and gradients of zero.
  *  - values of v are at most 1e25: sums may be that much larger for a while.
  *  - what a causal query does not see has to be finite all the same: a NaN or an
- *    infinity there may reach queries up to 63 keys earlier.
+ *    infinity in k or v may reach o and gq of queries that see up to 190 keys less,
+ *    one in q, go or o of a query gk and gv of keys up to 158 behind its last one.  In
+ *    a query that sees no key it may reach gk and gv of its sequence.
  * float32 tensors are computed in float32; for bfloat16 ones products are of
  * bfloat16 operands summed in float32, with the weights exp(x - max) and the
  * gradients of x rounded to bfloat16 (the bf16 bar).  Sums run in a fixed order:

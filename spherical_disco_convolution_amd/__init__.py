@@ -914,11 +914,14 @@ def attention_fwd(q, k, v, key_bias=None, cu_q=None, cu_k=None, causal: bool = F
 
     q [T, Hq, dk], k [S, Hkv, dk], v [S, Hkv, dv] hold the tokens of all
     sequences one after another, with int32 boundaries cu_q, cu_k (sequences + 1,
-    on the device; None: one sequence), or are a batch [B, T, Hq, dk] etc. of
-    equal lengths.  Hkv divides Hq: query head h reads head h // (Hq / Hkv).  Token
+    on the device; both None: one sequence, one of them None: equal shares), or are
+    a batch [B, T, Hq, dk] etc. of equal lengths whose sequences lie one after
+    another.  Hkv divides Hq: query head h reads head h // (Hq / Hkv).  Token
     and head strides are free (columns of a projection's output).  key_bias
-    (float32, a value a key: the logarithms of quadrature weights): -inf, or
-    anything below -1e30, leaves a key out.  causal: query i sees keys up to
+    (float32, a value a key of at most 1e30: the logarithms of quadrature weights):
+    -inf, or anything below -1e30, leaves a key out.  Values of v are at most 1e25.
+    What a causal query does not see has to be finite all the same: a NaN or an
+    infinity there may reach queries that see up to 190 keys less.  causal: query i sees keys up to
     i + Lk - Lq of its sequence.  A query that sees none gets zeros and
     lse = -inf.  scale None: dk ** -0.5.
 
@@ -946,7 +949,9 @@ def attention_bwd(q, k, v, o, lse, go, key_bias=None, cu_q=None, cu_k=None, caus
     """Gradients (gq, gk, gv) of sum(go * attention_fwd(q, k, v)[0]), in q's dtype;
     entries not asked for are None.  o and lse are the forward's.  gq, gk and gv may
     be given, as columns of one buffer too; gk and gv are summed over the heads of
-    their group."""
+    their group.  The forward's limits hold; a NaN or an infinity in q, go or o of a
+    causal query may reach gk and gv of up to 158 keys behind its last one, and in a
+    query that sees no key those of its sequence."""
     if stream is not None:
         return _on(stream, attention_bwd, q, k, v, o, lse, go, key_bias, cu_q, cu_k, causal, scale, need_gq, need_gkv,
                    gq, gk, gv)
