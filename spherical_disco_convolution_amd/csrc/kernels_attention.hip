@@ -3,8 +3,8 @@
 // 4 D operations a score against 2 / rows of a key's bytes: the matrix cores bound it
 // where there are more than a few hundred rows, with an exponential, two products
 // and a sum a score on the vector units beside them.  129 x 256 points, 8 heads of 64,
-// bf16: 2.9 ms, 0.76 PFLOP/s; the matrix cores take 39 percent of the cycles, the
-// vector units 60, and power holds the clock at 1.8 to 2.0 GHz.  Packed causal series
+// bf16: 2.9 to 3.0 ms, 0.75 PFLOP/s; the matrix cores take 39 percent of the cycles and
+// the vector units 57, mostly in turn, at a clock of 1.8 to 2.0 GHz.  Packed causal series
 // of 12001 tokens, 12 heads of 128 over 4: 0.13 ms, 0.82 PFLOP/s.  Few rows over many
 // keys are bound by the reading of the keys (8 points over 33024 keys, 34 MB: 20 us).
 //
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void attn_join_few(AttnArgs a) {
 }
 
 // A workgroup a row, its waves share the parts (8 points over 33024 keys, 128 rows
-// of 128 parts: 10 us, a wave a row 120)
+// of 97 parts: 6 us; of 128 parts 10, with a wave a row 120)
 template <typename T>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join(AttnArgs a) {
     constexpr int P = kMostSplits / 64;

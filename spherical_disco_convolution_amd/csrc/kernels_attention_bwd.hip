@@ -16,11 +16,13 @@
 // The matrix cores bound both, 6 D and 8 D operations a score; what they wait for are
 // the reads of LDS (each operand of gq, gk and gv is read by columns, at half the
 // width) and the vector units.  65 x 128 points, 8 heads of 64, bf16, in four parts:
-// gq 258 us (0.82 PFLOP/s of its three products), gk and gv 345 us (0.82 of four).
-// Packed causal series of 6007 tokens, 12 heads of 128 over 4: 62 and 127 us; there
+// gq 260 us (0.82 PFLOP/s of its three products), gk and gv 347 us (0.82 of four).
+// Packed causal series of 6007 tokens, 12 heads of 128 over 4: 62 and 129 us; there
 // gk and gv of 128 leave one workgroup a compute unit (two workgroups by spilling: 435
-// us), and nothing covers the 10 us in which one begins and ends.  float32, 2 x 33 x 64 points, 4 heads of 32: 80 and 108 us at 0.09 PFLOP/s of
-// the 0.15 that float32 products reach.
+// us), and nothing covers the 10 us in which one begins and ends.  float32, 2 x 33 x 64
+// points, 4 heads of 32: 86 and 115 us, 0.08 PFLOP/s of the 0.15 that float32 products
+// reach.  (Events around each launch under load; a card that has just begun took 277 and
+// 377, 62 and 136, 91 and 121.)
 //
 // The order of instructions is the compiler's: laid out as in the forward kernel,
 // gk and gv took 468 us instead of 457 and 190 instead of 147, gq 342 instead of 324.
